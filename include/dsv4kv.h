@@ -76,7 +76,11 @@ enum {
     DSV4_FP8_SLOT_BYTES = 584,
     DSV4_BF16_SLOT_BYTES = 1024,
     DSV4_INDEXER_DIM = 128,        /* indexer K width: one E4M3 row with one fp32 scale */
-    DSV4_INDEXER_SLOT_BYTES = 132  /* 128 E4M3 codes + 4 scale bytes per slot */
+    DSV4_INDEXER_SLOT_BYTES = 132, /* 128 E4M3 codes + 4 scale bytes per slot */
+    DSV4_FP4_GROUP = 32,           /* elements per UE8M0 exponent of the 4-bit cache */
+    DSV4_FP4_DATA_BYTES = 352,     /* 448 E2M1 codes (224 bytes) + 64 bf16 */
+    DSV4_FP4_SCALE_BYTES = 16,     /* 14 UE8M0 bytes + 2 zero pad bytes */
+    DSV4_FP4_SLOT_BYTES = 368
 };
 
 /* bits OR-ed into *device_error */
@@ -371,6 +375,126 @@ int dsv4_debug_bounds_flags(int reset);
 
 /* Static string naming a dsv4_status value ("unknown status" otherwise). */
 const char *dsv4_status_string(int status);
+
+/*
+ * ---- The 4-bit cache: insert, reader, attention, attention weights, eviction
+ *
+ * kv_cache (device) uint8, num_blocks * block_size * 368 bytes, 16-byte aligned.  Block
+ * b occupies [b*bs*368, (b+1)*bs*368); inside it, slot offset o has
+ *   data  at b*bs*368 + o*352         : 224 bytes of E2M1 codes of dims 0..447, then
+ *                                       dims 448..511 as 64 little-endian bf16,
+ *   scale at b*bs*368 + bs*352 + o*16 : UE8M0 bytes e_0..e_13 of the fourteen 32-dim
+ *                                       groups, then 0 0.
+ * The codes of dims 8i..8i+7 are the little-endian 32-bit word i; its nibbles 0..7
+ * (lowest first) are dims 8i + (0, 2, 4, 6, 1, 3, 5, 7).  A code is a sign bit over an
+ * E2M1 magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6; the value is code * 2^(e_g - 127).
+ * e_g = s_g + 127 with s_g the smallest integer such that max|v| over the group
+ * <= 6 * 2^s_g (at least -127), code = E2M1_rn(v * 2^-s_g) (ties to the even code), v
+ * as for the other stores: both follow the exact v = x * w * r, not an fp32 rounding
+ * of it.  A group whose maximum is not finite has e_g = 255 and reads back as NaN.
+ */
+
+/* num_blocks * block_size * 368; 0 for a size below 1 */
+size_t dsv4_fp4_cache_bytes(int64_t num_blocks, int32_t block_size);
+
+/*
+ * The fused step with the 4-bit store: q normalised and rotated in place, one KV row per
+ * token normalised with the weight, rotated and inserted.  Arguments as for
+ * dsv4_qnorm_rope_kv_quant_insert; num_heads may be 0 (KV rows only; q may be NULL).
+ */
+int dsv4_qnorm_rope_kv_fp4_insert(void *q, const void *kv, const void *kv_norm_weight,
+                                  const int64_t *positions, const float *cos_sin_cache,
+                                  int64_t max_position, const int64_t *slot_mapping,
+                                  uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
+                                  int64_t num_tokens, int32_t num_heads, float eps,
+                                  int32_t *device_error, void *stream);
+
+/* As dsv4_dequant_gather, for the 4-bit cache. */
+int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
+                            const int64_t *slots, int64_t num_rows, void *out,
+                            int32_t *device_error, void *stream);
+
+/*
+ * Attention over the 4-bit cache: every head of a new token attends to its request's
+ * latent rows, which are keys and values in one.
+ *
+ *  q            (device) bf16 [batch, q_len, num_heads, 512], contiguous, 16-byte aligned.
+ *  block_table  (device) int32: row b (table_stride elements after row b - 1) lists the
+ *               table_width blocks of request b in order.  Key i of request b is slot
+ *               i % block_size of block block_table[b][i / block_size].  Entries that no
+ *               length reaches are not read.  table_width * block_size < 2^31.
+ *  seq_lens     (device) int32 [batch]: keys of each request, its q_len new tokens included;
+ *               0 is an idle request.  Token j sees keys [max(0, n - window), n) with
+ *               n = seq_lens[b] - q_len + 1 + j (all of [0, n) for window 0).
+ *  scale        of the scores, finite and > 0:  s = scale * (q . k).
+ *  sinks        (device, nullable) fp32 [num_heads]: a score that takes part in the softmax
+ *               of its head and has no value.
+ *  out          (device) bf16 [batch, q_len, num_heads, 512], 16-byte aligned; may not overlap q.
+ *               A token that sees no key gives zeros.
+ *  lse          (device, nullable) fp32 [batch, q_len, num_heads]: log of the sum of exp over
+ *               the visible scores and the sink (-infinity where there is neither).
+ *  workspace    (device) at least dsv4_fp4_attention_workspace_bytes() bytes, 16-byte aligned.
+ *               Its contents need no preparation and mean nothing after the call; two calls
+ *               that may run at the same time need two.
+ *
+ * Scores and sums are fp32; the probabilities are rounded to bf16 for the product with
+ * the rows.  A key past every token's length, or outside every window, is not read, whatever its slot holds;
+ * the keys that some tokens of a request see and others do not must be finite.
+ * A block outside [0, num_blocks) sets DSV4_DEVERR_SLOT_RANGE and its keys take no part;
+ * a length past table_width * block_size sets it too and counts as that many.
+ */
+size_t dsv4_fp4_attention_workspace_bytes(void);
+int dsv4_fp4_attention(const void *q, const uint8_t *kv_cache, int64_t num_blocks,
+                       int32_t block_size, const int32_t *block_table, int64_t table_stride,
+                       int32_t table_width, const int32_t *seq_lens, int32_t batch,
+                       int32_t q_len, int32_t num_heads, float scale, int32_t window,
+                       const float *sinks, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *device_error, void *stream);
+
+/*
+ * The attention each key got: weights[b][i] += sum over the tokens and heads of request b
+ * that see key i of exp(scale * (q . k_i) - lse).  Arguments as above, lse as
+ * dsv4_fp4_attention left it (-infinity: the token adds nothing); weights (device) fp32,
+ * row b weights_stride elements after row b - 1.  Row b has at least seq_lens[b] elements:
+ * weights_width of them are the caller's, and a longer request sets
+ * DSV4_DEVERR_SLOT_RANGE and adds to those only.  Each sum is taken in a fixed order:
+ * the same call gives the same bits.
+ */
+int dsv4_fp4_attention_weights(const void *q, const uint8_t *kv_cache, int64_t num_blocks,
+                               int32_t block_size, const int32_t *block_table,
+                               int64_t table_stride, int32_t table_width,
+                               const int32_t *seq_lens, int32_t batch, int32_t q_len,
+                               int32_t num_heads, float scale, int32_t window, const float *lse,
+                               float *weights, int64_t weights_stride, int32_t weights_width,
+                               int32_t *device_error, void *stream);
+
+/*
+ * Eviction: request b keeps min(seq_lens[b], budget) of its rows, which are copied in
+ * their order to the blocks of new_block_table.  Kept are the last `recent` rows and, of
+ * the others, those of the highest weights, a tie going to the lower index (NaN counts as
+ * -infinity, -0 as 0).
+ *
+ *  weights          (device) fp32, row stride weights_stride, weights_width elements a row
+ *                   that may be read (a longer request is cut to that, with
+ *                   DSV4_DEVERR_SLOT_RANGE).
+ *  budget, recent   budget >= 1, 0 <= recent <= budget.
+ *  new_block_table  (device) int32 [batch], rows of new_table_width entries; new_table_width *
+ *                   block_size >= budget.  No block of it may be one that a request of the
+ *                   call still reads (block_table) or that it names twice.
+ *  kept             (device) int32 [batch, budget]: the rows' old indices, rising; -1 after them.
+ *  new_seq_lens     (device) int32 [batch].  May be seq_lens itself.
+ *  new_weights      (device) fp32 [batch, budget]: the kept rows' weights; 0 after them.  May not
+ *                   overlap weights.
+ * A block outside [0, num_blocks) in either table sets DSV4_DEVERR_SLOT_RANGE and the row
+ * is not copied.  Scale bytes, codes and rope dims are moved as they are.
+ */
+int dsv4_fp4_evict(uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
+                   const int32_t *block_table, int64_t table_stride, int32_t table_width,
+                   const int32_t *seq_lens, int32_t batch, const float *weights,
+                   int64_t weights_stride, int32_t weights_width, int32_t budget,
+                   int32_t recent, const int32_t *new_block_table, int64_t new_table_stride,
+                   int32_t new_table_width, int32_t *kept, int32_t *new_seq_lens,
+                   float *new_weights, int32_t *device_error, void *stream);
 
 #ifdef __cplusplus
 }

@@ -25,20 +25,22 @@ LIB_PATH = os.path.join(_HERE, "libdsv4kv.so")
 CHECKED_LIB_PATH = os.path.join(_HERE, "libdsv4kv_checked.so")
 _SOURCES = ["qnorm_rope_kv_insert.cu", "dequant_gather.cu",
             "gemma_rmsnorm_mxfp8.cu", "indexer_k.cu", "kv_rows.cu", "qnorm_rope_kv_insert_half.cu",
-            "wait_check.cu",
-            "api.cpp"]
+            "wait_check.cu", "fp4_gather.cu", "fp4_attention.cu", "fp4_evict.cu",
+            "api.cpp", "fp4_api.cpp"]
 _HEADERS = [os.path.join(_INCLUDE, "dsv4kv.h")] + [
     os.path.join(_CSRC, h)
     for h in ("launch.h", "ops.h", "fastdiv.h", "convert.cuh", "launch_status.h", "rowmath.cuh",
-              "halfrow.cuh", "bulkcopy.cuh", "bounds.cuh", "bounds_range.h")]
+              "halfrow.cuh", "bulkcopy.cuh", "bounds.cuh", "bounds_range.h", "fp4.cuh",
+              "hostcheck.h")]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # status codes and constants (mirrors include/dsv4kv.h)
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_VALUE, ERR_CUDA = range(6)
 DEVERR_SLOT_RANGE, DEVERR_POS_RANGE, DEVERR_TIMEOUT, DEVERR_BOUNDS = 1, 2, 4, 8
 STORE_FP8, STORE_BF16 = 0, 1
+_STORE_FP4 = 2  # of the checks below; the 4-bit store has its own entry point
 VARIANT_AUTO, VARIANT_SMALL, VARIANT_STREAM, VARIANT_HALF = 0, 1, 2, 4
-FP8_SLOT_BYTES, BF16_SLOT_BYTES = 584, 1024
+FP8_SLOT_BYTES, BF16_SLOT_BYTES, FP4_SLOT_BYTES = 584, 1024, 368
 
 EXPORTS = ("dsv4_qnorm_rope_kv_quant_insert", "dsv4_qnorm_rope_kv_bf16_insert",
            "dsv4_qnorm_rope_kv_insert_variant", "dsv4_qnorm_rope_kv_rope_quant_insert",
@@ -46,7 +48,10 @@ EXPORTS = ("dsv4_qnorm_rope_kv_quant_insert", "dsv4_qnorm_rope_kv_bf16_insert",
            "dsv4_add_gemma_rmsnorm_mxfp8", "dsv4_mxfp8_scale_bytes", "dsv4_launch_plan",
            "dsv4_fp8_cache_bytes", "dsv4_bf16_cache_bytes", "dsv4_indexer_k_quant_insert",
            "dsv4_indexer_k_gather", "dsv4_indexer_cache_bytes", "dsv4_check_bounded_wait",
-           "dsv4_debug_bounds_flags", "dsv4_status_string")
+           "dsv4_debug_bounds_flags", "dsv4_status_string", "dsv4_fp4_cache_bytes",
+           "dsv4_qnorm_rope_kv_fp4_insert", "dsv4_fp4_dequant_gather",
+           "dsv4_fp4_attention_workspace_bytes", "dsv4_fp4_attention",
+           "dsv4_fp4_attention_weights", "dsv4_fp4_evict")
 
 
 class Dsv4Error(RuntimeError):
@@ -179,6 +184,23 @@ def _load(path: str):
     L.dsv4_indexer_k_gather.restype = c_int
     L.dsv4_indexer_cache_bytes.argtypes = [i64, i32]
     L.dsv4_indexer_cache_bytes.restype = ctypes.c_size_t
+    L.dsv4_fp4_cache_bytes.argtypes = [i64, i32]
+    L.dsv4_fp4_cache_bytes.restype = ctypes.c_size_t
+    L.dsv4_qnorm_rope_kv_fp4_insert.argtypes = common
+    L.dsv4_qnorm_rope_kv_fp4_insert.restype = c_int
+    L.dsv4_fp4_dequant_gather.argtypes = [vp, i64, i32, vp, i64, vp, vp, vp]
+    L.dsv4_fp4_dequant_gather.restype = c_int
+    L.dsv4_fp4_attention_workspace_bytes.argtypes = []
+    L.dsv4_fp4_attention_workspace_bytes.restype = ctypes.c_size_t
+    batch = [vp, i64, i32, vp, i64, i32, vp, i32]  # cache, its sizes, the table, lens, batch
+    L.dsv4_fp4_attention.argtypes = ([vp] + batch + [i32, i32, f32, i32, vp, vp, vp, vp,
+                                                     ctypes.c_size_t, vp, vp])
+    L.dsv4_fp4_attention.restype = c_int
+    L.dsv4_fp4_attention_weights.argtypes = ([vp] + batch + [i32, i32, f32, i32, vp, vp, i64, i32,
+                                                             vp, vp])
+    L.dsv4_fp4_attention_weights.restype = c_int
+    L.dsv4_fp4_evict.argtypes = batch + [vp, i64, i32, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp]
+    L.dsv4_fp4_evict.restype = c_int
     L.dsv4_check_bounded_wait.argtypes = [i64, vp, vp]
     L.dsv4_check_bounded_wait.restype = c_int
     L.dsv4_debug_bounds_flags.argtypes = [c_int]
@@ -280,7 +302,8 @@ def _check_step(store_mode, q, kv, w, positions, cos_sin_cache, slot_mapping, kv
     _check("cos_sin_cache", cos_sin_cache, "f32")
     if not isinstance(cos_sin_cache, int) and cos_sin_cache.numel() % 64:
         raise ValueError("cos_sin_cache must hold rows of 64 fp32 (32 cos, 32 sin)")
-    need = (fp8_cache_bytes if store_mode == STORE_FP8 else bf16_cache_bytes)(num_blocks, block_size)
+    need = {STORE_FP8: fp8_cache_bytes, _STORE_FP4: fp4_cache_bytes}.get(
+        store_mode, bf16_cache_bytes)(num_blocks, block_size)
     _check("kv_cache", kv_cache, "bytes", min_bytes=need)
     _check("device_error", device_error, "i32")
     _on_cuda(q=q, kv=kv, kv_norm_weight=w, positions=positions, cos_sin_cache=cos_sin_cache,
@@ -476,3 +499,160 @@ def add_gemma_rmsnorm_mxfp8(x, residual, gamma, eps: float, residual_out, codes,
                                             _stream_handle(stream))
     if st != OK:
         raise Dsv4Error(st, "dsv4_add_gemma_rmsnorm_mxfp8")
+
+
+# ---- the 4-bit cache
+
+
+def fp4_cache_bytes(num_blocks: int, block_size: int) -> int:
+    return int(lib().dsv4_fp4_cache_bytes(num_blocks, block_size))
+
+
+def qnorm_rope_kv_fp4_insert(q, kv, kv_norm_weight, positions, cos_sin_cache, slot_mapping,
+                             kv_cache, num_blocks, block_size, eps, device_error=None,
+                             stream=None) -> None:
+    """dsv4_qnorm_rope_kv_fp4_insert: 4-bit (448 E2M1 + 14 UE8M0 + 64 bf16) cache rows;
+    q may be None (KV rows only)."""
+    T, H, max_pos = _shape_args(q, kv, positions, cos_sin_cache)
+    _check_step(_STORE_FP4, q, kv, kv_norm_weight, positions, cos_sin_cache, slot_mapping, kv_cache,
+                num_blocks, block_size, device_error, T, H)
+    st = lib().dsv4_qnorm_rope_kv_fp4_insert(
+        _ptr(q), _ptr(kv), _ptr(kv_norm_weight), _ptr(positions), _ptr(cos_sin_cache), max_pos,
+        _ptr(slot_mapping), _ptr(kv_cache), num_blocks, block_size, T, H, eps,
+        _ptr(device_error), _stream_handle(stream))
+    if st != OK:
+        raise Dsv4Error(st, "dsv4_qnorm_rope_kv_fp4_insert")
+
+
+def fp4_dequant_gather(kv_cache, num_blocks: int, block_size: int, slots, out, device_error=None,
+                       stream=None) -> None:
+    """dsv4_fp4_dequant_gather: out (bf16 [n, 512]) = 4-bit cache rows at ``slots`` read back."""
+    n = int(slots.shape[0])
+    _check("slots", slots, "i64", n)
+    _check("kv_cache", kv_cache, "bytes", min_bytes=fp4_cache_bytes(num_blocks, block_size))
+    _check("out", out, "bf16", n * 512)
+    _check("device_error", device_error, "i32")
+    _on_cuda(kv_cache=kv_cache, slots=slots, out=out, device_error=device_error)
+    st = lib().dsv4_fp4_dequant_gather(_ptr(kv_cache), num_blocks, block_size, _ptr(slots), n,
+                                       _ptr(out), _ptr(device_error), _stream_handle(stream))
+    if st != OK:
+        raise Dsv4Error(st, "dsv4_fp4_dequant_gather")
+
+
+def _check_rows(name: str, t, kind: str, batch: int) -> tuple:
+    """(stride, width) in elements of a 2-d tensor with one row per request, whose rows are
+    contiguous and may be further apart than they are long."""
+    if t.dtype not in _kinds()[kind]:
+        raise TypeError(f"{name}: expected {kind} data, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != batch:
+        raise ValueError(f"{name}: expected one row for each of {batch} requests, got "
+                         f"{tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1 or batch > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: its rows must be contiguous and apart")
+    return (t.stride(0) if batch > 1 else t.shape[1]), t.shape[1]
+
+
+def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens):
+    if q.dim() != 4 or q.shape[3] != 512:
+        raise ValueError(f"q: expected [batch, q_len, heads, 512], got {tuple(q.shape)}")
+    B, Q, H, _ = q.shape
+    _check("q", q, "bf16")
+    _check("kv_cache", kv_cache, "bytes", min_bytes=fp4_cache_bytes(num_blocks, block_size))
+    _check("seq_lens", seq_lens, "i32", B)
+    return B, Q, H, _check_rows("block_table", block_table, "i32", B)
+
+
+def fp4_attention_workspace_bytes() -> int:
+    return int(lib().dsv4_fp4_attention_workspace_bytes())
+
+
+def fp4_attention(q, kv_cache, num_blocks: int, block_size: int, block_table, seq_lens,
+                  scale: float, out, lse=None, sinks=None, window: int = 0, workspace=None,
+                  device_error=None, stream=None) -> None:
+    """dsv4_fp4_attention: out (bf16 [B, Q, H, 512]) = attention of q (bf16, same shape)
+    over the 4-bit rows of each request, key and value in one.
+
+    block_table: int32 [B, W] (rows may be strided); seq_lens: int32 [B], the Q new tokens
+    included; lse: optional fp32 [B, Q, H]; sinks: optional fp32 [H]; window: keys a token
+    sees, 0 for all.  workspace: uint8 of fp4_attention_workspace_bytes(); None takes one
+    from torch's allocator for the call, on ``stream``, which is then torch's current one,
+    or a torch stream."""
+    B, Q, H, (stride, width) = _check_attention(q, kv_cache, num_blocks, block_size, block_table,
+                                                seq_lens)
+    _check("out", out, "bf16", q.numel())
+    _check("lse", lse, "f32", B * Q * H)
+    _check("sinks", sinks, "f32", H)
+    _check("device_error", device_error, "i32")
+    if workspace is None:
+        workspace = _workspace(fp4_attention_workspace_bytes(), q.device, stream)
+    else:
+        _check("workspace", workspace, "bytes")
+    _on_cuda(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
+             sinks=sinks, workspace=workspace, device_error=device_error)
+    st = lib().dsv4_fp4_attention(
+        q.data_ptr(), _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
+        _ptr(seq_lens), B, Q, H, scale, window, _ptr(sinks), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(device_error), _stream_handle(stream))
+    if st != OK:
+        raise Dsv4Error(st, "dsv4_fp4_attention")
+
+
+def _workspace(nbytes: int, device, stream):
+    import torch
+    if isinstance(stream, int):
+        raise ValueError("workspace: pass one for a stream given by its handle")
+    if device.type != "cuda":
+        raise ValueError("q must be a CUDA tensor (there is no CPU path)")
+    with torch.cuda.stream(stream):  # the allocator gives it out again on this stream only
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def fp4_attention_weights(q, kv_cache, num_blocks: int, block_size: int, block_table, seq_lens,
+                          scale: float, lse, weights, window: int = 0, device_error=None,
+                          stream=None) -> None:
+    """dsv4_fp4_attention_weights: weights (fp32 [B, n], rows may be strided) += the attention
+    that each key of each request got from q, with the lse that fp4_attention returned."""
+    B, Q, H, (stride, width) = _check_attention(q, kv_cache, num_blocks, block_size, block_table,
+                                                seq_lens)
+    _check("lse", lse, "f32", B * Q * H)
+    w_stride, w_width = _check_rows("weights", weights, "f32", B)
+    _check("device_error", device_error, "i32")
+    _on_cuda(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, lse=lse,
+             weights=weights, device_error=device_error)
+    st = lib().dsv4_fp4_attention_weights(
+        q.data_ptr(), _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
+        _ptr(seq_lens), B, Q, H, scale, window, _ptr(lse), weights.data_ptr(), w_stride, w_width,
+        _ptr(device_error), _stream_handle(stream))
+    if st != OK:
+        raise Dsv4Error(st, "dsv4_fp4_attention_weights")
+
+
+def fp4_evict(kv_cache, num_blocks: int, block_size: int, block_table, seq_lens, weights,
+              budget: int, recent: int, new_block_table, kept, new_seq_lens, new_weights,
+              device_error=None, stream=None) -> None:
+    """dsv4_fp4_evict: each request keeps its last ``recent`` rows and the others of the
+    highest weights (fp32 [B, n]), ``budget`` in all, moved in order to new_block_table
+    (int32 [B, W]; blocks of the same cache that no request of the call reads).
+
+    kept: int32 [B, budget], the rows' old indices, -1 after them; new_seq_lens: int32 [B]
+    (may be seq_lens); new_weights: fp32 [B, budget]."""
+    B = int(seq_lens.shape[0])
+    _check("kv_cache", kv_cache, "bytes", min_bytes=fp4_cache_bytes(num_blocks, block_size))
+    _check("seq_lens", seq_lens, "i32", B)
+    stride, width = _check_rows("block_table", block_table, "i32", B)
+    w_stride, w_width = _check_rows("weights", weights, "f32", B)
+    n_stride, n_width = _check_rows("new_block_table", new_block_table, "i32", B)
+    _check("kept", kept, "i32", B * budget)
+    _check("new_seq_lens", new_seq_lens, "i32", B)
+    _check("new_weights", new_weights, "f32", B * budget)
+    _check("device_error", device_error, "i32")
+    _on_cuda(kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, weights=weights,
+             new_block_table=new_block_table, kept=kept, new_seq_lens=new_seq_lens,
+             new_weights=new_weights, device_error=device_error)
+    st = lib().dsv4_fp4_evict(
+        _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
+        _ptr(seq_lens), B, weights.data_ptr(), w_stride, w_width, budget, recent,
+        new_block_table.data_ptr(), n_stride, n_width, _ptr(kept), _ptr(new_seq_lens),
+        _ptr(new_weights), _ptr(device_error), _stream_handle(stream))
+    if st != OK:
+        raise Dsv4Error(st, "dsv4_fp4_evict")

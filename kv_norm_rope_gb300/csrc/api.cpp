@@ -9,30 +9,20 @@
 #include <cstdint>
 
 #include "dsv4kv.h"
+#include "hostcheck.h"
 #include "launch.h"
 #include "ops.h"
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-// Caches hold at most 2^32 slots (more than any one GPU can hold at 132 bytes
-// per slot), so the kernels divide 32-bit slot numbers by the block size.
-constexpr int64_t kMaxSlots = int64_t(1) << 32;
-
-bool too_many_slots(int64_t num_blocks, int32_t block_size)
-{
-    return num_blocks > kMaxSlots / block_size;
-}
+using dsv4::aligned;
+using dsv4::too_many_slots;
 
 // Per-device cache of (SM count, CTAs of the streaming kernel per SM) for the
-// two store modes: immutable properties, filled on first use.
+// three stores: immutable properties, filled on first use.
 constexpr int kMaxDevices = 64;
 std::atomic<int32_t> g_sms[kMaxDevices];
-std::atomic<int32_t> g_ctas[kMaxDevices][2];
+std::atomic<int32_t> g_ctas[kMaxDevices][3];
 
 int device_shape(int store_mode, int32_t *sms, int32_t *ctas)
 {
@@ -100,6 +90,7 @@ int resident_ctas(int kind, int64_t *resident)
 // flags of insert()
 constexpr int kKvNorm = 1;  // normalise the KV row with the weight
 constexpr int kNoQ = 2;     // num_heads may be 0 (KV rows only)
+constexpr int kFp4 = 4;     // the 4-bit store, whose layouts are SMALL and STREAM
 
 int insert(int store_mode, int variant, int flags, void *q, const void *kv, const void *w,
            const int64_t *positions, const float *cos_sin, int64_t max_position,
@@ -107,7 +98,8 @@ int insert(int store_mode, int variant, int flags, void *q, const void *kv, cons
            int64_t num_tokens, int32_t num_heads, float eps, int32_t *device_error, void *stream)
 {
     const bool kv_norm = (flags & kKvNorm) != 0;
-    if (store_mode != DSV4_STORE_FP8 && store_mode != DSV4_STORE_BF16)
+    const bool fp4 = (flags & kFp4) != 0;
+    if (!fp4 && store_mode != DSV4_STORE_FP8 && store_mode != DSV4_STORE_BF16)
         return DSV4_ERR_VALUE;
     if (variant != DSV4_VARIANT_AUTO && variant != DSV4_VARIANT_SMALL &&
         variant != DSV4_VARIANT_STREAM && variant != DSV4_VARIANT_HALF)
@@ -148,6 +140,13 @@ int insert(int store_mode, int variant, int flags, void *q, const void *kv, cons
     st = dsv4_launch_plan(num_tokens, num_heads, sms, ctas, variant, &plan);
     if (st != DSV4_OK)
         return st;
+    if (fp4 && plan.variant != DSV4_VARIANT_SMALL) {
+        // the whole-warp stream for any number of heads; with none, a warp per KV row
+        st = dsv4_launch_plan(num_tokens, num_heads > 0 ? num_heads : 1, sms, ctas,
+                              DSV4_VARIANT_STREAM, &plan);
+        if (st != DSV4_OK)
+            return st;
+    }
     if (variant == DSV4_VARIANT_AUTO && plan.variant == DSV4_VARIANT_HALF) {
         // size the grid with the half-warp kernel's own occupancy
         int64_t resident = 0;
@@ -177,7 +176,7 @@ int insert(int store_mode, int variant, int flags, void *q, const void *kv, cons
     a.kv_norm = kv_norm;
     if (plan.variant == DSV4_VARIANT_HALF)
         return dsv4::launch_half(store_mode, a, plan.ctas, static_cast<cudaStream_t>(stream));
-    if (num_heads == 0 && plan.variant == DSV4_VARIANT_STREAM) {
+    if (num_heads == 0 && plan.variant == DSV4_VARIANT_STREAM && !fp4) {
         // KV rows only: the quarter-warp-per-row kernel
         int64_t resident = 0;
         if (resident_ctas(kOccKvRows, &resident) != DSV4_OK)
@@ -312,6 +311,18 @@ int dsv4_kv_norm_rope_insert(int store_mode, const void *kv, const void *kv_norm
     return insert(store_mode, DSV4_VARIANT_AUTO, kKvNorm | kNoQ, nullptr, kv, kv_norm_weight,
                   positions, cos_sin_cache, max_position, slot_mapping, kv_cache, num_blocks,
                   block_size, num_tokens, 0, eps, device_error, stream);
+}
+
+int dsv4_qnorm_rope_kv_fp4_insert(void *q, const void *kv, const void *kv_norm_weight,
+                                  const int64_t *positions, const float *cos_sin_cache,
+                                  int64_t max_position, const int64_t *slot_mapping,
+                                  uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
+                                  int64_t num_tokens, int32_t num_heads, float eps,
+                                  int32_t *device_error, void *stream)
+{
+    return insert(dsv4::kStoreFp4, DSV4_VARIANT_AUTO, kKvNorm | kNoQ | kFp4, q, kv, kv_norm_weight,
+                  positions, cos_sin_cache, max_position, slot_mapping, kv_cache, num_blocks,
+                  block_size, num_tokens, num_heads, eps, device_error, stream);
 }
 
 int dsv4_insert_ex(int store_mode, int variant, int kv_norm, void *q, const void *kv,
@@ -463,7 +474,9 @@ int dsv4_debug_bounds_flags(int reset)
 {
     int (*const readers[])(int) = {dsv4::bounds_flag_fused, dsv4::bounds_flag_half,
                                    dsv4::bounds_flag_kv_rows, dsv4::bounds_flag_gather,
-                                   dsv4::bounds_flag_indexer, dsv4::bounds_flag_mxfp8};
+                                   dsv4::bounds_flag_indexer, dsv4::bounds_flag_mxfp8,
+                                   dsv4::bounds_flag_fp4_gather, dsv4::bounds_flag_fp4_attention,
+                                   dsv4::bounds_flag_fp4_evict};
     int flags = 0;
     for (auto read : readers) {
         const int v = read(reset);

@@ -17,6 +17,10 @@ constexpr int kStreamRowsPerWarp = 3;
 constexpr int kStreamThreads = 256;
 constexpr int kSmallThreads = 64;
 
+// The 4-bit store, beside DSV4_STORE_FP8 and DSV4_STORE_BF16: it has an entry
+// point of its own and is no store mode of the others.
+constexpr int kStoreFp4 = 2;
+
 struct LaunchArgs {
     uint16_t *q;
     const uint16_t *kv;

@@ -47,6 +47,61 @@ int launch_indexer_gather(const uint8_t *cache, int64_t num_blocks, int32_t bloc
 // cycles (clamped to the kernels' own limit), then flags DSV4_DEVERR_TIMEOUT.
 int launch_wait_check(int64_t max_cycles, int32_t *err, cudaStream_t stream);
 
+// The 4-bit cache (fp4.cuh: its rows).  What the operators over it have in common:
+// B requests, their pages by a block table, and Q new tokens each.
+struct Fp4Batch {
+    const uint8_t *cache;
+    int64_t num_blocks;
+    int32_t block_size;
+    const int32_t *table;   // [batch] rows of `width` entries, `table_stride` apart
+    int64_t table_stride;
+    int32_t width;
+    const int32_t *lens;    // [batch], the new tokens included
+    int32_t batch;
+    int32_t *err;
+};
+
+struct Fp4AttentionArgs {
+    Fp4Batch b;
+    const uint16_t *q;      // [batch, q_len, heads, 512]
+    int32_t q_len;
+    int32_t heads;
+    float scale;
+    int32_t window;         // 0: none
+    const float *sinks;     // [heads] or null
+    uint16_t *out;
+    float *lse;             // [batch, q_len, heads]: written by the attention, read by the weights
+    float *weights;         // [batch] rows, weights_stride apart
+    int64_t weights_stride;
+    int32_t weights_width;
+};
+
+struct Fp4EvictArgs {
+    Fp4Batch b;             // b.cache is written too
+    const float *weights;
+    int64_t weights_stride;
+    int32_t weights_width;
+    int32_t budget;
+    int32_t recent;
+    const int32_t *new_table;
+    int64_t new_table_stride;
+    int32_t new_width;
+    int32_t *kept;          // [batch, budget]
+    int32_t *new_lens;      // [batch]
+    float *new_weights;     // [batch, budget]
+};
+
+// fp4_gather.cu; the grid is capped at max_ctas
+int fp4_gather_ctas_per_sm(int *ctas_per_sm);
+int launch_fp4_gather(const uint8_t *cache, int64_t num_blocks, int32_t block_size,
+                      const int64_t *slots, int64_t rows, uint16_t *out, int32_t *err,
+                      int64_t max_ctas, cudaStream_t stream);
+// fp4_attention.cu
+int launch_fp4_attention(const Fp4AttentionArgs &a, cudaStream_t stream);
+int launch_fp4_weights(const Fp4AttentionArgs &a, cudaStream_t stream);
+// fp4_evict.cu
+int launch_fp4_evict(const Fp4EvictArgs &a, cudaStream_t stream);
+
 // The checked build's record of skipped accesses, one reader per kernel file
 // (DSV4_BOUNDS_FLAG_READER of bounds.cuh); -1 in the release build.
 int bounds_flag_fused(int reset);
@@ -55,5 +110,8 @@ int bounds_flag_kv_rows(int reset);
 int bounds_flag_gather(int reset);
 int bounds_flag_indexer(int reset);
 int bounds_flag_mxfp8(int reset);
+int bounds_flag_fp4_gather(int reset);
+int bounds_flag_fp4_attention(int reset);
+int bounds_flag_fp4_evict(int reset);
 
 }  // namespace dsv4

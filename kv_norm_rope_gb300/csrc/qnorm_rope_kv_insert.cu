@@ -167,7 +167,10 @@ int stream_ctas_per_sm(int store_mode, int *ctas_per_sm)
     // the normalising FP8 kernel is the largest; every streaming kernel shares
     // its launch bounds, so its occupancy is the one used for all of them
     cudaError_t e;
-    if (store_mode == DSV4_STORE_BF16)
+    if (store_mode == kStoreFp4)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            ctas_per_sm, Kernels<kStoreFp4, true>::stream, kStreamThreads, 0);
+    else if (store_mode == DSV4_STORE_BF16)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
             ctas_per_sm, Kernels<DSV4_STORE_BF16, true>::stream, kStreamThreads, 0);
     else
@@ -196,6 +199,8 @@ int launch(int store_mode, const dsv4_plan &plan, const LaunchArgs &a, cudaStrea
     p.slot_div = fastdiv_magic(static_cast<uint32_t>(a.block_size));
     const dim3 grid(unsigned(plan.ctas)), block(unsigned(plan.threads));
     const bool small = plan.variant == DSV4_VARIANT_SMALL;
+    if (store_mode == kStoreFp4)  // always with the norm
+        return launch_one<kStoreFp4, true>(small, grid, block, stream, p);
     if (store_mode == DSV4_STORE_BF16)
         return a.kv_norm ? launch_one<DSV4_STORE_BF16, true>(small, grid, block, stream, p)
                          : launch_one<DSV4_STORE_BF16, false>(small, grid, block, stream, p);

@@ -71,7 +71,9 @@ template <int kStore>
 __device__ __forceinline__ Span cache_span(const KParams &p)
 {
     return Span{p.cache, uint64_t(p.num_slots) *
-                             (kStore == DSV4_STORE_BF16 ? DSV4_BF16_SLOT_BYTES : DSV4_FP8_SLOT_BYTES)};
+                             (kStore == DSV4_STORE_BF16 ? DSV4_BF16_SLOT_BYTES
+                              : kStore == kStoreFp4     ? DSV4_FP4_SLOT_BYTES
+                                                        : DSV4_FP8_SLOT_BYTES)};
 }
 
 
@@ -678,6 +680,198 @@ __device__ __forceinline__ float kv_products(const KParams &p, int lane, int64_t
     return r;
 }
 
+// ---- The 4-bit store (fp4.cuh: the row's format)
+//
+// Per group of 32 dims: s = the least integer with amax <= 6 * 2^s, codes
+// E2M1_rn(v * 2^-s).  4-bit codes are so coarse that a value on the other side
+// of a border moves by a whole step, so both decisions follow the exact v =
+// x * w * r.  fp32 settles nearly all: its v is within 2^-20 of the exact one,
+// so an element whose code is the same at v * (1 - 2^-18) and v * (1 + 2^-18),
+// and an amax outside kNearBand of 1.5 * 2^k, are decided.  A row with any other
+// element (about 4 in 1000 on Gaussian data), or with a group too small for
+// fp32 to hold to full precision, is evaluated again in fp64 by its warp.
+
+constexpr uint32_t kMant1p5 = 0x400000u;  // mantissa field of 1.5 (6 = 1.5 * 2^2)
+constexpr float kFp4Tiny = 0x1p-100f;     // a group amax below this goes to fp64
+
+// max over the 4 lanes that hold one 32-dim group
+template <typename F>
+__device__ __forceinline__ F group4_max(F v)
+{
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1) {
+        const F o = __shfl_xor_sync(kFull, v, m);
+        v = v > o ? v : o;
+    }
+    return v;
+}
+
+// The exponent of a group from its fp32 amax.  `exact` marks one that fp64 has
+// to decide; amax = NaN or infinity gives s = 128 (byte 255).
+struct Fp4Scale {
+    int s;
+    bool exact;
+};
+
+__device__ __forceinline__ Fp4Scale fp4_scale(float amax)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    const int ef = int(bits >> 23);
+    const uint32_t m = bits & 0x7fffffu;
+    Fp4Scale g;
+    g.s = !(amax < INFINITY) ? 128 : max(ef - 129 + (m > kMant1p5 ? 1 : 0), -127);
+    g.exact = (amax < kFp4Tiny && amax > 0.0f) ||
+              ((m - (kMant1p5 - kNearBand)) <= 2u * kNearBand && amax < INFINITY);
+    return g;
+}
+
+// 8 values -> 8 E2M1 codes (round to nearest even, saturating at 6) in the
+// nibble order 0 2 4 6 1 3 5 7.  The cvt instruction packs its first source
+// into the upper nibble.
+__device__ __forceinline__ uint32_t e2m1x8_rn(const float *u)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %3, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %7, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %4, %2;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %6;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3]), "f"(u[4]), "f"(u[5]), "f"(u[6]), "f"(u[7]));
+    return r;
+}
+
+// the codes of 8 elements v = xw * r of a group with exponent s; `exact` is set
+// when some code depends on the fp32 error of v
+__device__ __forceinline__ uint32_t fp4_codes(const float *xw, float r, int s, bool &exact)
+{
+    if (s == 128)
+        return 0u;
+    const float k = pow2_neg(s);
+    float u[8], lo[8], hi[8];
+    scale8(xw, r, u);
+    scale8(u, k, u);
+    scale8(u, 1.0f - 0x1p-18f, lo);
+    scale8(u, 1.0f + 0x1p-18f, hi);
+    const uint32_t c = e2m1x8_rn(lo);
+    exact = exact || c != e2m1x8_rn(hi);
+    return c;
+}
+
+// The row of token t in fp64: the lane's two code words and its groups' s.
+struct Fp4Lane {
+    uint32_t c0, c1;
+    int s0, s1;
+};
+
+__device__ __forceinline__ int fp4_scale_fp64(double amax)
+{
+    if (!(amax < 1.0e300))
+        return 128;
+    if (amax == 0.0)
+        return -127;
+    const int ef = int((__double2hiint(amax) >> 20) & 0x7ff) - 1023;
+    const double top = __hiloint2double(int(uint32_t(1023 + ef) << 20) | 0x00080000, 0);  // 1.5 * 2^ef
+    return min(max(ef - 2 + (amax > top ? 1 : 0), -127), 128);
+}
+
+__device__ __forceinline__ uint32_t e2m1_fp64(double u)
+{
+    const double a = fabs(u);
+    const uint32_t c = (a > 0.25 ? 1u : 0u) + (a >= 0.75 ? 1u : 0u) + (a > 1.25 ? 1u : 0u) +
+                       (a >= 1.75 ? 1u : 0u) + (a > 2.5 ? 1u : 0u) + (a >= 3.5 ? 1u : 0u) +
+                       (a > 5.0 ? 1u : 0u);
+    return c | (u < 0.0 ? 8u : 0u);
+}
+
+__device__ __noinline__ Fp4Lane fp4_row_fp64(KvSrc p, int lane, int64_t t)
+{
+    const uint4 *row = reinterpret_cast<const uint4 *>(p.kv + t * kHead);
+    const uint4 *wv = reinterpret_cast<const uint4 *>(p.w);
+    const uint4 xa = ldg16_in(row + lane, kv_span(p), p.err);
+    const uint4 xb = ldg16_in(row + 32 + lane, kv_span(p), p.err);
+    const uint4 wa = ldg16_in(wv + lane, w_span(p), p.err);
+    const uint4 wb = ldg16_in(wv + 32 + lane, w_span(p), p.err);
+    double ss = 0.0;
+#pragma unroll 1
+    for (int k = 0; k < 16; ++k) {
+        const double x = double(bf16_at(k < 8 ? xa : xb, k & 7));
+        ss = __fma_rn(x, x, ss);
+    }
+    const double r = 1.0 / sqrt(warp_sum(ss) / 512.0 + double(p.eps));
+    Fp4Lane out = {0u, 0u, 0, 0};
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        const uint4 x = h ? xb : xa, w = h ? wb : wa;
+        double amax = 0.0;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const double a = fabs(__dmul_rn(__dmul_rn(double(bf16_at(x, k)), r), double(bf16_at(w, k))));
+            amax = a > amax || a != a ? a : amax;
+        }
+        if (!(amax < 1.0e300))
+            amax = 1.0e308;  // a NaN loses every comparison of the maximum below
+        const int s = fp4_scale_fp64(group4_max(amax));
+        const double k2 = __hiloint2double(int(uint32_t(1023 - s) << 20), 0);
+        uint32_t c = 0u;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const double v = __dmul_rn(__dmul_rn(double(bf16_at(x, k)), r), double(bf16_at(w, k)));
+            c |= (s == 128 ? 0u : e2m1_fp64(__dmul_rn(v, k2))) << (4 * ((k >> 1) + 4 * (k & 1)));
+        }
+        if (h == 0) {
+            out.c0 = c;
+            out.s0 = s;
+        } else {
+            out.c1 = c;
+            out.s1 = s;
+        }
+    }
+    return out;
+}
+
+// The 4-bit store of a row in the whole-warp layout: xw, tmax, r as kv_products
+// leaves them (rope lanes hold their final dims in xw[8..15]).
+__device__ __forceinline__ void kv_row_fp4(const KParams &p, int lane, int64_t t, int64_t slot,
+                                           const float *xw, const float *tmax, float r)
+{
+    const bool rope_lane = lane >= 24;
+    const Fp4Scale g0 = fp4_scale(__fmul_rn(group4_max(tmax[0]), r));
+    const Fp4Scale g1 = fp4_scale(__fmul_rn(group4_max(tmax[1]), r));
+    bool exact = g0.exact || (!rope_lane && g1.exact);
+    Fp4Lane l;
+    l.s0 = g0.s;
+    l.s1 = g1.s;
+    l.c0 = fp4_codes(xw, r, g0.s, exact);
+    l.c1 = rope_lane ? 0u : fp4_codes(xw + 8, r, g1.s, exact);
+    if (__any_sync(kFull, exact))
+        l = fp4_row_fp64(kv_src(p), lane, t);
+
+    const uint32_t blk = fastdiv(static_cast<uint32_t>(slot), p.slot_div);
+    const uint32_t off = static_cast<uint32_t>(slot) - blk * static_cast<uint32_t>(p.block_size);
+    uint8_t *base = p.cache + uint64_t(blk) * static_cast<uint32_t>(p.block_size) * DSV4_FP4_SLOT_BYTES;
+    uint8_t *data = base + uint64_t(off) * DSV4_FP4_DATA_BYTES;
+    const Span cspan = cache_span<kStoreFp4>(p);
+    st_stream4_in(data + 4 * lane, l.c0, cspan, p.err);
+    if (!rope_lane)
+        st_stream4_in(data + 128 + 4 * lane, l.c1, cspan, p.err);
+    else
+        st_stream16_in(data + DSV4_NOPE_DIM / 2 + 16 * (lane - 24), bf16x8_rn(xw + 8), cspan, p.err);
+    // scale byte g (group g < 8: lanes 4g..4g+3 of half 0; g >= 8: lanes 4(g-8).. of half 1)
+    const uint32_t shift = 8u * (uint32_t(lane >> 2) & 3u);
+    const bool lead = (lane & 3) == 0, low = lane < 16;
+    const uint32_t b0 = uint32_t(l.s0 + 127) << shift, b1 = uint32_t(l.s1 + 127) << shift;
+    const uint32_t w0 = __reduce_or_sync(kFull, lead && low ? b0 : 0u);
+    const uint32_t w1 = __reduce_or_sync(kFull, lead && !low ? b0 : 0u);
+    const uint32_t w2 = __reduce_or_sync(kFull, lead && low ? b1 : 0u);
+    const uint32_t w3 = __reduce_or_sync(kFull, lead && !low && !rope_lane ? b1 : 0u);
+    if (lane == 0)
+        st_stream16_in(base + uint64_t(p.block_size) * DSV4_FP4_DATA_BYTES +
+                           uint64_t(off) * DSV4_FP4_SCALE_BYTES,
+                       make_uint4(w0, w1, w2, w3), cspan, p.err);
+}
+
 // The KV row of token t: v = x*w*r (or v = x when the row arrives normalised),
 // rotate, store into the paged cache.  xa, xb: the row's two 16-byte vectors of
 // this lane (from global memory or a shared-memory stage); pos, slot: the
@@ -714,6 +908,11 @@ __device__ __forceinline__ void kv_row(const KParams &p, int lane, int64_t t, in
         st_stream16_in(row + 8 * lane, bf16x8_scaled(xw, r), cache_span<kStore>(p), p.err);
         st_stream16_in(row + 256 + 8 * lane, rope_lane ? bf16x8_rn(xw + 8) : bf16x8_scaled(xw + 8, r),
                        cache_span<kStore>(p), p.err);
+        return;
+    }
+
+    if constexpr (kStore == kStoreFp4) {
+        kv_row_fp4(p, lane, t, slot, xw, tmax, r);
         return;
     }
 
