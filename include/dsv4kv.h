@@ -419,10 +419,11 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
  * latent rows, which are keys and values in one.
  *
  *  q            (device) bf16 [batch, q_len, num_heads, 512], contiguous, 16-byte aligned.
+ *               q_len <= 2^24.
  *  block_table  (device) int32: row b (table_stride elements after row b - 1) lists the
  *               table_width blocks of request b in order.  Key i of request b is slot
  *               i % block_size of block block_table[b][i / block_size].  Entries that no
- *               length reaches are not read.  table_width * block_size < 2^31.
+ *               length reaches are not read.  table_width * block_size <= 2^30.
  *  seq_lens     (device) int32 [batch]: keys of each request, its q_len new tokens included;
  *               0 is an idle request.  Token j sees keys [max(0, n - window), n) with
  *               n = seq_lens[b] - q_len + 1 + j (all of [0, n) for window 0).

@@ -25,13 +25,14 @@ LIB_PATH = os.path.join(_HERE, "libdsv4kv.so")
 CHECKED_LIB_PATH = os.path.join(_HERE, "libdsv4kv_checked.so")
 _SOURCES = ["qnorm_rope_kv_insert.cu", "dequant_gather.cu",
             "gemma_rmsnorm_mxfp8.cu", "indexer_k.cu", "kv_rows.cu", "qnorm_rope_kv_insert_half.cu",
-            "wait_check.cu", "fp4_gather.cu", "fp4_attention.cu", "fp4_evict.cu",
+            "wait_check.cu", "fp4_gather.cu", "fp4_attention.cu", "fp4_weights.cu",
+            "fp4_evict.cu",
             "api.cpp", "fp4_api.cpp"]
 _HEADERS = [os.path.join(_INCLUDE, "dsv4kv.h")] + [
     os.path.join(_CSRC, h)
     for h in ("launch.h", "ops.h", "fastdiv.h", "convert.cuh", "launch_status.h", "rowmath.cuh",
               "halfrow.cuh", "bulkcopy.cuh", "bounds.cuh", "bounds_range.h", "fp4.cuh",
-              "hostcheck.h")]
+              "fp4_tiles.cuh", "tcgen05.cuh", "hostcheck.h")]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # status codes and constants (mirrors include/dsv4kv.h)

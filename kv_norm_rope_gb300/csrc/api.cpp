@@ -476,6 +476,7 @@ int dsv4_debug_bounds_flags(int reset)
                                    dsv4::bounds_flag_kv_rows, dsv4::bounds_flag_gather,
                                    dsv4::bounds_flag_indexer, dsv4::bounds_flag_mxfp8,
                                    dsv4::bounds_flag_fp4_gather, dsv4::bounds_flag_fp4_attention,
+                                   dsv4::bounds_flag_fp4_weights,
                                    dsv4::bounds_flag_fp4_evict};
     int flags = 0;
     for (auto read : readers) {

@@ -41,6 +41,10 @@ int resident_readers(int64_t *resident)
     return DSV4_OK;
 }
 
+// keys of a request that a table can name: key indices, less a window and a
+// number of tokens, then stay in 32 bits
+constexpr int64_t kMaxKeys = int64_t(1) << 30;
+
 // sizes of what every operator over requests takes; pointers come after the
 // early return for an empty batch
 int check_sizes(int64_t num_blocks, int32_t block_size, int64_t table_stride, int32_t table_width,
@@ -50,19 +54,23 @@ int check_sizes(int64_t num_blocks, int32_t block_size, int64_t table_stride, in
         table_stride < table_width)
         return DSV4_ERR_SHAPE;
     if (too_many_slots(num_blocks, block_size) || num_blocks > INT32_MAX ||
-        int64_t(table_width) * block_size > INT32_MAX || table_stride > INT64_MAX / 4096 / 65536 ||
+        int64_t(table_width) * block_size > kMaxKeys || table_stride > INT64_MAX / 4096 / 65536 ||
         batch > 65535)
         return DSV4_ERR_SHAPE;
     return DSV4_OK;
 }
 
-int check_attention(int32_t q_len, int32_t num_heads, int32_t batch, float scale, int32_t window)
+int check_attention(int32_t q_len, int32_t num_heads, int32_t batch, float scale, int32_t window,
+                    int64_t most_keys)
 {
-    if (q_len < 1 || num_heads < 1 || window < 0)
+    if (q_len < 1 || q_len > (1 << 24) || num_heads < 1 || window < 0)
         return DSV4_ERR_SHAPE;
     if (int64_t(q_len) * num_heads > INT32_MAX ||
         int64_t(q_len) * num_heads * batch > INT64_MAX / 4096 ||
         (batch > 0 && int64_t(q_len) * num_heads > INT32_MAX / batch))
+        return DSV4_ERR_SHAPE;
+    // tiles of 64 rows and 128 keys are counted in 32 bits
+    if (((int64_t(q_len) * num_heads + 63) / 64) * batch > INT32_MAX / ((most_keys + 127) / 128))
         return DSV4_ERR_SHAPE;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DSV4_ERR_VALUE;
@@ -105,7 +113,7 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
 
 size_t dsv4_fp4_attention_workspace_bytes(void)
 {
-    return 16;
+    return dsv4::fp4_attention_workspace();
 }
 
 int dsv4_fp4_attention(const void *q, const uint8_t *kv_cache, int64_t num_blocks,
@@ -117,7 +125,8 @@ int dsv4_fp4_attention(const void *q, const uint8_t *kv_cache, int64_t num_block
 {
     int st = check_sizes(num_blocks, block_size, table_stride, table_width, batch);
     if (st == DSV4_OK)
-        st = check_attention(q_len, num_heads, batch, scale, window);
+        st = check_attention(q_len, num_heads, batch, scale, window,
+                             int64_t(table_width) * block_size);
     if (st != DSV4_OK)
         return st;
     if (workspace_bytes < dsv4_fp4_attention_workspace_bytes())
@@ -137,11 +146,11 @@ int dsv4_fp4_attention(const void *q, const uint8_t *kv_cache, int64_t num_block
     a.q_len = q_len;
     a.heads = num_heads;
     a.scale = scale;
-    a.window = window;
+    a.window = window < int64_t(table_width) * block_size ? window : 0;
     a.sinks = sinks;
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
-    return dsv4::launch_fp4_attention(a, static_cast<cudaStream_t>(stream));
+    return dsv4::launch_fp4_attention(a, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int dsv4_fp4_attention_weights(const void *q, const uint8_t *kv_cache, int64_t num_blocks,
@@ -154,7 +163,8 @@ int dsv4_fp4_attention_weights(const void *q, const uint8_t *kv_cache, int64_t n
 {
     int st = check_sizes(num_blocks, block_size, table_stride, table_width, batch);
     if (st == DSV4_OK)
-        st = check_attention(q_len, num_heads, batch, scale, window);
+        st = check_attention(q_len, num_heads, batch, scale, window,
+                             int64_t(table_width) * block_size);
     if (st != DSV4_OK)
         return st;
     if (weights_width < 0 || weights_stride < weights_width ||
@@ -175,7 +185,7 @@ int dsv4_fp4_attention_weights(const void *q, const uint8_t *kv_cache, int64_t n
     a.q_len = q_len;
     a.heads = num_heads;
     a.scale = scale;
-    a.window = window;
+    a.window = window < int64_t(table_width) * block_size ? window : 0;
     a.lse = const_cast<float *>(lse);
     a.weights = weights;
     a.weights_stride = weights_stride;

@@ -1,189 +1,656 @@
-// Attention over the 4-bit cache and the attention weights per key.
+// Attention over the 4-bit cache: out = softmax(scale * q k^T [sink]) k, where a
+// request's latent rows are keys and values in one.
+//
+// Per (query row, key) it takes 2 * 512 multiplications for the score and as many
+// for the value, and a key's 368 bytes are read once for all rows of its request:
+// at 64 heads 356 operations a byte, which puts the matrix units and the memory
+// near one another.  So the rows are multiplied with tcgen05 in bf16 (a 4-bit code
+// times its scale is a bf16 exactly) and converted on the way:
+//
+//  * A CTA holds 64 query rows (the heads of one or more tokens of a request) and
+//    walks its run of tiles of 128 keys (fp4_tiles.cuh).  Scores are computed
+//    transposed, S^T[key, row] = K q^T, and so are the outputs, O^T[dim, row] =
+//    K^T P^T: keys and dims take the 128 lanes of the tensor memory, so any number
+//    of rows up to 64 costs in proportion (N = 16, 32, 48, 64), and O^T of 512
+//    dims (4 x 64 columns) fits beside S^T.
+//  * One converted tile serves both products: K-major as the left operand of the
+//    first, read across (MN-major) as that of the second.  It is held in 8 chunks
+//    of 64 dims, each filled, and freed by the second product, on its own, so
+//    the next tile is converted under the products of this one.
+//  * Warps 8..15 convert, one thread of warp 16 issues the products, warps 0..7
+//    do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
+//    32 (w / 4)..; a thread has one key and 32 rows.
+//  * The softmax needs no maximum per tile.  Each row has a reference m, the
+//    largest score of the first tile it saw; p = 2^(x - m) is taken against that,
+//    and only when some x exceeds m by more than kSlack is m moved and everything
+//    rescaled (fp32 and bf16 have the same range, so a p of 2^kSlack loses
+//    nothing).  Sums stay per thread, in fp32, until the segment ends.
+//  * A run that covers all tiles of a request writes the output; else the
+//    unnormalised O, m and the sum go to the workspace and a second kernel joins
+//    them in the order of the runs.
+//
+// P is rounded to bf16 as an operand (relative 2^-9 each, unbiased); the sum that
+// divides it is of the unrounded p.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "fp4.cuh"
+#include <atomic>
+
+#include "fp4_tiles.cuh"
 #include "launch_status.h"
 #include "ops.h"
 
 namespace dsv4 {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
+constexpr int kRows = 64;            // query rows of a CTA
+constexpr int kThreads = 17 * 32;
+constexpr int kMaxCtas = 256;        // of a launch: what the workspace is for
+constexpr float kSlack = 16.0f;
+constexpr float kUnset = -1e30f;     // m of a row that has seen no key
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-struct AParams {
-    Fp4AttentionArgs a;
-    uint64_t block_div;
+// Workspace: two partial results a CTA, O [64, 512] then m [64] and sum [64].
+constexpr size_t kPartialFloats = size_t(kRows) * DSV4_HEAD_DIM + 2 * kRows;
+
+struct WParams {
+    AParams p;
+    float *partials;
+    int runs;  // CTAs
 };
 
-__device__ __forceinline__ Span cache_span(const Fp4Batch &b)
+__device__ __forceinline__ float *partial_at(const WParams &w, int x, int slot)
 {
-    return Span{b.cache, uint64_t(b.num_blocks) * uint32_t(b.block_size) * kFp4Slot};
+    return w.partials + (size_t(x) * 2 + slot) * kPartialFloats;
+}
+__device__ __forceinline__ Span partial_span(const WParams &w)
+{
+    return Span{w.partials, uint64_t(w.runs) * 2u * kPartialFloats * 4u};
 }
 
-__device__ __forceinline__ uint64_t rows_of(const Fp4AttentionArgs &a)
+// Shared memory (from a 1024-byte boundary).
+constexpr uint32_t kKeys = 0;                                  // 8 chunks of a converted tile
+constexpr uint32_t kQuery = kKeys + kChunks * kChunkBytes;     // 8 chunks of 64 rows
+constexpr uint32_t kProbs = kQuery + kChunks * kRows * 128;    // P^T: 128 keys of 64 rows
+constexpr uint32_t kShared = kProbs + kTileKeys * 128;
+
+struct Shared {
+    uint64_t full[kChunks], free[kChunks / 2];
+    uint64_t scores, probs, query, query_free, output;
+    uint32_t tmem;
+    int scratch[18];
+    alignas(16) float m[kRows];
+    alignas(16) float factor[kRows];
+    float sum[4][kRows], top[4][kRows];
+    int seen_to[kRows], seen_from[kRows];
+    uint8_t key_ok[kTileKeys];
+};
+constexpr size_t kSmemBytes = 1024 + kShared + sizeof(Shared);
+static_assert(kSmemBytes <= 227 * 1024, "too much shared memory");
+
+// monotone map of a float to an int, for integer maxima; NaN counts as -infinity
+__device__ __forceinline__ int ordered(float x)
 {
-    return uint64_t(a.b.batch) * uint32_t(a.q_len) * uint32_t(a.heads);
+    const int b = __float_as_int(x == x ? x : -INFINITY);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i)
+{
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
-__device__ __forceinline__ void flag(int32_t *err, int bit)
-{
-    if (err != nullptr)
-        atomicOr(err, bit);
-}
+// ---- Warps 8..15: cache rows and queries into operands
 
-__device__ __forceinline__ float warp_sum(float v)
+__device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c)
 {
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
-        v += __shfl_xor_sync(kFull, v, m);
-    return v;
-}
-
-// the keys of request r, as many as its row of the table can name
-__device__ __forceinline__ int length_of(const Fp4Batch &b, int r)
-{
-    const int limit = b.width * b.block_size;
-    const int n = int(ldg4_in(b.lens + r, Span{b.lens, uint64_t(b.batch) * 4u}, b.err));
-    if (n > limit)
-        flag(b.err, DSV4_DEVERR_SLOT_RANGE);
-    return n < 0 ? 0 : n > limit ? limit : n;
-}
-
-// dims [8l, 8l+8) and [256+8l, 256+8l+8) of key i of request r as fp32; false for a bad block
-__device__ __forceinline__ bool load_key(const AParams &p, int lane, int r, int i, float *x)
-{
-    const Fp4Batch &b = p.a.b;
-    const uint32_t at = fastdiv(uint32_t(i), p.block_div);
-    const int32_t *entry = b.table + r * b.table_stride + at;
-    const uint32_t blk = ldg4_in(entry, Span{b.table, (uint64_t(b.batch - 1) * b.table_stride + b.width) * 4u}, b.err);
-    if (int64_t(blk) >= b.num_blocks) {
-        flag(b.err, DSV4_DEVERR_SLOT_RANGE);
-        return false;
-    }
-    const Fp4Row row = fp4_row(b.cache, blk, uint32_t(i) - at * uint32_t(b.block_size), uint32_t(b.block_size));
-    const Span cs = cache_span(b);
-    const uint32_t e0 = ldg_byte_in(row.scale + (lane >> 2), cs, b.err);
-    widen8(fp4x8_to_bf16(ldg4_in(row.data + 4 * lane, cs, b.err), fp4_scale_bf16x2(e0)), x);
-    if (lane < 24) {
-        const uint32_t e1 = ldg_byte_in(row.scale + 8 + (lane >> 2), cs, b.err);
-        widen8(fp4x8_to_bf16(ldg4_in(row.data + 128 + 4 * lane, cs, b.err), fp4_scale_bf16x2(e1)), x + 8);
-    } else {
-        widen8(ldg16_in(row.data + kFp4Codes + 16 * (lane - 24), cs, b.err), x + 8);
-    }
-    return true;
-}
-
-__device__ __forceinline__ float dot16(const float *x, const float *y)
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        s = __fmaf_rn(x[i], y[i], s);
-    return warp_sum(s);
-}
-
-// one warp per query row, the running maximum and sum of a softmax over its keys
-__global__ void __launch_bounds__(128) fp4_attention_kernel(const AParams p)
-{
-    const Fp4AttentionArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= int64_t(rows_of(a)))
-        return;
-    const int h = int(row % a.heads);
-    const int64_t token = row / a.heads;
-    const int r = int(token / a.q_len), j = int(token % a.q_len);
-    const int n = length_of(a.b, r);
-    const int to = n - a.q_len + 1 + j;
-    const int from = a.window > 0 && to > a.window ? to - a.window : 0;
-    const Span qs{a.q, rows_of(a) * 1024u};
-    float q[16], o[16];
-    widen8(ldg16_in(a.q + row * 512 + 8 * lane, qs, a.b.err), q);
-    widen8(ldg16_in(a.q + row * 512 + 256 + 8 * lane, qs, a.b.err), q + 8);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        o[i] = 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    if (a.sinks != nullptr) {
-        m = ldg_f32_in(a.sinks + h, Span{a.sinks, uint64_t(a.heads) * 4u}, a.b.err);
-        l = 1.0f;
-    }
-    for (int i = from; i < to; ++i) {
-        float x[16];
-        if (!load_key(p, lane, r, i, x))
-            continue;
-        const float s = dot16(q, x) * a.scale;
-        const float top = fmaxf(m, s);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - top), w = expf(s - top);
-        m = top;
-        l = l * keep + w;
-#pragma unroll
-        for (int d = 0; d < 16; ++d)
-            o[d] = __fmaf_rn(o[d], keep, w * x[d]);
-    }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int d = 0; d < 16; ++d)
-        o[d] *= inv;
-    const Span os{a.out, rows_of(a) * 1024u};
-    st16_in(a.out + row * 512 + 8 * lane, bf16x8_rn(o), os, a.b.err);
-    st16_in(a.out + row * 512 + 256 + 8 * lane, bf16x8_rn(o + 8), os, a.b.err);
-    if (a.lse != nullptr && lane == 0)
-        st_f32_in(a.lse + row, l == 0.0f ? -INFINITY : m + logf(l), Span{a.lse, rows_of(a) * 4u}, a.b.err);
-}
-
-// one warp per key, the rows in order
-__global__ void __launch_bounds__(128) fp4_weights_kernel(const AParams p)
-{
-    const Fp4AttentionArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.y;
-    const int n = length_of(a.b, r);
-    if (n > a.weights_width)
-        flag(a.b.err, DSV4_DEVERR_SLOT_RANGE);
-    const int most = n < a.weights_width ? n : a.weights_width;
-    const Span qs{a.q, rows_of(a) * 1024u}, ls{a.lse, rows_of(a) * 4u};
-    const Span ws{a.weights, (uint64_t(a.b.batch - 1) * a.weights_stride + a.weights_width) * 4u};
-    for (int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5); i < most; i += int(gridDim.x) * 4) {
-        float x[16];
-        if (!load_key(p, lane, r, i, x))
-            continue;
-        float sum = 0.0f;
-        for (int j = 0; j < a.q_len; ++j) {
-            const int to = n - a.q_len + 1 + j;
-            if (i >= to || (a.window > 0 && i < to - a.window))
-                continue;
-            for (int h = 0; h < a.heads; ++h) {
-                const int64_t row = (int64_t(r) * a.q_len + j) * a.heads + h;
-                float q[16];
-                widen8(ldg16_in(a.q + row * 512 + 8 * lane, qs, a.b.err), q);
-                widen8(ldg16_in(a.q + row * 512 + 256 + 8 * lane, qs, a.b.err), q + 8);
-                const float lse = ldg_f32_in(a.lse + row, ls, a.b.err);
-                const float s = dot16(q, x) * a.scale;
-                sum += lse == -INFINITY ? 0.0f : expf(s - lse);
-            }
+    const int tid = threadIdx.x - 256, key = tid >> 1, half = tid & 1, lane = tid & 31;
+    const int count = c.left;
+    KeyPlace now = key_place(p, c, true, key);
+    Fp4Row row = row_at(p, now);
+    RawTile raw;
+    const auto load_all = [&](auto self, auto ci) {
+        constexpr int i = decltype(ci)::value;
+        load_chunk<i>(p, raw, row, half);
+        if constexpr (i < kChunks - 1)
+            self(self, std::integral_constant<int, i + 1>{});
+    };
+    load_all(load_all, std::integral_constant<int, 0>{});
+    raw.scales = load_raw(p, row.scale, row.data != nullptr);
+    bool ok = row.data != nullptr;
+    bool moved = c.advance(p);
+    KeyPlace next = key_place(p, c, moved, key);
+    int segment = 0;
+    for (int t = 0; t < count; ++t) {
+        row = row_at(p, next);
+        const uint4 next_scales = load_raw(p, row.scale, row.data != nullptr);
+        KeyPlace after = next;
+        if (c.left > 0) {
+            moved = c.advance(p);
+            after = key_place(p, c, moved, key);
         }
-        float *w = a.weights + r * a.weights_stride + i;
-        if (lane == 0)
-            st_f32_in(w, ld_f32_in(w, ws, a.b.err) + sum, ws, a.b.err);
+        bool alive = true;
+        if (now.new_unit) {
+            if (segment > 0)
+                alive = __all_sync(kFull, mbar_wait(&s.query_free, (segment - 1) & 1));
+            if (alive) {
+                load_query(p, now.unit, smem + kQuery, kRows, tid, 256);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&s.query);
+            }
+            ++segment;
+        }
+        const auto chunk = [&](auto self, auto ci) {
+            constexpr int i = decltype(ci)::value;
+            if (i % 2 == 0 && t > 0 && alive)
+                alive = __all_sync(kFull, mbar_wait(&s.free[i / 2], (t - 1) & 1));
+            if (!alive)
+                return;
+            if (i == 0 && half == 0)
+                s.key_ok[key] = ok ? 1 : 0;
+            convert_chunk<i>(raw, smem + kKeys + i * kChunkBytes, key, half);
+            load_chunk<i>(p, raw, row, half);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.full[i]);
+            if constexpr (i < kChunks - 1)
+                self(self, std::integral_constant<int, i + 1>{});
+        };
+        chunk(chunk, std::integral_constant<int, 0>{});
+        if (!alive) {
+            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+            return;
+        }
+        raw.scales = next_scales;
+        ok = row.data != nullptr;
+        now = next;
+        next = after;
     }
+}
+
+// ---- One thread of warp 16: the products
+
+__device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
+{
+    const uint32_t d_scores = s.tmem, d_output = s.tmem + kRows;
+    uint32_t scores_inst = 0, output_inst = 0;
+    int segment = 0;
+    bool first = true;  // of its segment
+    for (uint32_t t = 0; c.left > 0; ++t) {
+        if (first) {
+            const uint32_t n = uint32_t((c.row1 - c.row0 + 15) & ~15);
+            scores_inst = instruction(n, false);
+            output_inst = instruction(n, true);
+            if (!mbar_wait(&s.query, segment & 1))
+                break;
+            ++segment;
+        }
+        const bool last = c.ends_segment();
+        bool alive = true;
+        for (int i = 0; i < kChunks && alive; ++i) {
+            alive = mbar_wait(&s.full[i], t & 1);
+            tmem_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (alive)
+                    mma_bf16(d_scores, operand(smem + kKeys + i * kChunkBytes + 32 * k, 16, 1024),
+                             operand(smem + kQuery + i * kRows * 128 + 32 * k, 16, 1024), scores_inst,
+                             i > 0 || k > 0);
+        }
+        if (!alive)
+            break;
+        mma_commit(&s.scores);
+        if (last)
+            mma_commit(&s.query_free);
+        if (!mbar_wait(&s.probs, t & 1))
+            break;
+        tmem_fence_after();
+        for (int i = 0; i < kChunks / 2; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_bf16(d_output + i * kRows,
+                         operand(smem + kKeys + 2 * i * kChunkBytes + 2048 * k, kChunkBytes, 1024),
+                         operand(smem + kProbs + 2048 * k, kChunkBytes, 1024), output_inst,
+                         !first || k > 0);
+            mma_commit(&s.free[i]);
+        }
+        if (last)
+            mma_commit(&s.output);
+        first = last;
+        c.advance(p);
+    }
+    if (c.left > 0)
+        flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+}
+
+// ---- Warps 0..7: softmax and results
+
+// Move the references of a warpgroup's rows up to the scores x of this tile and
+// rescale what was taken against the old ones.
+__device__ __forceinline__ void move_references(Shared &s, const float *x, float *sum, uint32_t tmem,
+                                                bool rescale_output)
+{
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
+    const int col0 = group * 32;
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const int top = __reduce_max_sync(kFull, ordered(x[j]));
+        if (lane == j)
+            mine = top;
+    }
+    s.top[warp][col0 + lane] = unordered(mine);
+    named_barrier(1 + group, 128);
+    if (warp == 0) {
+        const int j = col0 + lane;
+        const float old = s.m[j];
+        const float m = fmaxf(fmaxf(old, fmaxf(s.top[0][j], s.top[1][j])), fmaxf(s.top[2][j], s.top[3][j]));
+        s.m[j] = m;
+        s.factor[j] = exp2_approx(old - m);
+    }
+    named_barrier(1 + group, 128);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        sum[j] *= s.factor[col0 + j];
+    if (rescale_output) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = tmem + kRows + (i >> 1) * kRows + col0 + (i & 1) * 16;
+            float o[16];
+            tmem_load16(at, o);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                o[j] *= s.factor[col0 + (i & 1) * 16 + j];
+            tmem_store16(at, o);
+        }
+        tmem_wait_store();
+    }
+}
+
+// sums of 32 values over the 32 lanes of a warp: lane j returns that of v[j]
+__device__ __forceinline__ float transposed_sum(float *v, int lane)
+{
+#pragma unroll
+    for (int half = 16; half >= 1; half >>= 1) {
+        const bool upper = (lane & half) != 0;
+#pragma unroll
+        for (int j = 0; j < half; ++j) {
+            const float keep = upper ? v[j + half] : v[j];
+            const float give = upper ? v[j] : v[j + half];
+            v[j] = keep + __shfl_xor_sync(kFull, give, half);
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ float sink_of(const Fp4AttentionArgs &a, int row)
+{
+    return a.sinks == nullptr ? -INFINITY
+                              : kLog2e * ldg_f32_in(a.sinks + row % a.heads,
+                                                    Span{a.sinks, uint64_t(a.heads) * 4u}, a.b.err);
+}
+
+// From a row's m and sum (both without the sink): the factor that makes its O the
+// output, and its lse.
+__device__ __forceinline__ float finish(float m, float sum, float sink, float *lse)
+{
+    if (sum == 0.0f)
+        m = -INFINITY;
+    const float top = fmaxf(m, sink);
+    if (top == -INFINITY) {
+        *lse = -INFINITY;
+        return 0.0f;
+    }
+    const float w = exp2_approx(m - top), total = sum * w + exp2_approx(sink - top);
+    *lse = (top + log2f(total)) * kLn2;
+    return w / total;
+}
+
+__device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor c)
+{
+    const AParams &p = w.p;
+    const Fp4AttentionArgs &a = p.a;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
+    const int key = warp * 32 + lane, col0 = group * 32;
+    const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
+    const float scale = a.scale * kLog2e;
+    float sum[32];
+    bool first = true;
+    int segment = 0, from_tile = 0;
+    for (uint32_t t = 0; c.left > 0; ++t) {
+        const int row0 = c.row0, rows = c.row1 - c.row0;
+        if (first) {
+            from_tile = c.tile;
+            if (warp == 0) {
+                const int r = col0 + lane;
+                const int to = r < rows ? c.n - a.q_len + 1 + (row0 + r) / a.heads : 0;
+                s.seen_to[r] = to;
+                s.seen_from[r] = a.window > 0 ? to - a.window : INT32_MIN;
+                s.m[r] = kUnset;
+            }
+            named_barrier(1 + group, 128);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                sum[j] = 0.0f;
+        }
+        const bool last = c.ends_segment();
+        bool failed = !mbar_wait(&s.scores, t & 1);
+        tmem_fence_after();
+        const int i = c.tile * kTileKeys + key;
+        // every row of the group sees every key of the tile: the first row sees the
+        // fewest at the end, the last one the fewest at the start
+        const bool whole = rows >= col0 + 32 && (c.tile + 1) * kTileKeys <= s.seen_to[col0] &&
+                           c.tile * kTileKeys >= s.seen_from[col0 + 31];
+        const bool ok = s.key_ok[key] != 0;
+        float v[32];
+        // v = the scores less `reference` (a row each; null: none), -infinity where unseen
+        const auto load_scores = [&](const float *reference) {
+            __syncwarp();
+            tmem_load32(tmem + col0, v);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 m = reference != nullptr
+                                     ? *reinterpret_cast<const float4 *>(reference + col0 + j)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[j] = __fmaf_rn(v[j], scale, -m.x);
+                v[j + 1] = __fmaf_rn(v[j + 1], scale, -m.y);
+                v[j + 2] = __fmaf_rn(v[j + 2], scale, -m.z);
+                v[j + 3] = __fmaf_rn(v[j + 3], scale, -m.w);
+            }
+            if (!whole) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (i >= s.seen_to[col0 + j] || i < s.seen_from[col0 + j])
+                        v[j] = -INFINITY;
+            }
+            if (!ok) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = -INFINITY;
+            }
+        };
+        load_scores(s.m);
+        float over = v[0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j)
+            over = fmaxf(over, v[j]);
+        if (named_barrier_any(1 + group, 128, failed || over > kSlack)) {
+            if (named_barrier_any(1 + group, 128, failed)) {
+                flag(a.b.err, DSV4_DEVERR_TIMEOUT);
+                return;
+            }
+            load_scores(nullptr);
+            move_references(s, v, sum, tmem, !first);
+            load_scores(s.m);
+        }
+        uint32_t packed[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float p0 = exp2_approx(v[j]), p1 = exp2_approx(v[j + 1]);
+            sum[j] += p0;
+            sum[j + 1] += p1;
+            packed[j / 2] = bf16x2_rn(p0, p1);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4 *>(smem + kProbs + swizzled(key, group * 4 + k)) =
+                make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
+        fence_proxy_async_smem();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&s.probs);
+        if (last) {
+            // the segment's result
+            s.sum[warp][col0 + lane] = transposed_sum(sum, lane);
+            failed = !mbar_wait(&s.output, segment & 1);
+            ++segment;
+            if (named_barrier_any(1 + group, 128, failed)) {
+                flag(a.b.err, DSV4_DEVERR_TIMEOUT);
+                return;
+            }
+            tmem_fence_after();
+            const bool whole_range = from_tile == c.range.first() && c.tile + 1 == c.range.stop();
+            const int r = col0 + lane;
+            float total = (s.sum[0][r] + s.sum[1][r]) + (s.sum[2][r] + s.sum[3][r]);
+            const int64_t out_row = int64_t(c.request(p)) * p.all_rows + row0;
+            // the run's first segment or its last
+            float *part = partial_at(w, blockIdx.x, t + 1 == uint32_t(c.tile + 1 - from_tile) ? 0 : 1);
+            const Span ps = partial_span(w);
+            if (warp == 0) {
+                if (whole_range) {
+                    float lse = 0.0f;
+                    if (r < rows)
+                        s.factor[r] = finish(s.m[r], total, sink_of(a, row0 + r), &lse);
+                    if (r < rows && a.lse != nullptr)
+                        st_f32_in(a.lse + out_row + r, lse, Span{a.lse, rows_of(a) * 4u}, a.b.err);
+                } else {
+                    st_f32_in(part + kRows * DSV4_HEAD_DIM + r, s.m[r], ps, a.b.err);
+                    st_f32_in(part + kRows * DSV4_HEAD_DIM + kRows + r, total, ps, a.b.err);
+                }
+            }
+            named_barrier(1 + group, 128);
+            const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
+            const int mine = rows - col0 < 32 ? rows - col0 : 32;
+            if (mine > 0) {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    float o[32];
+                    tmem_load32(tmem + kRows + k * kRows + col0, o);
+                    tmem_wait_load();
+                    const int dim = k * 128 + key;
+                    if (whole_range) {
+                        // neighbouring lanes swap, so that each stores two dims of one row
+                        const int odd = lane & 1;
+                        uint16_t *to = a.out + (out_row + col0 + odd) * DSV4_HEAD_DIM + (dim - odd);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float o0 = o[j] * s.factor[col0 + j];
+                            const float o1 = o[j + 1] * s.factor[col0 + j + 1];
+                            const float other = __shfl_xor_sync(kFull, odd ? o0 : o1, 1);
+                            if (j + odd < mine)
+                                st4_in(to + j * DSV4_HEAD_DIM, odd ? bf16x2_rn(other, o1) : bf16x2_rn(o0, other),
+                                       os, a.b.err);
+                        }
+                    } else {
+                        float *to = part + col0 * DSV4_HEAD_DIM + dim;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < mine)
+                                st_f32_in(to + j * DSV4_HEAD_DIM, o[j], ps, a.b.err);
+                    }
+                }
+            }
+            tmem_fence_before();
+            named_barrier(1 + group, 128);  // m, sum and factor are free for the next segment
+        }
+        first = last;
+        c.advance(p);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid_constant__ WParams w)
+{
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+    Shared &s = *reinterpret_cast<Shared *>(smem + kShared);
+    const AParams &p = w.p;
+    const int warp = threadIdx.x >> 5;
+    Cursor c;
+    deal(p, blockIdx.x, gridDim.x, s.scratch, c);
+    if (c.left == 0)
+        return;
+    if (warp == 16) {
+        tmem_alloc512(&s.tmem);
+        if ((threadIdx.x & 31) == 0) {
+            for (int i = 0; i < kChunks; ++i)
+                mbar_init(&s.full[i], 8);
+            for (int i = 0; i < kChunks / 2; ++i)
+                mbar_init(&s.free[i], 1);
+            mbar_init(&s.scores, 1);
+            mbar_init(&s.probs, 8);
+            mbar_init(&s.query, 8);
+            mbar_init(&s.query_free, 1);
+            mbar_init(&s.output, 1);
+            mbar_init_fence();
+        }
+        tmem_fence_before();
+    }
+    __syncthreads();
+    tmem_fence_after();
+    if (warp < 8) {
+        softmax_role(w, s, smem, c);
+    } else if (warp < 16) {
+        convert_role(p, s, smem, c);
+    } else {
+        if ((threadIdx.x & 31) == 0)
+            multiply_role(p, s, smem_addr(smem), c);
+        __syncwarp();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 16) {
+        tmem_fence_after();
+        tmem_free512(s.tmem);
+    }
+}
+
+// Joins the partial results of the units whose tiles more than one run took, and
+// writes the rows that see no key.  Block (u, z): rows z * join_rows.. of unit u.
+constexpr int kJoinThreads = 128;
+
+struct JParams {
+    WParams w;
+    int join_rows;
+};
+
+__global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const __grid_constant__ JParams jp)
+{
+    __shared__ int before_s[4], total_s[4];
+    const WParams &w = jp.w;
+    const AParams &p = w.p;
+    const Fp4AttentionArgs &a = p.a;
+    const int r0 = blockIdx.y * jp.join_rows;
+    Cursor c;
+    c.unit = blockIdx.x;
+    c.enter(p);
+    const int row0 = c.row0, row1 = c.row1;
+    if (row0 + r0 >= row1)
+        return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int before = 0, total = 0;
+    for (int i = threadIdx.x; i < p.units; i += kJoinThreads) {
+        const int tiles = tiles_of(p, i);
+        total += tiles;
+        before += i < c.unit ? tiles : 0;
+    }
+    before = __reduce_add_sync(kFull, before);
+    total = __reduce_add_sync(kFull, total);
+    if (lane == 0) {
+        before_s[warp] = before;
+        total_s[warp] = total;
+    }
+    __syncthreads();
+    before = before_s[0] + before_s[1] + before_s[2] + before_s[3];
+    total = total_s[0] + total_s[1] + total_s[2] + total_s[3];
+    const int tiles = c.range.tiles();
+    const int share = (total + w.runs - 1) / w.runs;
+    const int x0 = tiles > 0 ? before / share : 0, x1 = tiles > 0 ? (before + tiles - 1) / share : -1;
+    if (tiles > 0 && x0 == x1)
+        return;  // written by its run
+    const Span ps = partial_span(w);
+    const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
+    // the first run may have begun with an earlier unit
+    const int slot0 = before == x0 * share ? 0 : 1;
+    for (int r = r0; r < r0 + jp.join_rows && row0 + r < row1; ++r) {
+        float m = kUnset;
+        for (int x = x0 + lane; x <= x1; x += 32) {
+            const float *part = partial_at(w, x, x == x0 ? slot0 : 0) + kRows * DSV4_HEAD_DIM;
+            if (ld_f32_in(part + kRows + r, ps, a.b.err) != 0.0f)
+                m = fmaxf(m, ld_f32_in(part + r, ps, a.b.err));
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+        float sum = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int x = x0; x <= x1; ++x) {
+            const float *part = partial_at(w, x, x == x0 ? slot0 : 0);
+            const float n = ld_f32_in(part + kRows * DSV4_HEAD_DIM + kRows + r, ps, a.b.err);
+            const float f = n == 0.0f ? 0.0f : exp2_approx(ld_f32_in(part + kRows * DSV4_HEAD_DIM + r, ps, a.b.err) - m);
+            const float4 v = ld_f4_in(part + r * DSV4_HEAD_DIM + 4 * threadIdx.x, ps, a.b.err);
+            sum += n * f;
+            o.x += v.x * f;
+            o.y += v.y * f;
+            o.z += v.z * f;
+            o.w += v.w * f;
+        }
+        const int64_t row = int64_t(c.request(p)) * p.all_rows + row0 + r;
+        float lse;
+        const float f = finish(m, sum, sink_of(a, row0 + r), &lse);
+        st8_in(a.out + row * DSV4_HEAD_DIM + 4 * threadIdx.x,
+               f == 0.0f ? make_uint2(0u, 0u)
+                         : make_uint2(bf16x2_rn(o.x * f, o.y * f), bf16x2_rn(o.z * f, o.w * f)),
+               os, a.b.err);
+        if (threadIdx.x == 0 && a.lse != nullptr)
+            st_f32_in(a.lse + row, lse, Span{a.lse, rows_of(a) * 4u}, a.b.err);
+    }
+}
+
+int configure(int *sms)
+{
+    static std::atomic<int> sm_count[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return DSV4_ERR_CUDA;
+    const bool cached = dev >= 0 && dev < 64;
+    *sms = cached ? sm_count[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms > 0)
+        return DSV4_OK;
+    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms < 1 ||
+        cudaFuncSetAttribute(fp4_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(kSmemBytes)) != cudaSuccess)
+        return DSV4_ERR_CUDA;
+    if (cached)
+        sm_count[dev].store(*sms, std::memory_order_relaxed);
+    return DSV4_OK;
 }
 
 }  // namespace
 
-int launch_fp4_attention(const Fp4AttentionArgs &a, cudaStream_t stream)
+size_t fp4_attention_workspace()
 {
-    AParams p{a, fastdiv_magic(uint32_t(a.b.block_size))};
-    const int64_t rows = int64_t(a.b.batch) * a.q_len * a.heads;
-    return launch_kernel(fp4_attention_kernel, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, stream, p);
+    return size_t(kMaxCtas) * 2 * kPartialFloats * sizeof(float);
 }
 
-int launch_fp4_weights(const Fp4AttentionArgs &a, cudaStream_t stream)
+int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_t stream)
 {
-    AParams p{a, fastdiv_magic(uint32_t(a.b.block_size))};
-    return launch_kernel(fp4_weights_kernel, dim3(1024, unsigned(a.b.batch)), dim3(128), 0, stream, p);
+    int sms = 0;
+    if (configure(&sms) != DSV4_OK)
+        return DSV4_ERR_CUDA;
+    JParams j;
+    j.w.p = tile_params(a, kRows);
+    j.w.partials = static_cast<float *>(workspace);
+    const int64_t most = (int64_t(a.b.width) * a.b.block_size + kTileKeys - 1) / kTileKeys * j.w.p.units;
+    int runs = sms < kMaxCtas ? sms : kMaxCtas;
+    runs = most < runs ? int(most) : runs;
+    j.w.runs = runs;
+    const int st = launch_kernel(fp4_attention_kernel, dim3(unsigned(runs)), dim3(kThreads), kSmemBytes,
+                                 stream, j.w);
+    if (st != DSV4_OK)
+        return st;
+    j.join_rows = j.w.p.units >= 32 ? 4 : 1;
+    const int rows = j.w.p.all_rows < kRows ? j.w.p.all_rows : kRows;
+    return launch_kernel(fp4_join_kernel,
+                         dim3(unsigned(j.w.p.units), unsigned((rows + j.join_rows - 1) / j.join_rows)),
+                         dim3(kJoinThreads), 0, stream, j);
 }
 
 }  // namespace dsv4

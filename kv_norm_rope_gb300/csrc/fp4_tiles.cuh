@@ -1,0 +1,309 @@
+// What the attention over the 4-bit cache and the attention weights share: which
+// keys a tile of query rows sees, how the tiles of keys of all requests are
+// dealt out to CTAs, and how a tile of cache rows becomes a bf16 matrix operand.
+//
+// A tile is 128 keys, aligned in the request.  The tiles that some row of a row
+// tile sees, over all requests in order, form one line; each CTA takes an equal
+// run of it.  So a long request is shared by many CTAs and short ones share a
+// CTA, whatever the lengths, which only the device knows.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "bounds.cuh"
+#include "fp4.cuh"
+#include "ops.h"
+#include "tcgen05.cuh"
+
+namespace dsv4 {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kTileKeys = 128;
+constexpr int kChunks = 8;                    // a row in chunks of 64 dims: 7 of codes, 1 of rope
+constexpr uint32_t kChunkBytes = kTileKeys * 128;
+
+struct AParams {
+    Fp4AttentionArgs a;
+    uint64_t block_div;  // fastdiv_magic(block_size)
+    int all_rows;        // q_len * heads
+    int tile_rows;       // of a row tile
+    int row_tiles;       // of a request
+    int units;           // row tiles of the batch
+};
+
+__device__ __forceinline__ Span cache_span(const Fp4Batch &b)
+{
+    return Span{b.cache, uint64_t(b.num_blocks) * uint32_t(b.block_size) * kFp4Slot};
+}
+__device__ __forceinline__ Span table_span(const Fp4Batch &b)
+{
+    return Span{b.table, (uint64_t(b.batch - 1) * b.table_stride + b.width) * 4u};
+}
+__device__ __forceinline__ uint64_t rows_of(const Fp4AttentionArgs &a)
+{
+    return uint64_t(a.b.batch) * uint32_t(a.q_len) * uint32_t(a.heads);
+}
+
+__device__ __forceinline__ void flag(int32_t *err, int bit)
+{
+    if (err != nullptr)
+        atomicOr(err, bit);
+}
+
+// the keys of request r, as many as its row of the table can name
+__device__ __forceinline__ int length_of(const Fp4Batch &b, int r)
+{
+    const int limit = b.width * b.block_size;
+    const int n = int(ldg4_in(b.lens + r, Span{b.lens, uint64_t(b.batch) * 4u}, b.err));
+    if (n > limit)
+        flag(b.err, DSV4_DEVERR_SLOT_RANGE);
+    return n < 0 ? 0 : n > limit ? limit : n;
+}
+
+// The keys [lo, hi) that some of the rows [row0, row1) of a request of n keys sees,
+// and the tiles they lie in.  Row r is head r % heads of token r / heads.
+struct Range {
+    int lo, hi;
+    __device__ __forceinline__ int first() const { return lo / kTileKeys; }
+    __device__ __forceinline__ int stop() const { return (hi + kTileKeys - 1) / kTileKeys; }
+    __device__ __forceinline__ int tiles() const { return stop() - first(); }
+};
+
+__device__ __forceinline__ Range range_of(const Fp4AttentionArgs &a, int n, int row0, int row1)
+{
+    const int hi = n - a.q_len + 1 + (row1 - 1) / a.heads;
+    if (hi <= 0)
+        return Range{0, 0};
+    const int from = a.window > 0 ? n - a.q_len + 1 + row0 / a.heads - a.window : 0;
+    return Range{from > 0 ? from : 0, hi};
+}
+
+// A place on a CTA's run of tiles.  A unit is one row tile of one request.
+struct Cursor {
+    int unit, tile, left, n, row0, row1;
+    Range range;
+
+    // the unit's numbers, for a place inside it
+    __device__ __forceinline__ void enter(const AParams &p)
+    {
+        row0 = unit % p.row_tiles * p.tile_rows;
+        row1 = row0 + p.tile_rows < p.all_rows ? row0 + p.tile_rows : p.all_rows;
+        n = length_of(p.a.b, request(p));
+        range = range_of(p.a, n, row0, row1);
+    }
+
+    __device__ __forceinline__ int request(const AParams &p) const { return unit / p.row_tiles; }
+
+    // true when this tile is the last of the run or of its unit
+    __device__ __forceinline__ bool ends_segment() const
+    {
+        return left == 1 || tile + 1 == range.stop();
+    }
+
+    // to the next tile; true when that is in another unit
+    __device__ __forceinline__ bool advance(const AParams &p)
+    {
+        if (--left == 0)
+            return false;
+        if (++tile < range.stop())
+            return false;
+        do {
+            if (++unit >= p.units) {  // only if the lengths changed under the launch
+                left = 0;
+                return false;
+            }
+            enter(p);
+        } while (range.tiles() == 0);
+        tile = range.first();
+        return true;
+    }
+};
+
+__device__ __forceinline__ int tiles_of(const AParams &p, int unit)
+{
+    Cursor c;
+    c.unit = unit;
+    c.enter(p);
+    return c.range.tiles();
+}
+
+// Places c at the start of CTA x's run.  All threads of the CTA (at least
+// kDealThreads) call it.  scratch: 18 words of shared memory.
+constexpr int kDealThreads = 512;
+
+__device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratch, Cursor &c)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const auto count = [&](int base) {
+        return tid < kDealThreads && base + tid < p.units ? tiles_of(p, base + tid) : 0;
+    };
+    int total = 0, mine = 0;
+    for (int base = 0; base < p.units; base += kDealThreads) {
+        mine = count(base);
+        const int sum = __reduce_add_sync(kFull, mine);
+        if (lane == 0 && warp < kDealThreads / 32)
+            scratch[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < kDealThreads / 32; ++w)
+            total += scratch[w];
+        __syncthreads();
+    }
+    const int share = (total + X - 1) / X;
+    const int64_t begin = int64_t(x) * share;
+    c.left = begin < total ? (total - int(begin) < share ? total - int(begin) : share) : 0;
+    if (c.left == 0)
+        return;
+    const int t0 = int(begin);
+    int before = 0;
+    for (int base = 0; base < p.units && before <= t0; base += kDealThreads) {
+        if (p.units > kDealThreads)
+            mine = count(base);
+        int upto = mine;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int o = __shfl_up_sync(kFull, upto, s);
+            if (lane >= s)
+                upto += o;
+        }
+        if (lane == 31 && warp < kDealThreads / 32)
+            scratch[warp] = upto;
+        __syncthreads();
+        int start = before;
+        for (int w = 0; w < kDealThreads / 32; ++w) {
+            if (w < warp)
+                start += scratch[w];
+            before += scratch[w];
+        }
+        upto += start;
+        if (mine > 0 && upto - mine <= t0 && t0 < upto) {
+            scratch[16] = base + tid;
+            scratch[17] = t0 - (upto - mine);
+        }
+        __syncthreads();
+    }
+    c.unit = scratch[16];
+    c.enter(p);
+    c.tile = c.range.first() + scratch[17];
+    __syncthreads();  // scratch may be used again
+}
+
+// ---- Cache rows -> operand
+//
+// 256 threads: thread i owns half (i & 1) of each chunk of key i / 2 of a tile,
+// that is one scale group (16 bytes of codes) of chunks 0..6 and 64 bytes of rope
+// in chunk 7.  The raw bytes of the next tile are loaded as soon as those of this
+// one are converted, so a whole tile (45 KB) is in flight per CTA.
+
+struct RawTile {
+    uint4 codes[7], rope[4], scales;
+};
+
+// where a thread's key of a tile is; found two tiles ahead, as the block number is
+// itself loaded
+struct KeyPlace {
+    uint32_t entry, off;
+    bool seen, new_unit;
+    int unit;
+};
+
+__device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c, bool new_unit,
+                                              int key)
+{
+    KeyPlace k;
+    const int i = c.tile * kTileKeys + key;
+    k.seen = c.left > 0 && i >= c.range.lo && i < c.range.hi;
+    k.new_unit = new_unit;
+    k.unit = c.unit;
+    k.entry = k.off = 0u;
+    if (k.seen) {
+        const uint32_t at = fastdiv(uint32_t(i), p.block_div);
+        k.off = uint32_t(i) - at * uint32_t(p.a.b.block_size);
+        k.entry = ldg4_in(p.a.b.table + c.request(p) * p.a.b.table_stride + at, table_span(p.a.b), p.a.b.err);
+    }
+    return k;
+}
+
+// the row of a placed key; data = null for none (not seen, or a bad block, which is flagged)
+__device__ __forceinline__ Fp4Row row_at(const AParams &p, const KeyPlace &k)
+{
+    if (!k.seen)
+        return Fp4Row{nullptr, nullptr};
+    if (int64_t(k.entry) >= p.a.b.num_blocks) {
+        flag(p.a.b.err, DSV4_DEVERR_SLOT_RANGE);
+        return Fp4Row{nullptr, nullptr};
+    }
+    return fp4_row(p.a.b.cache, k.entry, k.off, uint32_t(p.a.b.block_size));
+}
+
+__device__ __forceinline__ uint4 load_raw(const AParams &p, const uint8_t *at, bool ok)
+{
+    return ok ? ldg16_in(at, cache_span(p.a.b), p.a.b.err) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// chunk c of a key's half, from its raw bytes into the operand at `chunk`
+template <int c>
+__device__ __forceinline__ void convert_chunk(const RawTile &t, uint8_t *chunk, int key, int half)
+{
+    if constexpr (c == 7) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) = t.rope[i];
+    } else {
+        const uint32_t four = c < 2 ? t.scales.x : c < 4 ? t.scales.y : c < 6 ? t.scales.z : t.scales.w;
+        const uint32_t scale2 = fp4_scale_bf16x2((four >> (16 * (c & 1) + 8 * half)) & 255u);
+        const uint32_t w[4] = {t.codes[c].x, t.codes[c].y, t.codes[c].z, t.codes[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) = fp4x8_to_bf16(w[i], scale2);
+    }
+}
+
+template <int c>
+__device__ __forceinline__ void load_chunk(const AParams &p, RawTile &t, const Fp4Row &row, int half)
+{
+    const bool ok = row.data != nullptr;
+    if constexpr (c == 7) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t.rope[i] = load_raw(p, row.data + kFp4Codes + 64 * half + 16 * i, ok);
+    } else {
+        t.codes[c] = load_raw(p, row.data + 32 * c + 16 * half, ok);
+    }
+}
+
+// The query rows of a unit into the K-major operand of `rows` rows (chunk j: dims
+// 64j.., rows * 128 bytes), zeros past the unit's last.  `threads` threads.
+__device__ __forceinline__ void load_query(const AParams &p, int unit, uint8_t *to, int rows, int tid,
+                                           int threads)
+{
+    const Fp4AttentionArgs &a = p.a;
+    const int row0 = unit % p.row_tiles * p.tile_rows, real = p.all_rows - row0;
+    const uint16_t *q = a.q + (int64_t(unit / p.row_tiles) * p.all_rows + row0) * DSV4_HEAD_DIM;
+    const Span qs{a.q, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
+#pragma unroll 8
+    for (int i = tid; i < rows * 64; i += threads) {
+        const int r = i >> 6, c = i & 63;
+        const uint4 v = r < real ? ldg16_in(q + r * DSV4_HEAD_DIM + c * 8, qs, a.b.err)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(to + (c >> 3) * rows * 128 + swizzled(r, c & 7)) = v;
+    }
+}
+
+inline AParams tile_params(const Fp4AttentionArgs &a, int tile_rows)
+{
+    AParams p;
+    p.a = a;
+    p.block_div = fastdiv_magic(uint32_t(a.b.block_size));
+    p.all_rows = a.q_len * a.heads;
+    p.tile_rows = tile_rows;
+    p.row_tiles = (p.all_rows + tile_rows - 1) / tile_rows;
+    p.units = p.row_tiles * a.b.batch;
+    return p;
+}
+
+}  // namespace
+}  // namespace dsv4

@@ -96,8 +96,10 @@ int fp4_gather_ctas_per_sm(int *ctas_per_sm);
 int launch_fp4_gather(const uint8_t *cache, int64_t num_blocks, int32_t block_size,
                       const int64_t *slots, int64_t rows, uint16_t *out, int32_t *err,
                       int64_t max_ctas, cudaStream_t stream);
-// fp4_attention.cu
-int launch_fp4_attention(const Fp4AttentionArgs &a, cudaStream_t stream);
+// fp4_attention.cu; the workspace holds fp4_attention_workspace() bytes
+size_t fp4_attention_workspace();
+int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_t stream);
+// fp4_weights.cu
 int launch_fp4_weights(const Fp4AttentionArgs &a, cudaStream_t stream);
 // fp4_evict.cu
 int launch_fp4_evict(const Fp4EvictArgs &a, cudaStream_t stream);
@@ -112,6 +114,7 @@ int bounds_flag_indexer(int reset);
 int bounds_flag_mxfp8(int reset);
 int bounds_flag_fp4_gather(int reset);
 int bounds_flag_fp4_attention(int reset);
+int bounds_flag_fp4_weights(int reset);
 int bounds_flag_fp4_evict(int reset);
 
 }  // namespace dsv4

@@ -1,0 +1,164 @@
+// The fifth-generation tensor core: tensor memory, matrix instructions on
+// shared-memory operands, and their completion.
+//
+// Operands are bf16 in shared memory in the 128-byte swizzle: rows of 128 bytes
+// (64 elements), 8 rows to a 1024-byte atom, the 16-byte chunk c of row r stored
+// at chunk c ^ (r % 8).  The same bytes serve both ways round: read along the
+// rows (K-major: 64 elements of the product's inner dimension) or across them
+// (MN-major: 64 elements of an outer dimension, the rows being the inner one).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "bulkcopy.cuh"
+
+namespace dsv4 {
+namespace {
+
+// Byte offset of 16-byte chunk c of row r in a swizzled operand.
+__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c)
+{
+    return r * 128u + ((c ^ (r & 7u)) << 4);
+}
+
+// All columns of the CTA's tensor memory (one warp calls it; the address is
+// written to shared memory).
+__device__ __forceinline__ void tmem_alloc512(uint32_t *address)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(address))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free512(uint32_t address)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(address));
+}
+
+// Order this thread's tensor-memory accesses before a barrier / after one.
+__device__ __forceinline__ void tmem_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// Descriptor of a swizzled operand.  K-major: `stride` is the distance of the
+// 8-row groups.  MN-major: `stride` is that of the 8-row groups along the inner
+// dimension, `lead` that of the blocks of 64 outer elements.
+__device__ __forceinline__ uint64_t operand(uint32_t address, uint32_t lead, uint32_t stride)
+{
+    return uint64_t((address & 0x3ffffu) >> 4) | (uint64_t(lead >> 4) << 16) |
+           (uint64_t(stride >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor: bf16 operands, fp32 accumulator, M = 128, N = n;
+// `across` marks MN-major operands (both).
+__device__ __forceinline__ uint32_t instruction(uint32_t n, bool across)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (across ? 3u << 15 : 0u) | ((n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+
+// d[128, n] (+)= a[128, 16] b[16, n]; one thread issues it
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t inst,
+                                         bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(inst), "r"(accumulate ? 1u : 0u)
+                 : "memory");
+}
+
+// arrive on *bar once every matrix instruction this thread has issued is done
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
+
+// 32 columns from `address` on of the calling thread's lane (warp w of a
+// warpgroup: lanes 32w..); finished after tmem_wait_load
+__device__ __forceinline__ void tmem_load32(uint32_t address, float *v)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+          "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+          "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(address));
+}
+
+// the same for 16 columns
+__device__ __forceinline__ void tmem_load16(uint32_t address, float *v)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15])
+        : "r"(address));
+}
+
+__device__ __forceinline__ void tmem_wait_load()
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t address, const float *v)
+{
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(v);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(address),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+        "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_store()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 2^x, flushing subnormal results
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// barrier `id` over `threads` threads that also returns whether any of them brought `v`
+__device__ __forceinline__ bool named_barrier_any(int id, int threads, bool v)
+{
+    uint32_t any;
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.or.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(v ? 1u : 0u), "r"(id), "r"(threads)
+                 : "memory");
+    return any != 0u;
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads)
+{
+    __syncwarp();
+    asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+}  // namespace
+}  // namespace dsv4
