@@ -53,16 +53,40 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// the 8 codes of a word times the group's scale -> 8 bf16 in dim order, exact
-__device__ __forceinline__ uint4 fp4x8_to_bf16(uint32_t w, uint32_t scale2)
+// the 8 codes of a word as bf16 2^-126 times their values, in dim order
+__device__ __forceinline__ uint4 fp4x8_small(uint32_t w)
 {
-    const uint32_t k126 = 0x7E807E80u;  // bf16x2 (2^126, 2^126)
-    const auto pair = [&](uint32_t sign, uint32_t rest) {
-        return mul_bf16x2(mul_bf16x2((sign & 0x80008000u) | (rest & 0x01C001C0u), k126), scale2);
+    const auto pair = [](uint32_t sign, uint32_t rest) {
+        return (sign & 0x80008000u) | (rest & 0x01C001C0u);
     };
     return make_uint4(pair(w << 12, w << 6), pair(w << 8, w << 2), pair(w << 4, w >> 2),
                       pair(w, w >> 6));
 }
+
+__device__ __forceinline__ uint4 mul_bf16x8(uint4 v, uint32_t k2)
+{
+    return make_uint4(mul_bf16x2(v.x, k2), mul_bf16x2(v.y, k2), mul_bf16x2(v.z, k2),
+                      mul_bf16x2(v.w, k2));
+}
+
+// the 8 codes of a word times the group's scale -> 8 bf16 in dim order, exact
+__device__ __forceinline__ uint4 fp4x8_to_bf16(uint32_t w, uint32_t scale2)
+{
+    return mul_bf16x8(mul_bf16x8(fp4x8_small(w), 0x7E807E80u), scale2);  // by 2^126 first
+}
+
+// As matrix operands the rows are held times 2^-80: then 2^126 and the scale are one
+// factor, 2^(e - 81), a bf16 for e <= 208 (values to 2^83; above, it is infinite, as
+// it is for e = 255).  What becomes subnormal was below 2^-46, far under the fp32
+// rounding of any sum with a normalised row.  Products take the 2^80 back in fp32.
+constexpr float kOperandUnit = 0x1p80f;
+
+__device__ __forceinline__ uint32_t fp4_operand_scale(uint32_t e)
+{
+    return (e > 208u ? 0x7F80u : (e + 46u) << 7) * 0x00010001u;
+}
+
+constexpr uint32_t kRopeToOperand = 0x17801780u;  // bf16x2 (2^-80, 2^-80)
 
 }  // namespace
 }  // namespace dsv4

@@ -12,12 +12,12 @@
 //    transposed, S^T[key, row] = K q^T, and so are the outputs, O^T[dim, row] =
 //    K^T P^T: keys and dims take the 128 lanes of the tensor memory, so any number
 //    of rows up to 64 costs in proportion (N = 16, 32, 48, 64), and O^T of 512
-//    dims (4 x 64 columns) fits beside S^T.
+//    dims (4 x 64 columns) fits beside S^T.  Rows are held times 2^-80 (fp4.cuh).
 //  * One converted tile serves both products: K-major as the left operand of the
-//    first, read across (MN-major) as that of the second.  It is held in 8 chunks
-//    of 64 dims, each filled, and freed by the second product, on its own, so
-//    the next tile is converted under the products of this one.
-//  * Warps 8..15 convert, one thread of warp 16 issues the products, warps 0..7
+//    first, read across (MN-major) as that of the second.  It is held in 4 pairs
+//    of chunks of 64 dims, each filled, and freed by the second product, on its
+//    own, so the next tile is converted under the products of this one.
+//  * Warps 8..15 convert, warp 16 issues the products, warps 0..7
 //    do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
 //    32 (w / 4)..; a thread has one key and 32 rows.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the
@@ -77,7 +77,7 @@ constexpr uint32_t kProbs = kQuery + kChunks * kRows * 128;    // P^T: 128 keys 
 constexpr uint32_t kShared = kProbs + kTileKeys * 128;
 
 struct Shared {
-    uint64_t full[kChunks], free[kChunks / 2];
+    uint64_t full[kChunks / 2], free[kChunks / 2];  // of a pair of chunks
     uint64_t scores, probs, query, query_free, output;
     uint32_t tmem;
     int scratch[18];
@@ -143,24 +143,33 @@ __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor 
             }
             ++segment;
         }
-        const auto chunk = [&](auto self, auto ci) {
-            constexpr int i = decltype(ci)::value;
-            if (i % 2 == 0 && t > 0 && alive)
-                alive = __all_sync(kFull, mbar_wait(&s.free[i / 2], (t - 1) & 1));
+        const auto pair = [&](auto ci) {
+            constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1
+            if (t > 0 && alive)
+                alive = __all_sync(kFull, mbar_wait(&s.free[i], (t - 1) & 1));
             if (!alive)
                 return;
             if (i == 0 && half == 0)
                 s.key_ok[key] = ok ? 1 : 0;
-            convert_chunk<i>(raw, smem + kKeys + i * kChunkBytes, key, half);
-            load_chunk<i>(p, raw, row, half);
+            convert_chunk<2 * i>(raw, smem + kKeys + 2 * i * kChunkBytes, key, half);
+            convert_chunk<2 * i + 1>(raw, smem + kKeys + (2 * i + 1) * kChunkBytes, key, half);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&s.full[i]);
-            if constexpr (i < kChunks - 1)
-                self(self, std::integral_constant<int, i + 1>{});
         };
-        chunk(chunk, std::integral_constant<int, 0>{});
+        pair(std::integral_constant<int, 0>{});
+        pair(std::integral_constant<int, 1>{});
+        load_chunk<0>(p, raw, row, half);
+        load_chunk<1>(p, raw, row, half);
+        load_chunk<2>(p, raw, row, half);
+        load_chunk<3>(p, raw, row, half);
+        pair(std::integral_constant<int, 2>{});
+        pair(std::integral_constant<int, 3>{});
+        load_chunk<4>(p, raw, row, half);
+        load_chunk<5>(p, raw, row, half);
+        load_chunk<6>(p, raw, row, half);
+        load_chunk<7>(p, raw, row, half);
         if (!alive) {
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
             return;
@@ -172,11 +181,15 @@ __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor 
     }
 }
 
-// ---- One thread of warp 16: the products
+// ---- Warp 16: the products
 
 __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
+    const uint32_t elected = elect_one();
     const uint32_t d_scores = s.tmem, d_output = s.tmem + kRows;
+    const Operand keys = operand(smem + kKeys, 16, 1024), query = operand(smem + kQuery, 16, 1024);
+    const Operand values = operand(smem + kKeys, kChunkBytes, 1024);
+    const Operand probs = operand(smem + kProbs, kChunkBytes, 1024);
     uint32_t scores_inst = 0, output_inst = 0;
     int segment = 0;
     bool first = true;  // of its segment
@@ -185,41 +198,43 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
             const uint32_t n = uint32_t((c.row1 - c.row0 + 15) & ~15);
             scores_inst = instruction(n, false);
             output_inst = instruction(n, true);
-            if (!mbar_wait(&s.query, segment & 1))
+            if (!__all_sync(kFull, mbar_wait(&s.query, segment & 1)))
                 break;
             ++segment;
         }
         const bool last = c.ends_segment();
         bool alive = true;
-        for (int i = 0; i < kChunks && alive; ++i) {
-            alive = mbar_wait(&s.full[i], t & 1);
-            tmem_fence_after();
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            if (i % 2 == 0) {
+                alive = alive && __all_sync(kFull, mbar_wait(&s.full[i / 2], t & 1));
+                if (!alive)
+                    break;
+                tmem_fence_after();
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (alive)
-                    mma_bf16(d_scores, operand(smem + kKeys + i * kChunkBytes + 32 * k, 16, 1024),
-                             operand(smem + kQuery + i * kRows * 128 + 32 * k, 16, 1024), scores_inst,
-                             i > 0 || k > 0);
+                mma_bf16(d_scores, keys + (i * kChunkBytes + 32 * k), query + (i * kRows * 128 + 32 * k),
+                         scores_inst, i > 0 || k > 0, elected);
         }
         if (!alive)
             break;
-        mma_commit(&s.scores);
+        mma_commit(&s.scores, elected);
         if (last)
-            mma_commit(&s.query_free);
-        if (!mbar_wait(&s.probs, t & 1))
+            mma_commit(&s.query_free, elected);
+        if (!__all_sync(kFull, mbar_wait(&s.probs, t & 1)))
             break;
         tmem_fence_after();
+#pragma unroll
         for (int i = 0; i < kChunks / 2; ++i) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                mma_bf16(d_output + i * kRows,
-                         operand(smem + kKeys + 2 * i * kChunkBytes + 2048 * k, kChunkBytes, 1024),
-                         operand(smem + kProbs + 2048 * k, kChunkBytes, 1024), output_inst,
-                         !first || k > 0);
-            mma_commit(&s.free[i]);
+                mma_bf16(d_output + i * kRows, values + (2 * i * kChunkBytes + 2048 * k),
+                         probs + 2048 * k, output_inst, !first || k > 0, elected);
+            mma_commit(&s.free[i], elected);
         }
         if (last)
-            mma_commit(&s.output);
+            mma_commit(&s.output, elected);
         first = last;
         c.advance(p);
     }
@@ -308,7 +323,7 @@ __device__ __forceinline__ float finish(float m, float sum, float sink, float *l
     }
     const float w = exp2_approx(m - top), total = sum * w + exp2_approx(sink - top);
     *lse = (top + log2f(total)) * kLn2;
-    return w / total;
+    return w / total * kOperandUnit;
 }
 
 __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor c)
@@ -318,7 +333,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
     const int key = warp * 32 + lane, col0 = group * 32;
     const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
-    const float scale = a.scale * kLog2e;
+    const float scale = a.scale * (kLog2e * kOperandUnit);
     float sum[32];
     bool first = true;
     int segment = 0, from_tile = 0;
@@ -489,10 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     if (warp == 16) {
         tmem_alloc512(&s.tmem);
         if ((threadIdx.x & 31) == 0) {
-            for (int i = 0; i < kChunks; ++i)
+            for (int i = 0; i < kChunks / 2; ++i) {
                 mbar_init(&s.full[i], 8);
-            for (int i = 0; i < kChunks / 2; ++i)
                 mbar_init(&s.free[i], 1);
+            }
             mbar_init(&s.scores, 1);
             mbar_init(&s.probs, 8);
             mbar_init(&s.query, 8);
@@ -509,9 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     } else if (warp < 16) {
         convert_role(p, s, smem, c);
     } else {
-        if ((threadIdx.x & 31) == 0)
-            multiply_role(p, s, smem_addr(smem), c);
-        __syncwarp();
+        multiply_role(p, s, smem_addr(smem), c);
     }
     tmem_fence_before();
     __syncthreads();

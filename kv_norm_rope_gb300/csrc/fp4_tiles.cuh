@@ -195,8 +195,10 @@ __device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratc
 //
 // 256 threads: thread i owns half (i & 1) of each chunk of key i / 2 of a tile,
 // that is one scale group (16 bytes of codes) of chunks 0..6 and 64 bytes of rope
-// in chunk 7.  The raw bytes of the next tile are loaded as soon as those of this
-// one are converted, so a whole tile (45 KB) is in flight per CTA.
+// in chunk 7.  The raw bytes of the next tile's chunks 0..3 are loaded as soon as
+// this tile's are converted, and so are those of chunks 4..7, so a whole tile
+// (45 KB) is in flight per CTA.  (Loaded chunk by chunk, each conversion waited for
+// the loads just issued: a warp has few scoreboards, and they were shared.)
 
 struct RawTile {
     uint4 codes[7], rope[4], scales;
@@ -251,14 +253,16 @@ __device__ __forceinline__ void convert_chunk(const RawTile &t, uint8_t *chunk, 
     if constexpr (c == 7) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) = t.rope[i];
+            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) =
+                mul_bf16x8(t.rope[i], kRopeToOperand);
     } else {
         const uint32_t four = c < 2 ? t.scales.x : c < 4 ? t.scales.y : c < 6 ? t.scales.z : t.scales.w;
-        const uint32_t scale2 = fp4_scale_bf16x2((four >> (16 * (c & 1) + 8 * half)) & 255u);
+        const uint32_t scale2 = fp4_operand_scale((four >> (16 * (c & 1) + 8 * half)) & 255u);
         const uint32_t w[4] = {t.codes[c].x, t.codes[c].y, t.codes[c].z, t.codes[c].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) = fp4x8_to_bf16(w[i], scale2);
+            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) =
+                mul_bf16x8(fp4x8_small(w[i]), scale2);
     }
 }
 

@@ -47,13 +47,22 @@ __device__ __forceinline__ void tmem_fence_after()
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// Descriptor of a swizzled operand.  K-major: `stride` is the distance of the
-// 8-row groups.  MN-major: `stride` is that of the 8-row groups along the inner
-// dimension, `lead` that of the blocks of 64 outer elements.
-__device__ __forceinline__ uint64_t operand(uint32_t address, uint32_t lead, uint32_t stride)
+// Descriptor of a swizzled operand: `low` has the address, `high` the stride.
+// K-major: `stride` is the distance of the 8-row groups.  MN-major: `stride` is that
+// of the 8-row groups along the inner dimension, `lead` that of the blocks of 64
+// outer elements.  Addresses are below 2^18, so adding bytes / 16 to `low` moves it.
+struct Operand {
+    uint32_t low, high;
+};
+
+__device__ __forceinline__ Operand operand(uint32_t address, uint32_t lead, uint32_t stride)
 {
-    return uint64_t((address & 0x3ffffu) >> 4) | (uint64_t(lead >> 4) << 16) |
-           (uint64_t(stride >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+    return Operand{(address >> 4) | (lead >> 4 << 16), (stride >> 4) | (1u << 14) | (2u << 29)};
+}
+
+__device__ __forceinline__ Operand operator+(Operand o, uint32_t bytes)
+{
+    return Operand{o.low + (bytes >> 4), o.high};
 }
 
 // Instruction descriptor: bf16 operands, fp32 accumulator, M = 128, N = n;
@@ -64,21 +73,39 @@ __device__ __forceinline__ uint32_t instruction(uint32_t n, bool across)
            ((128u >> 4) << 24);
 }
 
-// d[128, n] (+)= a[128, 16] b[16, n]; one thread issues it
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t inst,
-                                         bool accumulate)
+// The matrix instructions take their operands from uniform registers, so a whole
+// warp runs the code that issues them, with values the same in every lane, and
+// one elected lane issues: `elected` is 1 there.  (Issued from a branch that only
+// one lane takes, each cost 110 cycles of moving descriptors, three times what the
+// product takes.)
+__device__ __forceinline__ uint32_t elect_one()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(inst), "r"(accumulate ? 1u : 0u)
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(e));
+    return e;
+}
+
+// d[128, n] (+)= a[128, 16] b[16, n]
+__device__ __forceinline__ void mma_bf16(uint32_t d, Operand a, Operand b, uint32_t inst,
+                                         bool accumulate, uint32_t elected)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
+                 "setp.ne.u32 p, %6, 0;\n\tsetp.ne.u32 e, %7, 0;\n\t"
+                 "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+                 "r"(a.low), "r"(a.high), "r"(b.low), "r"(b.high), "r"(inst),
+                 "r"(accumulate ? 1u : 0u), "r"(elected)
                  : "memory");
 }
 
-// arrive on *bar once every matrix instruction this thread has issued is done
-__device__ __forceinline__ void mma_commit(uint64_t *bar)
+// arrive on *bar once every matrix instruction the elected lane has issued is done
+__device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t elected)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_addr(bar))
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::
+                     "r"(smem_addr(bar)),
+                 "r"(elected)
                  : "memory");
 }
 
