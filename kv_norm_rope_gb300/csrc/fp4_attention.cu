@@ -17,9 +17,9 @@
 //    first, read across (MN-major) as that of the second.  It is held in 4 pairs
 //    of chunks of 64 dims, each filled, and freed by the second product, on its
 //    own, so the next tile is converted under the products of this one.
-//  * Warps 8..15 convert, warp 16 issues the products, warps 0..7
-//    do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
-//    32 (w / 4)..; a thread has one key and 32 rows.
+//  * Warps 16..23 convert, warp 24 issues the products, warps 0..15 do the softmax:
+//    warp w has the keys of lanes 32 (w % 4).. and rows 16 (w / 4)..; a thread has
+//    one key and 16 rows.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the
 //    largest score of the first tile it saw; p = 2^(x - m) is taken against that,
 //    and only when some x exceeds m by more than kSlack is m moved and everything
@@ -45,7 +45,10 @@ namespace dsv4 {
 namespace {
 
 constexpr int kRows = 64;            // query rows of a CTA
-constexpr int kThreads = 17 * 32;
+constexpr int kGroups = 4;           // of 4 softmax warps
+constexpr int kCols = kRows / kGroups;
+constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 8;
+constexpr int kThreads = (kMultiplyWarp + 1) * 32;
 constexpr int kMaxCtas = 256;        // of a launch: what the workspace is for
 constexpr float kSlack = 16.0f;
 constexpr float kUnset = -1e30f;     // m of a row that has seen no key
@@ -74,7 +77,8 @@ __device__ __forceinline__ Span partial_span(const WParams &w)
 constexpr uint32_t kKeys = 0;                                  // 8 chunks of a converted tile
 constexpr uint32_t kQuery = kKeys + kChunks * kChunkBytes;     // 8 chunks of 64 rows
 constexpr uint32_t kProbs = kQuery + kChunks * kRows * 128;    // P^T: 128 keys of 64 rows
-constexpr uint32_t kShared = kProbs + kTileKeys * 128;
+constexpr uint32_t kRing = kProbs + kTileKeys * 128;            // codes on their way: 2 slots
+constexpr uint32_t kShared = kRing + 2 * kRingSlot;
 
 struct Shared {
     uint64_t full[kChunks / 2], free[kChunks / 2];  // of a pair of chunks
@@ -83,11 +87,12 @@ struct Shared {
     int scratch[18];
     alignas(16) float m[kRows];
     alignas(16) float factor[kRows];
-    float sum[4][kRows], top[4][kRows];
+    float warp_rows[4][kRows];  // maxima or sums of the four warps' keys
     int seen_to[kRows], seen_from[kRows];
+    uint32_t block[kTileKeys];
     uint8_t key_ok[kTileKeys];
 };
-constexpr size_t kSmemBytes = 1024 + kShared + sizeof(Shared);
+constexpr size_t kSmemBytes = kShared + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "too much shared memory");
 
 // monotone map of a float to an int, for integer maxima; NaN counts as -infinity
@@ -101,31 +106,27 @@ __device__ __forceinline__ float unordered(int i)
     return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
-// ---- Warps 8..15: cache rows and queries into operands
+// ---- Warps 16..23: cache rows and queries into operands
 
 __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c)
 {
-    const int tid = threadIdx.x - 256, key = tid >> 1, half = tid & 1, lane = tid & 31;
+    const int tid = threadIdx.x - kConvertWarp * 32, key = tid >> 1, half = tid & 1, lane = tid & 31;
     const int count = c.left;
+    const uint32_t ring = smem_addr(smem + kRing), block = smem_addr(&s.block[key]);
     KeyPlace now = key_place(p, c, true, key);
-    Fp4Row row = row_at(p, now);
-    RawTile raw;
-    const auto load_all = [&](auto self, auto ci) {
-        constexpr int i = decltype(ci)::value;
-        load_chunk<i>(p, raw, row, half);
-        if constexpr (i < kChunks - 1)
-            self(self, std::integral_constant<int, i + 1>{});
-    };
-    load_all(load_all, std::integral_constant<int, 0>{});
-    raw.scales = load_raw(p, row.scale, row.data != nullptr);
-    bool ok = row.data != nullptr;
+    Fp4Row row = row_at(p, now, now.entry != nullptr ? ldg4_in(now.entry, table_span(p.a.b), p.a.b.err) : 0u);
+    copy_step<0>(p, ring, tid, row, row, nullptr, block);
+    copy_step<1>(p, ring, tid, row, row, nullptr, block);
+    uint4 scales = row.data != nullptr ? ldg16_in(row.scale, cache_span(p.a.b), p.a.b.err)
+                                       : make_uint4(0u, 0u, 0u, 0u);
     bool moved = c.advance(p);
     KeyPlace next = key_place(p, c, moved, key);
+    uint32_t next_block = next.entry != nullptr ? ldg4_in(next.entry, table_span(p.a.b), p.a.b.err) : 0u;
     int segment = 0;
     for (int t = 0; t < count; ++t) {
-        row = row_at(p, next);
-        const uint4 next_scales = load_raw(p, row.scale, row.data != nullptr);
+        const Fp4Row next_row = row_at(p, next, next_block);
         KeyPlace after = next;
+        after.entry = nullptr;
         if (c.left > 0) {
             moved = c.advance(p);
             after = key_place(p, c, moved, key);
@@ -143,16 +144,56 @@ __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor 
             }
             ++segment;
         }
+        uint4 next_scales = scales;
+        // step j: its bytes out of the ring, the copies two steps on
+        const auto take = [&](auto cj, uint4 &first, uint4 &second) {
+            constexpr int j = decltype(cj)::value;
+            const uint8_t *from = smem + kRing + (j & 1) * kRingSlot;
+            copy_wait_but_one();
+            first = *reinterpret_cast<const uint4 *>(from + tid * 16);
+            second = *reinterpret_cast<const uint4 *>(from + 4096 + tid * 16);
+            if constexpr (j == 3) {
+                next_scales = second;
+                // the copy was the even thread's
+                next_block = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t *>(&s.block[key]), lane & ~1);
+            }
+            computed(first);
+            computed(second);
+            if constexpr (j + 2 < kSteps)
+                copy_step<j + 2>(p, ring, tid, row, next_row, after.entry, block);
+            else
+                copy_step<j + 2 - kSteps>(p, ring, tid, next_row, next_row, nullptr, block);
+        };
         const auto pair = [&](auto ci) {
             constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1
+            uint8_t *to = smem + kKeys + 2 * i * kChunkBytes;
+            uint4 a, b, out[8];
+            take(ci, a, b);
+            convert_codes<2 * i>(scales, a, half, out);
+            if constexpr (i < 3) {
+                convert_codes<2 * i + 1>(scales, b, half, out + 4);
+            } else {
+                take(std::integral_constant<int, 4>{}, a, b);
+                out[4] = mul_bf16x8(a, kRopeToOperand);
+                out[5] = mul_bf16x8(b, kRopeToOperand);
+                take(std::integral_constant<int, 5>{}, a, b);
+                out[6] = mul_bf16x8(a, kRopeToOperand);
+                out[7] = mul_bf16x8(b, kRopeToOperand);
+            }
+            // converted before the wait for the place
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                computed(out[k]);
             if (t > 0 && alive)
                 alive = __all_sync(kFull, mbar_wait(&s.free[i], (t - 1) & 1));
             if (!alive)
                 return;
             if (i == 0 && half == 0)
-                s.key_ok[key] = ok ? 1 : 0;
-            convert_chunk<2 * i>(raw, smem + kKeys + 2 * i * kChunkBytes, key, half);
-            convert_chunk<2 * i + 1>(raw, smem + kKeys + (2 * i + 1) * kChunkBytes, key, half);
+                s.key_ok[key] = row.data != nullptr ? 1 : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4 *>(to + (k >> 2) * kChunkBytes + swizzled(key, half * 4 + (k & 3))) =
+                    out[k];
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
@@ -160,28 +201,21 @@ __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor 
         };
         pair(std::integral_constant<int, 0>{});
         pair(std::integral_constant<int, 1>{});
-        load_chunk<0>(p, raw, row, half);
-        load_chunk<1>(p, raw, row, half);
-        load_chunk<2>(p, raw, row, half);
-        load_chunk<3>(p, raw, row, half);
         pair(std::integral_constant<int, 2>{});
         pair(std::integral_constant<int, 3>{});
-        load_chunk<4>(p, raw, row, half);
-        load_chunk<5>(p, raw, row, half);
-        load_chunk<6>(p, raw, row, half);
-        load_chunk<7>(p, raw, row, half);
         if (!alive) {
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
-            return;
+            break;
         }
-        raw.scales = next_scales;
-        ok = row.data != nullptr;
+        scales = next_scales;
+        row = next_row;
         now = next;
         next = after;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// ---- Warp 16: the products
+// ---- Warp 24: the products
 
 __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
@@ -242,7 +276,7 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
 
-// ---- Warps 0..7: softmax and results
+// ---- Warps 0..15: softmax and results
 
 // Move the references of a warpgroup's rows up to the scores x of this tile and
 // rescale what was taken against the old ones.
@@ -250,48 +284,49 @@ __device__ __forceinline__ void move_references(Shared &s, const float *x, float
                                                 bool rescale_output)
 {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
-    const int col0 = group * 32;
+    const int col0 = group * kCols;
     int mine = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < kCols; ++j) {
         const int top = __reduce_max_sync(kFull, ordered(x[j]));
         if (lane == j)
             mine = top;
     }
-    s.top[warp][col0 + lane] = unordered(mine);
+    if (lane < kCols)
+        s.warp_rows[warp][col0 + lane] = unordered(mine);
     named_barrier(1 + group, 128);
-    if (warp == 0) {
+    if (warp == 0 && lane < kCols) {
         const int j = col0 + lane;
         const float old = s.m[j];
-        const float m = fmaxf(fmaxf(old, fmaxf(s.top[0][j], s.top[1][j])), fmaxf(s.top[2][j], s.top[3][j]));
+        const float m = fmaxf(fmaxf(old, fmaxf(s.warp_rows[0][j], s.warp_rows[1][j])),
+                              fmaxf(s.warp_rows[2][j], s.warp_rows[3][j]));
         s.m[j] = m;
         s.factor[j] = exp2_approx(old - m);
     }
     named_barrier(1 + group, 128);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
+    for (int j = 0; j < kCols; ++j)
         sum[j] *= s.factor[col0 + j];
     if (rescale_output) {
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t at = tmem + kRows + (i >> 1) * kRows + col0 + (i & 1) * 16;
-            float o[16];
-            tmem_load16(at, o);
+        for (int i = 0; i < 4; ++i) {
+            float o[kCols];
+            tmem_load16(tmem + kRows + i * kRows + col0, o);
             tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                o[j] *= s.factor[col0 + (i & 1) * 16 + j];
-            tmem_store16(at, o);
+            for (int j = 0; j < kCols; ++j)
+                o[j] *= s.factor[col0 + j];
+            tmem_store16(tmem + kRows + i * kRows + col0, o);
         }
         tmem_wait_store();
     }
 }
 
-// sums of 32 values over the 32 lanes of a warp: lane j returns that of v[j]
+// sums of 16 values over the 32 lanes of a warp: lanes j and 16 + j return that of v[j]
 __device__ __forceinline__ float transposed_sum(float *v, int lane)
 {
 #pragma unroll
-    for (int half = 16; half >= 1; half >>= 1) {
+    for (int half = 8; half >= 1; half >>= 1) {
         const bool upper = (lane & half) != 0;
 #pragma unroll
         for (int j = 0; j < half; ++j) {
@@ -300,7 +335,7 @@ __device__ __forceinline__ float transposed_sum(float *v, int lane)
             v[j] = keep + __shfl_xor_sync(kFull, give, half);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(kFull, v[0], 16);
 }
 
 __device__ __forceinline__ float sink_of(const Fp4AttentionArgs &a, int row)
@@ -331,17 +366,17 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
     const AParams &p = w.p;
     const Fp4AttentionArgs &a = p.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
-    const int key = warp * 32 + lane, col0 = group * 32;
+    const int key = warp * 32 + lane, col0 = group * kCols;
     const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
     const float scale = a.scale * (kLog2e * kOperandUnit);
-    float sum[32];
+    float sum[kCols];
     bool first = true;
     int segment = 0, from_tile = 0;
     for (uint32_t t = 0; c.left > 0; ++t) {
         const int row0 = c.row0, rows = c.row1 - c.row0;
         if (first) {
             from_tile = c.tile;
-            if (warp == 0) {
+            if (warp == 0 && lane < kCols) {
                 const int r = col0 + lane;
                 const int to = r < rows ? c.n - a.q_len + 1 + (row0 + r) / a.heads : 0;
                 s.seen_to[r] = to;
@@ -350,7 +385,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             }
             named_barrier(1 + group, 128);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < kCols; ++j)
                 sum[j] = 0.0f;
         }
         const bool last = c.ends_segment();
@@ -359,17 +394,17 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
         const int i = c.tile * kTileKeys + key;
         // every row of the group sees every key of the tile: the first row sees the
         // fewest at the end, the last one the fewest at the start
-        const bool whole = rows >= col0 + 32 && (c.tile + 1) * kTileKeys <= s.seen_to[col0] &&
-                           c.tile * kTileKeys >= s.seen_from[col0 + 31];
+        const bool whole = rows >= col0 + kCols && (c.tile + 1) * kTileKeys <= s.seen_to[col0] &&
+                           c.tile * kTileKeys >= s.seen_from[col0 + kCols - 1];
         const bool ok = s.key_ok[key] != 0;
-        float v[32];
+        float v[kCols];
         // v = the scores less `reference` (a row each; null: none), -infinity where unseen
         const auto load_scores = [&](const float *reference) {
             __syncwarp();
-            tmem_load32(tmem + col0, v);
+            tmem_load16(tmem + col0, v);
             tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
+            for (int j = 0; j < kCols; j += 4) {
                 const float4 m = reference != nullptr
                                      ? *reinterpret_cast<const float4 *>(reference + col0 + j)
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -380,20 +415,20 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             }
             if (!whole) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < kCols; ++j)
                     if (i >= s.seen_to[col0 + j] || i < s.seen_from[col0 + j])
                         v[j] = -INFINITY;
             }
             if (!ok) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < kCols; ++j)
                     v[j] = -INFINITY;
             }
         };
         load_scores(s.m);
         float over = v[0];
 #pragma unroll
-        for (int j = 1; j < 32; ++j)
+        for (int j = 1; j < kCols; ++j)
             over = fmaxf(over, v[j]);
         if (named_barrier_any(1 + group, 128, failed || over > kSlack)) {
             if (named_barrier_any(1 + group, 128, failed)) {
@@ -404,17 +439,17 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             move_references(s, v, sum, tmem, !first);
             load_scores(s.m);
         }
-        uint32_t packed[16];
+        uint32_t packed[kCols / 2];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = 0; j < kCols; j += 2) {
             const float p0 = exp2_approx(v[j]), p1 = exp2_approx(v[j + 1]);
             sum[j] += p0;
             sum[j + 1] += p1;
             packed[j / 2] = bf16x2_rn(p0, p1);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4 *>(smem + kProbs + swizzled(key, group * 4 + k)) =
+        for (int k = 0; k < kCols / 8; ++k)
+            *reinterpret_cast<uint4 *>(smem + kProbs + swizzled(key, group * (kCols / 8) + k)) =
                 make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
         fence_proxy_async_smem();
         tmem_fence_before();
@@ -423,7 +458,9 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             mbar_arrive(&s.probs);
         if (last) {
             // the segment's result
-            s.sum[warp][col0 + lane] = transposed_sum(sum, lane);
+            const float key_sum = transposed_sum(sum, lane);
+            if (lane < kCols)
+                s.warp_rows[warp][col0 + lane] = key_sum;
             failed = !mbar_wait(&s.output, segment & 1);
             ++segment;
             if (named_barrier_any(1 + group, 128, failed)) {
@@ -432,13 +469,14 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             }
             tmem_fence_after();
             const bool whole_range = from_tile == c.range.first() && c.tile + 1 == c.range.stop();
-            const int r = col0 + lane;
-            float total = (s.sum[0][r] + s.sum[1][r]) + (s.sum[2][r] + s.sum[3][r]);
+            const int r = col0 + (lane & (kCols - 1));
+            const float total = (s.warp_rows[0][r] + s.warp_rows[1][r]) +
+                                (s.warp_rows[2][r] + s.warp_rows[3][r]);
             const int64_t out_row = int64_t(c.request(p)) * p.all_rows + row0;
             // the run's first segment or its last
             float *part = partial_at(w, blockIdx.x, t + 1 == uint32_t(c.tile + 1 - from_tile) ? 0 : 1);
             const Span ps = partial_span(w);
-            if (warp == 0) {
+            if (warp == 0 && lane < kCols) {
                 if (whole_range) {
                     float lse = 0.0f;
                     if (r < rows)
@@ -452,12 +490,12 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             }
             named_barrier(1 + group, 128);
             const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
-            const int mine = rows - col0 < 32 ? rows - col0 : 32;
+            const int mine = rows - col0 < kCols ? rows - col0 : kCols;
             if (mine > 0) {
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
-                    float o[32];
-                    tmem_load32(tmem + kRows + k * kRows + col0, o);
+                    float o[kCols];
+                    tmem_load16(tmem + kRows + k * kRows + col0, o);
                     tmem_wait_load();
                     const int dim = k * 128 + key;
                     if (whole_range) {
@@ -465,7 +503,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
                         const int odd = lane & 1;
                         uint16_t *to = a.out + (out_row + col0 + odd) * DSV4_HEAD_DIM + (dim - odd);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
+                        for (int j = 0; j < kCols; j += 2) {
                             const float o0 = o[j] * s.factor[col0 + j];
                             const float o1 = o[j + 1] * s.factor[col0 + j + 1];
                             const float other = __shfl_xor_sync(kFull, odd ? o0 : o1, 1);
@@ -476,7 +514,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
                     } else {
                         float *to = part + col0 * DSV4_HEAD_DIM + dim;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < kCols; ++j)
                             if (j < mine)
                                 st_f32_in(to + j * DSV4_HEAD_DIM, o[j], ps, a.b.err);
                     }
@@ -492,8 +530,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
 
 __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid_constant__ WParams w)
 {
-    extern __shared__ uint8_t raw_smem[];
-    uint8_t *smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem + kShared);
     const AParams &p = w.p;
     const int warp = threadIdx.x >> 5;
@@ -501,7 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     deal(p, blockIdx.x, gridDim.x, s.scratch, c);
     if (c.left == 0)
         return;
-    if (warp == 16) {
+    if ((smem_addr(smem) & 1023u) != 0u) {  // never: there is no static shared memory
+        flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+        return;
+    }
+    if (warp == kMultiplyWarp) {
         tmem_alloc512(&s.tmem);
         if ((threadIdx.x & 31) == 0) {
             for (int i = 0; i < kChunks / 2; ++i) {
@@ -509,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
                 mbar_init(&s.free[i], 1);
             }
             mbar_init(&s.scores, 1);
-            mbar_init(&s.probs, 8);
+            mbar_init(&s.probs, kConvertWarp);
             mbar_init(&s.query, 8);
             mbar_init(&s.query_free, 1);
             mbar_init(&s.output, 1);
@@ -519,16 +560,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     }
     __syncthreads();
     tmem_fence_after();
-    if (warp < 8) {
+    if (warp < kConvertWarp) {
         softmax_role(w, s, smem, c);
-    } else if (warp < 16) {
+    } else if (warp < kMultiplyWarp) {
         convert_role(p, s, smem, c);
     } else {
         multiply_role(p, s, smem_addr(smem), c);
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == kMultiplyWarp) {
         tmem_fence_after();
         tmem_free512(s.tmem);
     }

@@ -195,21 +195,24 @@ __device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratc
 //
 // 256 threads: thread i owns half (i & 1) of each chunk of key i / 2 of a tile,
 // that is one scale group (16 bytes of codes) of chunks 0..6 and 64 bytes of rope
-// in chunk 7.  The raw bytes of the next tile's chunks 0..3 are loaded as soon as
-// this tile's are converted, and so are those of chunks 4..7, so a whole tile
-// (45 KB) is in flight per CTA.  (Loaded chunk by chunk, each conversion waited for
-// the loads just issued: a warp has few scoreboards, and they were shared.)
+// in chunk 7.  Everything comes through a ring of two slots in shared memory by
+// asynchronous copies, in six steps a tile, each issued two steps ahead into the
+// thread's own bytes:
+//   0, 1, 2: the codes of chunks 0 1, 2 3, 4 5;   4, 5: the halves of the rope dims;
+//   3: the codes of chunk 6, the scales of the next tile and the block number of the
+//      one after it (into a word of the key's own elsewhere).
+// (Held in registers instead, the loads took half as long again: a warp has six
+// scoreboards, so using one load also waited for others issued long after it.)
 
-struct RawTile {
-    uint4 codes[7], rope[4], scales;
-};
+constexpr uint32_t kRingSlot = 256 * 32;
+constexpr int kSteps = 6;
 
-// where a thread's key of a tile is; found two tiles ahead, as the block number is
-// itself loaded
+// where a thread's key of a tile is
 struct KeyPlace {
-    uint32_t entry, off;
-    bool seen, new_unit;
+    const int32_t *entry;  // its block's number; null: not seen by any row
+    uint32_t off;
     int unit;
+    bool new_unit;
 };
 
 __device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c, bool new_unit,
@@ -217,66 +220,89 @@ __device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c,
 {
     KeyPlace k;
     const int i = c.tile * kTileKeys + key;
-    k.seen = c.left > 0 && i >= c.range.lo && i < c.range.hi;
     k.new_unit = new_unit;
     k.unit = c.unit;
-    k.entry = k.off = 0u;
-    if (k.seen) {
+    k.entry = nullptr;
+    k.off = 0u;
+    if (c.left > 0 && i >= c.range.lo && i < c.range.hi) {
         const uint32_t at = fastdiv(uint32_t(i), p.block_div);
         k.off = uint32_t(i) - at * uint32_t(p.a.b.block_size);
-        k.entry = ldg4_in(p.a.b.table + c.request(p) * p.a.b.table_stride + at, table_span(p.a.b), p.a.b.err);
+        k.entry = p.a.b.table + c.request(p) * p.a.b.table_stride + at;
     }
     return k;
 }
 
-// the row of a placed key; data = null for none (not seen, or a bad block, which is flagged)
-__device__ __forceinline__ Fp4Row row_at(const AParams &p, const KeyPlace &k)
+// the row of a placed key whose block number is `block`; data = null for none (not
+// seen, or a bad block, which is flagged)
+__device__ __forceinline__ Fp4Row row_at(const AParams &p, const KeyPlace &k, uint32_t block)
 {
-    if (!k.seen)
+    if (k.entry == nullptr)
         return Fp4Row{nullptr, nullptr};
-    if (int64_t(k.entry) >= p.a.b.num_blocks) {
+    if (int64_t(block) >= p.a.b.num_blocks) {
         flag(p.a.b.err, DSV4_DEVERR_SLOT_RANGE);
         return Fp4Row{nullptr, nullptr};
     }
-    return fp4_row(p.a.b.cache, k.entry, k.off, uint32_t(p.a.b.block_size));
+    return fp4_row(p.a.b.cache, block, k.off, uint32_t(p.a.b.block_size));
 }
 
-__device__ __forceinline__ uint4 load_raw(const AParams &p, const uint8_t *at, bool ok)
+// 16 bytes to shared memory, zeros for none
+__device__ __forceinline__ void copy16(const AParams &p, uint32_t to, const uint8_t *from, bool ok)
 {
-    return ok ? ldg16_in(at, cache_span(p.a.b), p.a.b.err) : make_uint4(0u, 0u, 0u, 0u);
+    ok = ok && in_span(from, 16, cache_span(p.a.b), p.a.b.err);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(ok ? from : p.a.b.cache),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
 }
 
-// chunk c of a key's half, from its raw bytes into the operand at `chunk`
-template <int c>
-__device__ __forceinline__ void convert_chunk(const RawTile &t, uint8_t *chunk, int key, int half)
+// step j of a tile whose key is at `row`, the next tile's at `next`, the block
+// number after that at `entry`, to go to `block`
+template <int j>
+__device__ __forceinline__ void copy_step(const AParams &p, uint32_t ring, int tid, const Fp4Row &row,
+                                          const Fp4Row &next, const int32_t *entry, uint32_t block)
 {
-    if constexpr (c == 7) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) =
-                mul_bf16x8(t.rope[i], kRopeToOperand);
-    } else {
-        const uint32_t four = c < 2 ? t.scales.x : c < 4 ? t.scales.y : c < 6 ? t.scales.z : t.scales.w;
-        const uint32_t scale2 = fp4_operand_scale((four >> (16 * (c & 1) + 8 * half)) & 255u);
-        const uint32_t w[4] = {t.codes[c].x, t.codes[c].y, t.codes[c].z, t.codes[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + i)) =
-                mul_bf16x8(fp4x8_small(w[i]), scale2);
-    }
-}
-
-template <int c>
-__device__ __forceinline__ void load_chunk(const AParams &p, RawTile &t, const Fp4Row &row, int half)
-{
+    const uint32_t slot = ring + (j & 1) * kRingSlot;
+    const int half = tid & 1;
     const bool ok = row.data != nullptr;
-    if constexpr (c == 7) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            t.rope[i] = load_raw(p, row.data + kFp4Codes + 64 * half + 16 * i, ok);
+    if constexpr (j < 3) {
+        copy16(p, slot + tid * 16, row.data + 64 * j + 16 * half, ok);
+        copy16(p, slot + 4096 + tid * 16, row.data + 64 * j + 32 + 16 * half, ok);
+    } else if constexpr (j == 3) {
+        copy16(p, slot + tid * 16, row.data + 192 + 16 * half, ok);
+        copy16(p, slot + 4096 + tid * 16, next.scale, next.data != nullptr);
+        const bool known = entry != nullptr && in_span(entry, 4, table_span(p.a.b), p.a.b.err);
+        if (half == 0)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(block),
+                         "l"(known ? entry : p.a.b.table), "r"(known ? 4 : 0)
+                         : "memory");
     } else {
-        t.codes[c] = load_raw(p, row.data + 32 * c + 16 * half, ok);
+        copy16(p, slot + tid * 16, row.data + kFp4Codes + 64 * half + 32 * (j - 4), ok);
+        copy16(p, slot + 4096 + tid * 16, row.data + kFp4Codes + 64 * half + 32 * (j - 4) + 16, ok);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// all but the newest group of the thread's copies have landed
+__device__ __forceinline__ void copy_wait_but_one()
+{
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+
+// 32 codes of chunk c (the thread's half) with their scale -> 32 bf16
+template <int c>
+__device__ __forceinline__ void convert_codes(uint4 scales, uint4 codes, int half, uint4 *out)
+{
+    const uint32_t four = c < 2 ? scales.x : c < 4 ? scales.y : c < 6 ? scales.z : scales.w;
+    const uint32_t scale2 = fp4_operand_scale((four >> (16 * (c & 1) + 8 * half)) & 255u);
+    out[0] = mul_bf16x8(fp4x8_small(codes.x), scale2);
+    out[1] = mul_bf16x8(fp4x8_small(codes.y), scale2);
+    out[2] = mul_bf16x8(fp4x8_small(codes.z), scale2);
+    out[3] = mul_bf16x8(fp4x8_small(codes.w), scale2);
+}
+
+// keeps values from being computed later than here
+__device__ __forceinline__ void computed(uint4 &v)
+{
+    asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
 }
 
 // The query rows of a unit into the K-major operand of `rows` rows (chunk j: dims
