@@ -17,9 +17,9 @@
 //    first, read across (MN-major) as that of the second.  It is held in 4 pairs
 //    of chunks of 64 dims, each filled, and freed by the second product, on its
 //    own, so the next tile is converted under the products of this one.
-//  * Warps 16..23 convert, warp 24 issues the products, warps 0..15 do the softmax:
-//    warp w has the keys of lanes 32 (w % 4).. and rows 16 (w / 4)..; a thread has
-//    one key and 16 rows.
+//  * Warps 0..7 do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
+//    32 (w / 4)..; a thread has one key and 32 rows.  Warps 8..23 convert, warp 24
+//    issues the products.  Registers move from the converting warps to the softmax's.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the
 //    largest score of the first tile it saw; p = 2^(x - m) is taken against that,
 //    and only when some x exceeds m by more than kSlack is m moved and everything
@@ -45,10 +45,14 @@ namespace dsv4 {
 namespace {
 
 constexpr int kRows = 64;            // query rows of a CTA
-constexpr int kGroups = 4;           // of 4 softmax warps
+constexpr int kGroups = 2;           // of 4 softmax warps
 constexpr int kCols = kRows / kGroups;
-constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 8;
-constexpr int kThreads = (kMultiplyWarp + 1) * 32;
+constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
+constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three warps idle
+// registers a thread: 72 at launch (896 * 72 = 64512), then
+constexpr int kSoftmaxRegs = 96, kConvertRegs = 64, kMultiplyRegs = 56;
+static_assert(128 * (kGroups * kSoftmaxRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
+              "the shares exceed what the CTA was launched with");
 constexpr int kMaxCtas = 256;        // of a launch: what the workspace is for
 constexpr float kSlack = 16.0f;
 constexpr float kUnset = -1e30f;     // m of a row that has seen no key
@@ -77,7 +81,7 @@ __device__ __forceinline__ Span partial_span(const WParams &w)
 constexpr uint32_t kKeys = 0;                                  // 8 chunks of a converted tile
 constexpr uint32_t kQuery = kKeys + kChunks * kChunkBytes;     // 8 chunks of 64 rows
 constexpr uint32_t kProbs = kQuery + kChunks * kRows * 128;    // P^T: 128 keys of 64 rows
-constexpr uint32_t kRing = kProbs + kTileKeys * 128;            // codes on their way: 2 slots
+constexpr uint32_t kRing = kProbs + kTileKeys * 128;            // a slot of codes for each team
 constexpr uint32_t kShared = kRing + 2 * kRingSlot;
 
 struct Shared {
@@ -89,7 +93,6 @@ struct Shared {
     alignas(16) float factor[kRows];
     float warp_rows[4][kRows];  // maxima or sums of the four warps' keys
     int seen_to[kRows], seen_from[kRows];
-    uint32_t block[kTileKeys];
     uint8_t key_ok[kTileKeys];
 };
 constexpr size_t kSmemBytes = kShared + sizeof(Shared);
@@ -106,22 +109,23 @@ __device__ __forceinline__ float unordered(int i)
     return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
-// ---- Warps 16..23: cache rows and queries into operands
+// ---- Warps 8..23: cache rows and queries into operands
 
-__device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c)
+template <int team>
+__device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c)
 {
-    const int tid = threadIdx.x - kConvertWarp * 32, key = tid >> 1, half = tid & 1, lane = tid & 31;
+    const int tid = threadIdx.x - kConvertWarp * 32 - team * kTeam;
+    const int key = tid >> 1, half = tid & 1, lane = tid & 31;
     const int count = c.left;
-    const uint32_t ring = smem_addr(smem + kRing), block = smem_addr(&s.block[key]);
+    const uint8_t *mine = smem + kRing + team * kRingSlot;
+    const uint32_t slot = smem_addr(mine);
     KeyPlace now = key_place(p, c, true, key);
-    Fp4Row row = row_at(p, now, now.entry != nullptr ? ldg4_in(now.entry, table_span(p.a.b), p.a.b.err) : 0u);
-    copy_step<0>(p, ring, tid, row, row, nullptr, block);
-    copy_step<1>(p, ring, tid, row, row, nullptr, block);
-    uint4 scales = row.data != nullptr ? ldg16_in(row.scale, cache_span(p.a.b), p.a.b.err)
-                                       : make_uint4(0u, 0u, 0u, 0u);
+    Fp4Row row = row_at(p, now, load_block(p, now));
+    copy_codes<team>(p, slot, tid, row);
+    uint4 scales = load_raw(p, row.scale, row.data != nullptr);
     bool moved = c.advance(p);
     KeyPlace next = key_place(p, c, moved, key);
-    uint32_t next_block = next.entry != nullptr ? ldg4_in(next.entry, table_span(p.a.b), p.a.b.err) : 0u;
+    uint32_t next_block = load_block(p, next);
     int segment = 0;
     for (int t = 0; t < count; ++t) {
         const Fp4Row next_row = row_at(p, next, next_block);
@@ -131,12 +135,17 @@ __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor 
             moved = c.advance(p);
             after = key_place(p, c, moved, key);
         }
+        next_block = load_block(p, after);
+        const uint4 next_scales = load_raw(p, next_row.scale, next_row.data != nullptr);
+        if constexpr (team == 1)
+            prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
         bool alive = true;
         if (now.new_unit) {
             if (segment > 0)
                 alive = __all_sync(kFull, mbar_wait(&s.query_free, (segment - 1) & 1));
             if (alive) {
-                load_query(p, now.unit, smem + kQuery, kRows, tid, 256);
+                load_query(p, now.unit / p.row_tiles, now.unit % p.row_tiles * kRows, smem + kQuery, kRows,
+                           tid + team * kTeam, 2 * kTeam);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -144,65 +153,51 @@ __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor 
             }
             ++segment;
         }
-        uint4 next_scales = scales;
-        // step j: its bytes out of the ring, the copies two steps on
-        const auto take = [&](auto cj, uint4 &first, uint4 &second) {
-            constexpr int j = decltype(cj)::value;
-            const uint8_t *from = smem + kRing + (j & 1) * kRingSlot;
-            copy_wait_but_one();
-            first = *reinterpret_cast<const uint4 *>(from + tid * 16);
-            second = *reinterpret_cast<const uint4 *>(from + 4096 + tid * 16);
-            if constexpr (j == 3) {
-                next_scales = second;
-                // the copy was the even thread's
-                next_block = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t *>(&s.block[key]), lane & ~1);
-            }
-            computed(first);
-            computed(second);
-            if constexpr (j + 2 < kSteps)
-                copy_step<j + 2>(p, ring, tid, row, next_row, after.entry, block);
-            else
-                copy_step<j + 2 - kSteps>(p, ring, tid, next_row, next_row, nullptr, block);
-        };
+        uint4 rope[4];
         const auto pair = [&](auto ci) {
             constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1
             uint8_t *to = smem + kKeys + 2 * i * kChunkBytes;
-            uint4 a, b, out[8];
-            take(ci, a, b);
+            copy_wait();
+            uint4 a = *reinterpret_cast<const uint4 *>(mine + tid * 16), b = a, out[4];
+            if constexpr (i < 3)
+                b = *reinterpret_cast<const uint4 *>(mine + 4096 + tid * 16);
+            computed(a);
+            computed(b);
+            if constexpr (i < 2)
+                copy_codes<i + 2>(p, slot, tid, row);
+            else
+                copy_codes<i - 2>(p, slot, tid, next_row);
             convert_codes<2 * i>(scales, a, half, out);
-            if constexpr (i < 3) {
-                convert_codes<2 * i + 1>(scales, b, half, out + 4);
-            } else {
-                take(std::integral_constant<int, 4>{}, a, b);
-                out[4] = mul_bf16x8(a, kRopeToOperand);
-                out[5] = mul_bf16x8(b, kRopeToOperand);
-                take(std::integral_constant<int, 5>{}, a, b);
-                out[6] = mul_bf16x8(a, kRopeToOperand);
-                out[7] = mul_bf16x8(b, kRopeToOperand);
-            }
-            // converted before the wait for the place
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                computed(out[k]);
+            for (int k = 0; k < 4; ++k)
+                computed(out[k]);  // before the wait for its place
             if (t > 0 && alive)
                 alive = __all_sync(kFull, mbar_wait(&s.free[i], (t - 1) & 1));
             if (!alive)
                 return;
             if (i == 0 && half == 0)
                 s.key_ok[key] = row.data != nullptr ? 1 : 0;
+            store_half(to, key, half, out);
+            if constexpr (i < 3) {
+                convert_codes<2 * i + 1>(scales, b, half, out);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4 *>(to + (k >> 2) * kChunkBytes + swizzled(key, half * 4 + (k & 3))) =
-                    out[k];
+                for (int k = 0; k < 4; ++k)
+                    out[k] = mul_bf16x8(rope[k], kRopeToOperand);
+            }
+            store_half(to + kChunkBytes, key, half, out);
+            if constexpr (i == 1) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    rope[k] = load_raw(p, row.data + kFp4Codes + 64 * half + 16 * k, row.data != nullptr);
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&s.full[i]);
         };
-        pair(std::integral_constant<int, 0>{});
-        pair(std::integral_constant<int, 1>{});
-        pair(std::integral_constant<int, 2>{});
-        pair(std::integral_constant<int, 3>{});
+        pair(std::integral_constant<int, team>{});
+        pair(std::integral_constant<int, team + 2>{});
         if (!alive) {
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
             break;
@@ -212,7 +207,7 @@ __device__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor 
         now = next;
         next = after;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    copy_wait();
 }
 
 // ---- Warp 24: the products
@@ -276,7 +271,7 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
 
-// ---- Warps 0..15: softmax and results
+// ---- Warps 0..7: softmax and results
 
 // Move the references of a warpgroup's rows up to the scores x of this tile and
 // rescale what was taken against the old ones.
@@ -292,10 +287,9 @@ __device__ __forceinline__ void move_references(Shared &s, const float *x, float
         if (lane == j)
             mine = top;
     }
-    if (lane < kCols)
-        s.warp_rows[warp][col0 + lane] = unordered(mine);
+    s.warp_rows[warp][col0 + lane] = unordered(mine);
     named_barrier(1 + group, 128);
-    if (warp == 0 && lane < kCols) {
+    if (warp == 0) {
         const int j = col0 + lane;
         const float old = s.m[j];
         const float m = fmaxf(fmaxf(old, fmaxf(s.warp_rows[0][j], s.warp_rows[1][j])),
@@ -309,24 +303,25 @@ __device__ __forceinline__ void move_references(Shared &s, const float *x, float
         sum[j] *= s.factor[col0 + j];
     if (rescale_output) {
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            float o[kCols];
-            tmem_load16(tmem + kRows + i * kRows + col0, o);
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = tmem + kRows + (i >> 1) * kRows + col0 + (i & 1) * 16;
+            float o[16];
+            tmem_load16(at, o);
             tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < kCols; ++j)
-                o[j] *= s.factor[col0 + j];
-            tmem_store16(tmem + kRows + i * kRows + col0, o);
+            for (int j = 0; j < 16; ++j)
+                o[j] *= s.factor[col0 + (i & 1) * 16 + j];
+            tmem_store16(at, o);
         }
         tmem_wait_store();
     }
 }
 
-// sums of 16 values over the 32 lanes of a warp: lanes j and 16 + j return that of v[j]
+// sums of 32 values over the 32 lanes of a warp: lane j returns that of v[j]
 __device__ __forceinline__ float transposed_sum(float *v, int lane)
 {
 #pragma unroll
-    for (int half = 8; half >= 1; half >>= 1) {
+    for (int half = 16; half >= 1; half >>= 1) {
         const bool upper = (lane & half) != 0;
 #pragma unroll
         for (int j = 0; j < half; ++j) {
@@ -335,7 +330,7 @@ __device__ __forceinline__ float transposed_sum(float *v, int lane)
             v[j] = keep + __shfl_xor_sync(kFull, give, half);
         }
     }
-    return v[0] + __shfl_xor_sync(kFull, v[0], 16);
+    return v[0];
 }
 
 __device__ __forceinline__ float sink_of(const Fp4AttentionArgs &a, int row)
@@ -376,7 +371,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
         const int row0 = c.row0, rows = c.row1 - c.row0;
         if (first) {
             from_tile = c.tile;
-            if (warp == 0 && lane < kCols) {
+            if (warp == 0) {
                 const int r = col0 + lane;
                 const int to = r < rows ? c.n - a.q_len + 1 + (row0 + r) / a.heads : 0;
                 s.seen_to[r] = to;
@@ -402,6 +397,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
         const auto load_scores = [&](const float *reference) {
             __syncwarp();
             tmem_load16(tmem + col0, v);
+            tmem_load16(tmem + col0 + 16, v + 16);
             tmem_wait_load();
 #pragma unroll
             for (int j = 0; j < kCols; j += 4) {
@@ -459,8 +455,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
         if (last) {
             // the segment's result
             const float key_sum = transposed_sum(sum, lane);
-            if (lane < kCols)
-                s.warp_rows[warp][col0 + lane] = key_sum;
+            s.warp_rows[warp][col0 + lane] = key_sum;
             failed = !mbar_wait(&s.output, segment & 1);
             ++segment;
             if (named_barrier_any(1 + group, 128, failed)) {
@@ -469,14 +464,14 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             }
             tmem_fence_after();
             const bool whole_range = from_tile == c.range.first() && c.tile + 1 == c.range.stop();
-            const int r = col0 + (lane & (kCols - 1));
+            const int r = col0 + lane;
             const float total = (s.warp_rows[0][r] + s.warp_rows[1][r]) +
                                 (s.warp_rows[2][r] + s.warp_rows[3][r]);
-            const int64_t out_row = int64_t(c.request(p)) * p.all_rows + row0;
+            const int64_t out_row = int64_t(c.request) * p.all_rows + row0;
             // the run's first segment or its last
             float *part = partial_at(w, blockIdx.x, t + 1 == uint32_t(c.tile + 1 - from_tile) ? 0 : 1);
             const Span ps = partial_span(w);
-            if (warp == 0 && lane < kCols) {
+            if (warp == 0) {
                 if (whole_range) {
                     float lse = 0.0f;
                     if (r < rows)
@@ -496,6 +491,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
                 for (int k = 0; k < 4; ++k) {
                     float o[kCols];
                     tmem_load16(tmem + kRows + k * kRows + col0, o);
+                    tmem_load16(tmem + kRows + k * kRows + col0 + 16, o + 16);
                     tmem_wait_load();
                     const int dim = k * 128 + key;
                     if (whole_range) {
@@ -551,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
             }
             mbar_init(&s.scores, 1);
             mbar_init(&s.probs, kConvertWarp);
-            mbar_init(&s.query, 8);
+            mbar_init(&s.query, 16);
             mbar_init(&s.query_free, 1);
             mbar_init(&s.output, 1);
             mbar_init_fence();
@@ -561,11 +557,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     __syncthreads();
     tmem_fence_after();
     if (warp < kConvertWarp) {
+        registers_up<kSoftmaxRegs>();
         softmax_role(w, s, smem, c);
     } else if (warp < kMultiplyWarp) {
-        convert_role(p, s, smem, c);
+        registers_down<kConvertRegs>();
+        if (warp < kConvertWarp + 8)
+            convert_role<0>(p, s, smem, c);
+        else
+            convert_role<1>(p, s, smem, c);
     } else {
-        multiply_role(p, s, smem_addr(smem), c);
+        registers_down<kMultiplyRegs>();
+        if (warp == kMultiplyWarp)
+            multiply_role(p, s, smem_addr(smem), c);
     }
     tmem_fence_before();
     __syncthreads();
@@ -576,30 +579,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
 }
 
 // Joins the partial results of the units whose tiles more than one run took, and
-// writes the rows that see no key.  Block (u, z): rows z * join_rows.. of unit u.
-constexpr int kJoinThreads = 128;
+// writes the rows that see no key.  A row goes to one warp, or, where a few long
+// requests are spread over many runs, to the eight warps of a block (kSplit), each
+// with every eighth run.
+constexpr int kJoinWarps = 8;
 
-struct JParams {
-    WParams w;
-    int join_rows;
-};
-
-__global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const __grid_constant__ JParams jp)
+template <bool kSplit>
+__global__ void __launch_bounds__(kJoinWarps * 32) fp4_join_kernel(const __grid_constant__ WParams w)
 {
-    __shared__ int before_s[4], total_s[4];
-    const WParams &w = jp.w;
+    __shared__ int before_s[kJoinWarps], total_s[kJoinWarps];
+    __shared__ float4 o_s[kSplit ? kJoinWarps : 1][4][32];
+    __shared__ float sum_s[kJoinWarps];
     const AParams &p = w.p;
     const Fp4AttentionArgs &a = p.a;
-    const int r0 = blockIdx.y * jp.join_rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Cursor c;
     c.unit = blockIdx.x;
     c.enter(p);
-    const int row0 = c.row0, row1 = c.row1;
-    if (row0 + r0 >= row1)
-        return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = kSplit ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
     int before = 0, total = 0;
-    for (int i = threadIdx.x; i < p.units; i += kJoinThreads) {
+    for (int i = threadIdx.x; i < p.units; i += kJoinWarps * 32) {
         const int tiles = tiles_of(p, i);
         total += tiles;
         before += i < c.unit ? tiles : 0;
@@ -611,51 +610,89 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const __grid_con
         total_s[warp] = total;
     }
     __syncthreads();
-    before = before_s[0] + before_s[1] + before_s[2] + before_s[3];
-    total = total_s[0] + total_s[1] + total_s[2] + total_s[3];
+    before = total = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+        before += before_s[i];
+        total += total_s[i];
+    }
     const int tiles = c.range.tiles();
     const int share = (total + w.runs - 1) / w.runs;
     const int x0 = tiles > 0 ? before / share : 0, x1 = tiles > 0 ? (before + tiles - 1) / share : -1;
-    if (tiles > 0 && x0 == x1)
-        return;  // written by its run
+    // written by its run, or no row (with kSplit the same for the whole block)
+    if ((tiles > 0 && x0 == x1) || c.row0 + r >= c.row1)
+        return;
     const Span ps = partial_span(w);
     const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
     // the first run may have begun with an earlier unit
     const int slot0 = before == x0 * share ? 0 : 1;
-    for (int r = r0; r < r0 + jp.join_rows && row0 + r < row1; ++r) {
-        float m = kUnset;
-        for (int x = x0 + lane; x <= x1; x += 32) {
-            const float *part = partial_at(w, x, x == x0 ? slot0 : 0) + kRows * DSV4_HEAD_DIM;
-            if (ld_f32_in(part + kRows + r, ps, a.b.err) != 0.0f)
-                m = fmaxf(m, ld_f32_in(part + r, ps, a.b.err));
-        }
+    const float *ms = w.partials + kRows * DSV4_HEAD_DIM + r;
+    const auto part = [&](int x) { return (size_t(x) * 2 + (x == x0 ? slot0 : 0)) * kPartialFloats; };
+    float m = kUnset;
+    for (int x = x0 + lane; x <= x1; x += 32)
+        if (ld_f32_in(ms + part(x) + kRows, ps, a.b.err) != 0.0f)
+            m = fmaxf(m, ld_f32_in(ms + part(x), ps, a.b.err));
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-        float sum = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int d = 16; d >= 1; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    float sum = 0.0f;
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int x = x0; x <= x1; ++x) {
-            const float *part = partial_at(w, x, x == x0 ? slot0 : 0);
-            const float n = ld_f32_in(part + kRows * DSV4_HEAD_DIM + kRows + r, ps, a.b.err);
-            const float f = n == 0.0f ? 0.0f : exp2_approx(ld_f32_in(part + kRows * DSV4_HEAD_DIM + r, ps, a.b.err) - m);
-            const float4 v = ld_f4_in(part + r * DSV4_HEAD_DIM + 4 * threadIdx.x, ps, a.b.err);
-            sum += n * f;
-            o.x += v.x * f;
-            o.y += v.y * f;
-            o.z += v.z * f;
-            o.w += v.w * f;
+    for (int x = x0 + (kSplit ? warp : 0); x <= x1; x += kSplit ? kJoinWarps : 1) {
+        const float n = ld_f32_in(ms + part(x) + kRows, ps, a.b.err);
+        const float f = n == 0.0f ? 0.0f : exp2_approx(ld_f32_in(ms + part(x), ps, a.b.err) - m);
+        const float *from = w.partials + part(x) + r * DSV4_HEAD_DIM + 4 * lane;
+        sum += n * f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = ld_f4_in(from + 128 * k, ps, a.b.err);
+            o[k].x += v.x * f;
+            o[k].y += v.y * f;
+            o[k].z += v.z * f;
+            o[k].w += v.w * f;
         }
-        const int64_t row = int64_t(c.request(p)) * p.all_rows + row0 + r;
-        float lse;
-        const float f = finish(m, sum, sink_of(a, row0 + r), &lse);
-        st8_in(a.out + row * DSV4_HEAD_DIM + 4 * threadIdx.x,
-               f == 0.0f ? make_uint2(0u, 0u)
-                         : make_uint2(bf16x2_rn(o.x * f, o.y * f), bf16x2_rn(o.z * f, o.w * f)),
-               os, a.b.err);
-        if (threadIdx.x == 0 && a.lse != nullptr)
-            st_f32_in(a.lse + row, lse, Span{a.lse, rows_of(a) * 4u}, a.b.err);
     }
+    if constexpr (kSplit) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o_s[warp][k][lane] = o[k];
+        if (lane == 0)
+            sum_s[warp] = sum;
+        __syncthreads();
+        if (warp >= 4)
+            return;
+        // warp k finishes dims 128k..
+        sum = 0.0f;
+        o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+            const float4 v = o_s[i][warp][lane];
+            sum += sum_s[i];
+            o[0].x += v.x;
+            o[0].y += v.y;
+            o[0].z += v.z;
+            o[0].w += v.w;
+        }
+    }
+    const int64_t row = int64_t(c.request) * p.all_rows + c.row0 + r;
+    float lse;
+    const float f = finish(m, sum, sink_of(a, c.row0 + r), &lse);
+    const int first = kSplit ? warp : 0, last = kSplit ? warp : 3;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (k < first || k > last)
+            continue;
+        const float4 v = kSplit ? o[0] : o[k];
+        st8_in(a.out + row * DSV4_HEAD_DIM + 128 * k + 4 * lane,
+               f == 0.0f ? make_uint2(0u, 0u)
+                         : make_uint2(bf16x2_rn(v.x * f, v.y * f), bf16x2_rn(v.z * f, v.w * f)),
+               os, a.b.err);
+    }
+    if (lane == 0 && first == 0 && a.lse != nullptr)
+        st_f32_in(a.lse + row, lse, Span{a.lse, rows_of(a) * 4u}, a.b.err);
 }
 
 int configure(int *sms)
@@ -689,22 +726,25 @@ int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_
     int sms = 0;
     if (configure(&sms) != DSV4_OK)
         return DSV4_ERR_CUDA;
-    JParams j;
-    j.w.p = tile_params(a, kRows);
-    j.w.partials = static_cast<float *>(workspace);
-    const int64_t most = (int64_t(a.b.width) * a.b.block_size + kTileKeys - 1) / kTileKeys * j.w.p.units;
+    WParams w;
+    w.p = tile_params(a, kRows);
+    w.partials = static_cast<float *>(workspace);
+    const int64_t most = (int64_t(a.b.width) * a.b.block_size + kTileKeys - 1) / kTileKeys * w.p.units;
     int runs = sms < kMaxCtas ? sms : kMaxCtas;
     runs = most < runs ? int(most) : runs;
-    j.w.runs = runs;
+    w.runs = runs;
     const int st = launch_kernel(fp4_attention_kernel, dim3(unsigned(runs)), dim3(kThreads), kSmemBytes,
-                                 stream, j.w);
+                                 stream, w);
     if (st != DSV4_OK)
         return st;
-    j.join_rows = j.w.p.units >= 32 ? 4 : 1;
-    const int rows = j.w.p.all_rows < kRows ? j.w.p.all_rows : kRows;
-    return launch_kernel(fp4_join_kernel,
-                         dim3(unsigned(j.w.p.units), unsigned((rows + j.join_rows - 1) / j.join_rows)),
-                         dim3(kJoinThreads), 0, stream, j);
+    const unsigned rows = unsigned(w.p.all_rows < kRows ? w.p.all_rows : kRows);
+    // a unit spans runs / units of them and at most two more
+    if (runs / w.p.units >= kJoinWarps)
+        return launch_kernel(fp4_join_kernel<true>, dim3(unsigned(w.p.units), rows), dim3(kJoinWarps * 32),
+                             0, stream, w);
+    return launch_kernel(fp4_join_kernel<false>,
+                         dim3(unsigned(w.p.units), (rows + kJoinWarps - 1) / kJoinWarps),
+                         dim3(kJoinWarps * 32), 0, stream, w);
 }
 
 }  // namespace dsv4

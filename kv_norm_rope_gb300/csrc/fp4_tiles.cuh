@@ -84,19 +84,18 @@ __device__ __forceinline__ Range range_of(const Fp4AttentionArgs &a, int n, int 
 
 // A place on a CTA's run of tiles.  A unit is one row tile of one request.
 struct Cursor {
-    int unit, tile, left, n, row0, row1;
+    int unit, request, tile, left, n, row0, row1;
     Range range;
 
     // the unit's numbers, for a place inside it
     __device__ __forceinline__ void enter(const AParams &p)
     {
-        row0 = unit % p.row_tiles * p.tile_rows;
+        request = unit / p.row_tiles;
+        row0 = (unit - request * p.row_tiles) * p.tile_rows;
         row1 = row0 + p.tile_rows < p.all_rows ? row0 + p.tile_rows : p.all_rows;
-        n = length_of(p.a.b, request(p));
+        n = length_of(p.a.b, request);
         range = range_of(p.a, n, row0, row1);
     }
-
-    __device__ __forceinline__ int request(const AParams &p) const { return unit / p.row_tiles; }
 
     // true when this tile is the last of the run or of its unit
     __device__ __forceinline__ bool ends_segment() const
@@ -193,19 +192,15 @@ __device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratc
 
 // ---- Cache rows -> operand
 //
-// 256 threads: thread i owns half (i & 1) of each chunk of key i / 2 of a tile,
-// that is one scale group (16 bytes of codes) of chunks 0..6 and 64 bytes of rope
-// in chunk 7.  Everything comes through a ring of two slots in shared memory by
-// asynchronous copies, in six steps a tile, each issued two steps ahead into the
-// thread's own bytes:
-//   0, 1, 2: the codes of chunks 0 1, 2 3, 4 5;   4, 5: the halves of the rope dims;
-//   3: the codes of chunk 6, the scales of the next tile and the block number of the
-//      one after it (into a word of the key's own elsewhere).
-// (Held in registers instead, the loads took half as long again: a warp has six
-// scoreboards, so using one load also waited for others issued long after it.)
+// Two teams of 256 threads: team 0 converts the pairs of chunks 0 1 and 4 5, team 1
+// those of 2 3 and 6 7.  Thread i of a team owns half (i & 1) of each chunk of key
+// i / 2 of the tile, that is one scale group (16 bytes of codes) or 64 bytes of rope.
+// Codes come through a slot in shared memory by asynchronous copies into the thread's
+// own bytes, issued a pair ahead, half a tile; scales and block numbers are loaded a
+// tile ahead, and rope dims, after a prefetch into L2, when the pair before is done.
 
-constexpr uint32_t kRingSlot = 256 * 32;
-constexpr int kSteps = 6;
+constexpr int kTeam = 256;
+constexpr uint32_t kRingSlot = kTeam * 32;
 
 // where a thread's key of a tile is
 struct KeyPlace {
@@ -227,7 +222,7 @@ __device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c,
     if (c.left > 0 && i >= c.range.lo && i < c.range.hi) {
         const uint32_t at = fastdiv(uint32_t(i), p.block_div);
         k.off = uint32_t(i) - at * uint32_t(p.a.b.block_size);
-        k.entry = p.a.b.table + c.request(p) * p.a.b.table_stride + at;
+        k.entry = p.a.b.table + c.request * p.a.b.table_stride + at;
     }
     return k;
 }
@@ -254,37 +249,36 @@ __device__ __forceinline__ void copy16(const AParams &p, uint32_t to, const uint
                  : "memory");
 }
 
-// step j of a tile whose key is at `row`, the next tile's at `next`, the block
-// number after that at `entry`, to go to `block`
-template <int j>
-__device__ __forceinline__ void copy_step(const AParams &p, uint32_t ring, int tid, const Fp4Row &row,
-                                          const Fp4Row &next, const int32_t *entry, uint32_t block)
+// the thread's codes of pair i of chunks on their way into its place of a slot
+template <int i>
+__device__ __forceinline__ void copy_codes(const AParams &p, uint32_t slot, int tid, const Fp4Row &row)
 {
-    const uint32_t slot = ring + (j & 1) * kRingSlot;
-    const int half = tid & 1;
-    const bool ok = row.data != nullptr;
-    if constexpr (j < 3) {
-        copy16(p, slot + tid * 16, row.data + 64 * j + 16 * half, ok);
-        copy16(p, slot + 4096 + tid * 16, row.data + 64 * j + 32 + 16 * half, ok);
-    } else if constexpr (j == 3) {
-        copy16(p, slot + tid * 16, row.data + 192 + 16 * half, ok);
-        copy16(p, slot + 4096 + tid * 16, next.scale, next.data != nullptr);
-        const bool known = entry != nullptr && in_span(entry, 4, table_span(p.a.b), p.a.b.err);
-        if (half == 0)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(block),
-                         "l"(known ? entry : p.a.b.table), "r"(known ? 4 : 0)
-                         : "memory");
-    } else {
-        copy16(p, slot + tid * 16, row.data + kFp4Codes + 64 * half + 32 * (j - 4), ok);
-        copy16(p, slot + 4096 + tid * 16, row.data + kFp4Codes + 64 * half + 32 * (j - 4) + 16, ok);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint8_t *from = row.data + 64 * i + 16 * (tid & 1);
+    copy16(p, slot + tid * 16, from, row.data != nullptr);
+    if constexpr (i < 3)
+        copy16(p, slot + 4096 + tid * 16, from + 32, row.data != nullptr);
 }
 
-// all but the newest group of the thread's copies have landed
-__device__ __forceinline__ void copy_wait_but_one()
+// the thread's copies have landed
+__device__ __forceinline__ void copy_wait()
 {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 load_raw(const AParams &p, const uint8_t *at, bool ok)
+{
+    return ok ? ldg16_now_in(at, cache_span(p.a.b), p.a.b.err) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+__device__ __forceinline__ void prefetch64(const AParams &p, const uint8_t *at, bool ok)
+{
+    if (ok && in_span(at, 64, cache_span(p.a.b), p.a.b.err))
+        asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 32];" ::"l"(at));
+}
+
+__device__ __forceinline__ uint32_t load_block(const AParams &p, const KeyPlace &k)
+{
+    return k.entry != nullptr ? ldg4_now_in(k.entry, table_span(p.a.b), p.a.b.err) : 0u;
 }
 
 // 32 codes of chunk c (the thread's half) with their scale -> 32 bf16
@@ -305,14 +299,22 @@ __device__ __forceinline__ void computed(uint4 &v)
     asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
 }
 
-// The query rows of a unit into the K-major operand of `rows` rows (chunk j: dims
-// 64j.., rows * 128 bytes), zeros past the unit's last.  `threads` threads.
-__device__ __forceinline__ void load_query(const AParams &p, int unit, uint8_t *to, int rows, int tid,
-                                           int threads)
+// the thread's half of a chunk's row into the operand
+__device__ __forceinline__ void store_half(uint8_t *chunk, int key, int half, const uint4 *v)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + k)) = v[k];
+}
+
+// Query rows row0.. of a request into the K-major operand of `rows` rows (chunk j:
+// dims 64j.., rows * 128 bytes), zeros past the request's last.  `threads` threads.
+__device__ __forceinline__ void load_query(const AParams &p, int request, int row0, uint8_t *to,
+                                           int rows, int tid, int threads)
 {
     const Fp4AttentionArgs &a = p.a;
-    const int row0 = unit % p.row_tiles * p.tile_rows, real = p.all_rows - row0;
-    const uint16_t *q = a.q + (int64_t(unit / p.row_tiles) * p.all_rows + row0) * DSV4_HEAD_DIM;
+    const int real = p.all_rows - row0;
+    const uint16_t *q = a.q + (int64_t(request) * p.all_rows + row0) * DSV4_HEAD_DIM;
     const Span qs{a.q, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
 #pragma unroll 8
     for (int i = tid; i < rows * 64; i += threads) {

@@ -1,132 +1,434 @@
-// The attention that each key of the 4-bit cache gets.
+// The attention each key of the 4-bit cache gets: weights[key] += the sum over query
+// rows of exp(scale * q . k - lse).
+//
+// The first product of the attention (fp4_attention.cu) with another end: S^T[key,
+// row] = K q^T on the tensor cores, keys in the lanes, so a thread holds one key and
+// its sum over rows needs no exchange.  2 * 512 multiplications a (row, key), no
+// second product, and nothing for the matrix unit to wait for but converted rows:
+//
+//  * 128 query rows a pass (N = 128: the rows' operand then costs the matrix unit no
+//    more shared-memory reads than it has time for).  More rows take more passes
+//    over the same run of keys, whose bytes then come from L2.
+//  * The tile passes through two slots of two chunks, one for each converting team,
+//    so a chunk is converted while the one before is multiplied; S^T has two
+//    places, so the sums of a tile run under the product of the next.
+//  * Each key's sum is finished by one thread of one CTA in a fixed order of rows
+//    and added by it: no atomics, the same bits every time.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "fp4.cuh"
+#include <atomic>
+
+#include "fp4_tiles.cuh"
 #include "launch_status.h"
 #include "ops.h"
 
 namespace dsv4 {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
+constexpr int kRows = 128;  // query rows of a pass
+constexpr int kGroups = 2;  // of 4 summing warps, each with half of the rows
+constexpr int kCols = kRows / kGroups;
+constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
+constexpr int kThreads = (kMultiplyWarp + 1) * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kOkTiles = 4;
 
-struct AParams {
-    Fp4AttentionArgs a;
-    uint64_t block_div;
+// Shared memory (from a 1024-byte boundary).
+constexpr uint32_t kSlotBytes = 2 * kChunkBytes;                // a pair of chunks
+constexpr uint32_t kQuery = 2 * kSlotBytes;                     // 8 chunks of 128 rows
+constexpr uint32_t kRing = kQuery + kChunks * kRows * 128;      // codes on their way
+constexpr uint32_t kShared = kRing + 2 * kRingSlot;
+
+struct Shared {
+    uint64_t full[2], free[2], scores[2], scores_free[2], query, query_free;
+    uint32_t tmem;
+    int scratch[18];
+    alignas(16) float lse[kRows];
+    int seen_to[kRows], seen_from[kRows];
+    float part[kTileKeys];
+    uint8_t key_ok[kOkTiles][kTileKeys];
+};
+constexpr size_t kSmemBytes = kShared + sizeof(Shared);
+static_assert(kSmemBytes <= 227 * 1024, "too much shared memory");
+
+struct WParams {
+    AParams p;   // one unit a request: all of its rows
+    int passes;  // of 128 rows
 };
 
-__device__ __forceinline__ Span cache_span(const Fp4Batch &b)
-{
-    return Span{b.cache, uint64_t(b.num_blocks) * uint32_t(b.block_size) * kFp4Slot};
-}
+// The order in which a CTA works: its run of tiles request by request, each
+// request's part once a pass.
+struct Sweep {
+    Cursor c;
+    int length, k, pass;
+    bool live, new_pass;
 
-__device__ __forceinline__ uint64_t rows_of(const Fp4AttentionArgs &a)
-{
-    return uint64_t(a.b.batch) * uint32_t(a.q_len) * uint32_t(a.heads);
-}
-
-__device__ __forceinline__ void flag(int32_t *err, int bit)
-{
-    if (err != nullptr)
-        atomicOr(err, bit);
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
-        v += __shfl_xor_sync(kFull, v, m);
-    return v;
-}
-
-// the keys of request r, as many as its row of the table can name
-__device__ __forceinline__ int length_of(const Fp4Batch &b, int r)
-{
-    const int limit = b.width * b.block_size;
-    const int n = int(ldg4_in(b.lens + r, Span{b.lens, uint64_t(b.batch) * 4u}, b.err));
-    if (n > limit)
-        flag(b.err, DSV4_DEVERR_SLOT_RANGE);
-    return n < 0 ? 0 : n > limit ? limit : n;
-}
-
-// dims [8l, 8l+8) and [256+8l, 256+8l+8) of key i of request r as fp32; false for a bad block
-__device__ __forceinline__ bool load_key(const AParams &p, int lane, int r, int i, float *x)
-{
-    const Fp4Batch &b = p.a.b;
-    const uint32_t at = fastdiv(uint32_t(i), p.block_div);
-    const int32_t *entry = b.table + r * b.table_stride + at;
-    const uint32_t blk = ldg4_in(entry, Span{b.table, (uint64_t(b.batch - 1) * b.table_stride + b.width) * 4u}, b.err);
-    if (int64_t(blk) >= b.num_blocks) {
-        flag(b.err, DSV4_DEVERR_SLOT_RANGE);
-        return false;
+    __device__ __forceinline__ void begin()
+    {
+        live = c.left > 0;
+        const int rest = c.range.stop() - c.tile;
+        length = c.left < rest ? c.left : rest;
+        k = pass = 0;
+        new_pass = true;
     }
-    const Fp4Row row = fp4_row(b.cache, blk, uint32_t(i) - at * uint32_t(b.block_size), uint32_t(b.block_size));
-    const Span cs = cache_span(b);
-    const uint32_t e0 = ldg_byte_in(row.scale + (lane >> 2), cs, b.err);
-    widen8(fp4x8_to_bf16(ldg4_in(row.data + 4 * lane, cs, b.err), fp4_scale_bf16x2(e0)), x);
-    if (lane < 24) {
-        const uint32_t e1 = ldg_byte_in(row.scale + 8 + (lane >> 2), cs, b.err);
-        widen8(fp4x8_to_bf16(ldg4_in(row.data + 128 + 4 * lane, cs, b.err), fp4_scale_bf16x2(e1)), x + 8);
-    } else {
-        widen8(ldg16_in(row.data + kFp4Codes + 16 * (lane - 24), cs, b.err), x + 8);
+
+    // the place as a cursor, for key_place
+    __device__ __forceinline__ Cursor at() const
+    {
+        Cursor x = c;
+        x.tile = c.tile + k;
+        x.left = live ? 1 : 0;
+        return x;
     }
-    return true;
+
+    __device__ __forceinline__ void advance(const WParams &w)
+    {
+        new_pass = false;
+        if (++k < length)
+            return;
+        k = 0;
+        new_pass = true;
+        if (++pass < w.passes)
+            return;
+        c.tile += length - 1;
+        c.left -= length - 1;
+        c.advance(w.p);
+        begin();
+    }
+};
+
+__device__ __forceinline__ int pass_rows(const WParams &w, int pass)
+{
+    const int rest = w.p.all_rows - pass * kRows;
+    return rest < kRows ? rest : kRows;
 }
 
-__device__ __forceinline__ float dot16(const float *x, const float *y)
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        s = __fmaf_rn(x[i], y[i], s);
-    return warp_sum(s);
-}
+// ---- Warps 8..23: cache rows and queries into operands
 
-// one warp per key, the rows in order
-__global__ void __launch_bounds__(128) fp4_weights_kernel(const AParams p)
+template <int team>
+__device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_t *smem, Sweep sw)
 {
-    const Fp4AttentionArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.y;
-    const int n = length_of(a.b, r);
-    if (n > a.weights_width)
-        flag(a.b.err, DSV4_DEVERR_SLOT_RANGE);
-    const int most = n < a.weights_width ? n : a.weights_width;
-    const Span qs{a.q, rows_of(a) * 1024u}, ls{a.lse, rows_of(a) * 4u};
-    const Span ws{a.weights, (uint64_t(a.b.batch - 1) * a.weights_stride + a.weights_width) * 4u};
-    for (int i = int(blockIdx.x) * 4 + (threadIdx.x >> 5); i < most; i += int(gridDim.x) * 4) {
-        float x[16];
-        if (!load_key(p, lane, r, i, x))
-            continue;
-        float sum = 0.0f;
-        for (int j = 0; j < a.q_len; ++j) {
-            const int to = n - a.q_len + 1 + j;
-            if (i >= to || (a.window > 0 && i < to - a.window))
-                continue;
-            for (int h = 0; h < a.heads; ++h) {
-                const int64_t row = (int64_t(r) * a.q_len + j) * a.heads + h;
-                float q[16];
-                widen8(ldg16_in(a.q + row * 512 + 8 * lane, qs, a.b.err), q);
-                widen8(ldg16_in(a.q + row * 512 + 256 + 8 * lane, qs, a.b.err), q + 8);
-                const float lse = ldg_f32_in(a.lse + row, ls, a.b.err);
-                const float s = dot16(q, x) * a.scale;
-                sum += lse == -INFINITY ? 0.0f : expf(s - lse);
-            }
+    const AParams &p = w.p;
+    const int tid = threadIdx.x - kConvertWarp * 32 - team * kTeam;
+    const int key = tid >> 1, half = tid & 1, lane = tid & 31;
+    const uint8_t *mine = smem + kRing + team * kRingSlot;
+    uint8_t *to = smem + team * kSlotBytes;
+    const uint32_t slot = smem_addr(mine);
+    KeyPlace now = key_place(p, sw.at(), true, key);
+    int now_pass = 0;
+    Fp4Row row = row_at(p, now, load_block(p, now));
+    copy_codes<team>(p, slot, tid, row);
+    uint4 scales = load_raw(p, row.scale, row.data != nullptr);
+    sw.advance(w);
+    KeyPlace next = key_place(p, sw.at(), sw.new_pass, key);
+    bool next_live = sw.live;
+    int next_pass = sw.pass;
+    uint32_t next_block = load_block(p, next);
+    uint32_t passes = 0;
+    for (uint32_t t = 0;; ++t) {
+        const Fp4Row next_row = row_at(p, next, next_block);
+        KeyPlace after = next;
+        after.entry = nullptr;
+        bool after_live = false;
+        int after_pass = 0;
+        if (next_live) {
+            sw.advance(w);
+            after = key_place(p, sw.at(), sw.new_pass, key);
+            after_live = sw.live;
+            after_pass = sw.pass;
         }
-        float *w = a.weights + r * a.weights_stride + i;
-        if (lane == 0)
-            st_f32_in(w, ld_f32_in(w, ws, a.b.err) + sum, ws, a.b.err);
+        next_block = load_block(p, after);
+        const uint4 next_scales = load_raw(p, next_row.scale, next_row.data != nullptr);
+        if constexpr (team == 1)
+            prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
+        bool alive = true;
+        if (now.new_unit) {
+            if (passes > 0)
+                alive = __all_sync(kFull, mbar_wait(&s.query_free, (passes - 1) & 1));
+            if (alive) {
+                load_query(p, now.unit, now_pass * kRows, smem + kQuery, kRows, tid + team * kTeam,
+                           2 * kTeam);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&s.query);
+            }
+            ++passes;
+        }
+        uint4 rope[4];
+        const auto pair = [&](auto ci) {
+            constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1, this slot's use 2t + i / 2
+            const uint32_t use = 2 * t + i / 2;
+            copy_wait();
+            uint4 a = *reinterpret_cast<const uint4 *>(mine + tid * 16), b = a, out[4];
+            if constexpr (i < 3)
+                b = *reinterpret_cast<const uint4 *>(mine + 4096 + tid * 16);
+            computed(a);
+            computed(b);
+            if constexpr (i < 2)
+                copy_codes<i + 2>(p, slot, tid, row);
+            else
+                copy_codes<i - 2>(p, slot, tid, next_row);
+            convert_codes<2 * i>(scales, a, half, out);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                computed(out[k]);  // before the wait for its place
+            if (use > 0 && alive)
+                alive = __all_sync(kFull, mbar_wait(&s.free[team], (use - 1) & 1));
+            if (!alive)
+                return;
+            if (i == 0 && half == 0)
+                s.key_ok[t % kOkTiles][key] = row.data != nullptr ? 1 : 0;
+            store_half(to, key, half, out);
+            if constexpr (i < 3) {
+                convert_codes<2 * i + 1>(scales, b, half, out);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    out[k] = mul_bf16x8(rope[k], kRopeToOperand);
+            }
+            store_half(to + kChunkBytes, key, half, out);
+            if constexpr (i == 1) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    rope[k] = load_raw(p, row.data + kFp4Codes + 64 * half + 16 * k, row.data != nullptr);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&s.full[team]);
+        };
+        pair(std::integral_constant<int, team>{});
+        pair(std::integral_constant<int, team + 2>{});
+        if (!alive) {
+            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+            break;
+        }
+        if (!next_live)
+            break;
+        scales = next_scales;
+        row = next_row;
+        now = next;
+        now_pass = next_pass;
+        next = after;
+        next_live = after_live;
+        next_pass = after_pass;
     }
+    copy_wait();
+}
+
+// ---- Warp 24: the products
+
+__device__ __forceinline__ void multiply_role(const WParams &w, Shared &s, uint32_t smem, Sweep sw)
+{
+    const uint32_t elected = elect_one();
+    const Operand keys = operand(smem, 16, 1024), query = operand(smem + kQuery, 16, 1024);
+    uint32_t inst = 0, passes = 0;
+    for (uint32_t t = 0; sw.live; ++t) {
+        bool alive = true;
+        if (sw.new_pass) {
+            inst = instruction(uint32_t((pass_rows(w, sw.pass) + 15) & ~15), false);
+            alive = __all_sync(kFull, mbar_wait(&s.query, passes & 1));
+            ++passes;
+        }
+        const bool last = sw.k + 1 == sw.length;
+        if (t >= 2)
+            alive = alive && __all_sync(kFull, mbar_wait(&s.scores_free[t & 1], (t / 2 - 1) & 1));
+        const uint32_t d = s.tmem + (t & 1) * kRows;
+#pragma unroll
+        for (int i = 0; i < kChunks / 2; ++i) {
+            alive = alive && __all_sync(kFull, mbar_wait(&s.full[i & 1], (2 * t + i / 2) & 1));
+            if (!alive)
+                break;
+            tmem_fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_bf16(d, keys + ((i & 1) * kSlotBytes + (k >> 2) * kChunkBytes + 32 * (k & 3)),
+                         query + ((2 * i + (k >> 2)) * kRows * 128 + 32 * (k & 3)), inst, i > 0 || k > 0,
+                         elected);
+            mma_commit(&s.free[i & 1], elected);
+        }
+        if (!alive) {
+            flag(w.p.a.b.err, DSV4_DEVERR_TIMEOUT);
+            break;
+        }
+        mma_commit(&s.scores[t & 1], elected);
+        if (last)
+            mma_commit(&s.query_free, elected);
+        sw.advance(w);
+    }
+}
+
+// ---- Warps 0..7: the sums
+
+__device__ __forceinline__ void sum_role(const WParams &w, Shared &s, Sweep sw)
+{
+    const AParams &p = w.p;
+    const Fp4AttentionArgs &a = p.a;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
+    const int key = warp * 32 + lane, col0 = group * kCols, tid = threadIdx.x;
+    const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
+    const float scale = a.scale * (kLog2e * kOperandUnit);
+    const Span ws{a.weights, (uint64_t(a.b.batch - 1) * a.weights_stride + a.weights_width) * 4u};
+    for (uint32_t t = 0; sw.live; ++t) {
+        const int rows = pass_rows(w, sw.pass), n = sw.c.n;
+        if (sw.new_pass) {
+            named_barrier(1, 256);  // the rows before are done with
+            if (tid < kRows) {
+                const int r = sw.pass * kRows + tid;
+                float lse = INFINITY;  // no row: its exponentials are 0
+                int to = 0;
+                if (tid < rows) {
+                    lse = kLog2e * ldg_f32_in(a.lse + int64_t(sw.c.request) * p.all_rows + r,
+                                              Span{a.lse, rows_of(a) * 4u}, a.b.err);
+                    if (lse == -INFINITY)
+                        lse = INFINITY;  // a row that saw nothing adds nothing
+                    to = n - a.q_len + 1 + r / a.heads;
+                }
+                s.lse[tid] = lse;
+                s.seen_to[tid] = to;
+                s.seen_from[tid] = a.window > 0 ? to - a.window : INT32_MIN;
+            }
+            named_barrier(1, 256);
+        }
+        const int tile = sw.c.tile + sw.k, i = tile * kTileKeys + key;
+        const bool mine = group == 0 && i >= sw.c.range.lo && i < sw.c.range.hi;
+        if (mine && i >= a.weights_width)
+            flag(a.b.err, DSV4_DEVERR_SLOT_RANGE);
+        const bool add = mine && i < a.weights_width;
+        float *to = a.weights + int64_t(sw.c.request) * a.weights_stride + i;
+        const float before = add ? ld_f32_now_in(to, ws, a.b.err) : 0.0f;
+        const bool failed = !mbar_wait(&s.scores[t & 1], (t / 2) & 1);
+        if (named_barrier_any(1, 256, failed)) {
+            flag(a.b.err, DSV4_DEVERR_TIMEOUT);
+            return;
+        }
+        tmem_fence_after();
+        // every row of the group sees every key of the tile
+        const bool whole = rows >= col0 + kCols && (tile + 1) * kTileKeys <= s.seen_to[col0] &&
+                           tile * kTileKeys >= s.seen_from[col0 + kCols - 1];
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j0 = 0; j0 < kCols; j0 += 32) {
+            if (col0 + j0 >= rows)
+                break;
+            float v[32];
+            tmem_load16(tmem + (t & 1) * kRows + col0 + j0, v);
+            tmem_load16(tmem + (t & 1) * kRows + col0 + j0 + 16, v + 16);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(&s.lse[col0 + j0 + j]);
+                v[j] = exp2_approx(__fmaf_rn(v[j], scale, -l.x));
+                v[j + 1] = exp2_approx(__fmaf_rn(v[j + 1], scale, -l.y));
+                v[j + 2] = exp2_approx(__fmaf_rn(v[j + 2], scale, -l.z));
+                v[j + 3] = exp2_approx(__fmaf_rn(v[j + 3], scale, -l.w));
+            }
+            if (!whole) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (i >= s.seen_to[col0 + j0 + j] || i < s.seen_from[col0 + j0 + j])
+                        v[j] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                sum[j & 3] += v[j];
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&s.scores_free[t & 1]);
+        const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (group == 1)
+            s.part[key] = total;
+        named_barrier(1, 256);
+        if (add && s.key_ok[t % kOkTiles][key] != 0)
+            st_f32_in(to, before + (total + s.part[key]), ws, a.b.err);
+        sw.advance(w);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fp4_weights_kernel(const __grid_constant__ WParams w)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared &s = *reinterpret_cast<Shared *>(smem + kShared);
+    const int warp = threadIdx.x >> 5;
+    Sweep sw;
+    deal(w.p, blockIdx.x, gridDim.x, s.scratch, sw.c);
+    if (sw.c.left == 0)
+        return;
+    if ((smem_addr(smem) & 1023u) != 0u) {  // never: there is no static shared memory
+        flag(w.p.a.b.err, DSV4_DEVERR_TIMEOUT);
+        return;
+    }
+    sw.begin();
+    if (warp == kMultiplyWarp) {
+        tmem_alloc512(&s.tmem);
+        if ((threadIdx.x & 31) == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&s.full[i], 8);
+                mbar_init(&s.free[i], 1);
+                mbar_init(&s.scores[i], 1);
+                mbar_init(&s.scores_free[i], 4 * kGroups);
+            }
+            mbar_init(&s.query, 16);
+            mbar_init(&s.query_free, 1);
+            mbar_init_fence();
+        }
+        tmem_fence_before();
+    }
+    __syncthreads();
+    tmem_fence_after();
+    if (warp < kConvertWarp)
+        sum_role(w, s, sw);
+    else if (warp < kConvertWarp + 8)
+        convert_role<0>(w, s, smem, sw);
+    else if (warp < kMultiplyWarp)
+        convert_role<1>(w, s, smem, sw);
+    else
+        multiply_role(w, s, smem_addr(smem), sw);
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kMultiplyWarp) {
+        tmem_fence_after();
+        tmem_free512(s.tmem);
+    }
+}
+
+int configure(int *sms)
+{
+    static std::atomic<int> sm_count[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return DSV4_ERR_CUDA;
+    const bool cached = dev >= 0 && dev < 64;
+    *sms = cached ? sm_count[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms > 0)
+        return DSV4_OK;
+    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms < 1 ||
+        cudaFuncSetAttribute(fp4_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(kSmemBytes)) != cudaSuccess)
+        return DSV4_ERR_CUDA;
+    if (cached)
+        sm_count[dev].store(*sms, std::memory_order_relaxed);
+    return DSV4_OK;
 }
 
 }  // namespace
 
 int launch_fp4_weights(const Fp4AttentionArgs &a, cudaStream_t stream)
 {
-    AParams p{a, fastdiv_magic(uint32_t(a.b.block_size))};
-    return launch_kernel(fp4_weights_kernel, dim3(1024, unsigned(a.b.batch)), dim3(128), 0, stream, p);
+    int sms = 0;
+    if (configure(&sms) != DSV4_OK)
+        return DSV4_ERR_CUDA;
+    WParams w;
+    w.p = tile_params(a, a.q_len * a.heads);
+    w.passes = (w.p.all_rows + kRows - 1) / kRows;
+    const int64_t most = (int64_t(a.b.width) * a.b.block_size + kTileKeys - 1) / kTileKeys * w.p.units;
+    return launch_kernel(fp4_weights_kernel, dim3(unsigned(most < sms ? most : sms)), dim3(kThreads),
+                         kSmemBytes, stream, w);
 }
 
 }  // namespace dsv4

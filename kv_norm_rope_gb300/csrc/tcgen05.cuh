@@ -144,6 +144,19 @@ __device__ __forceinline__ void tmem_wait_store()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// A warpgroup's registers a thread, out of what the CTA was launched with: up waits
+// until others went down by as much.
+template <int n>
+__device__ __forceinline__ void registers_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void registers_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
+
 // 2^x, flushing subnormal results
 __device__ __forceinline__ float exp2_approx(float x)
 {
