@@ -249,17 +249,26 @@ def _ptr(t) -> int | None:
 def _stream_handle(stream) -> int | None:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object is made
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
+_kinds_table = None
+
+
 def _kinds():
-    import torch
-    two_byte = (torch.bfloat16, torch.int16) + ((torch.uint16,) if hasattr(torch, "uint16") else ())
-    return {"bf16": two_byte, "i64": (torch.int64,), "f32": (torch.float32,),
-            "u8": (torch.uint8, torch.int8), "i32": (torch.int32,), "bytes": None}
+    global _kinds_table
+    if _kinds_table is None:
+        import torch
+        two_byte = (torch.bfloat16, torch.int16) + ((torch.uint16,) if hasattr(torch, "uint16") else ())
+        _kinds_table = {"bf16": two_byte, "i64": (torch.int64,), "f32": (torch.float32,),
+                        "u8": (torch.uint8, torch.int8), "i32": (torch.int32,), "bytes": None}
+    return _kinds_table
 
 
 def _check(name: str, t, kind: str, numel: int | None = None, min_bytes: int | None = None):
@@ -506,7 +515,7 @@ def add_gemma_rmsnorm_mxfp8(x, residual, gamma, eps: float, residual_out, codes,
 
 
 def fp4_cache_bytes(num_blocks: int, block_size: int) -> int:
-    return int(lib().dsv4_fp4_cache_bytes(num_blocks, block_size))
+    return num_blocks * block_size * FP4_SLOT_BYTES if num_blocks > 0 and block_size > 0 else 0
 
 
 def qnorm_rope_kv_fp4_insert(q, kv, kv_norm_weight, positions, cos_sin_cache, slot_mapping,
@@ -563,8 +572,14 @@ def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens)
     return B, Q, H, _check_rows("block_table", block_table, "i32", B)
 
 
+_workspace_bytes = 0
+
+
 def fp4_attention_workspace_bytes() -> int:
-    return int(lib().dsv4_fp4_attention_workspace_bytes())
+    global _workspace_bytes
+    if _workspace_bytes == 0:
+        _workspace_bytes = int(lib().dsv4_fp4_attention_workspace_bytes())
+    return _workspace_bytes
 
 
 def fp4_attention(q, kv_cache, num_blocks: int, block_size: int, block_table, seq_lens,
@@ -604,6 +619,8 @@ def _workspace(nbytes: int, device, stream):
         raise ValueError("workspace: pass one for a stream given by its handle")
     if device.type != "cuda":
         raise ValueError("q must be a CUDA tensor (there is no CPU path)")
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):  # the allocator gives it out again on this stream only
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 

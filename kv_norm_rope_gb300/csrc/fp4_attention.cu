@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     const AParams &p = w.p;
     const int warp = threadIdx.x >> 5;
     Cursor c;
+    let_kernel_after_begin();
     deal(p, blockIdx.x, gridDim.x, s.scratch, c);
     if (c.left == 0)
         return;
@@ -581,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
 // Joins the partial results of the units whose tiles more than one run took, and
 // writes the rows that see no key.  A row goes to one warp, or, where a few long
 // requests are spread over many runs, to the eight warps of a block (kSplit), each
-// with every eighth run.
+// with every eighth run.  It is launched while the attention ends, and finds its
+// place among the runs meanwhile.
 constexpr int kJoinWarps = 8;
 
 template <bool kSplit>
@@ -616,6 +618,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fp4_join_kernel(const __grid_
         before += before_s[i];
         total += total_s[i];
     }
+    wait_for_kernel_before();
     const int tiles = c.range.tiles();
     const int share = (total + w.runs - 1) / w.runs;
     const int x0 = tiles > 0 ? before / share : 0, x1 = tiles > 0 ? (before + tiles - 1) / share : -1;
@@ -740,11 +743,11 @@ int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_
     const unsigned rows = unsigned(w.p.all_rows < kRows ? w.p.all_rows : kRows);
     // a unit spans runs / units of them and at most two more
     if (runs / w.p.units >= kJoinWarps)
-        return launch_kernel(fp4_join_kernel<true>, dim3(unsigned(w.p.units), rows), dim3(kJoinWarps * 32),
-                             0, stream, w);
-    return launch_kernel(fp4_join_kernel<false>,
-                         dim3(unsigned(w.p.units), (rows + kJoinWarps - 1) / kJoinWarps),
-                         dim3(kJoinWarps * 32), 0, stream, w);
+        return launch_after(fp4_join_kernel<true>, dim3(unsigned(w.p.units), rows),
+                            dim3(kJoinWarps * 32), stream, w);
+    return launch_after(fp4_join_kernel<false>,
+                        dim3(unsigned(w.p.units), (rows + kJoinWarps - 1) / kJoinWarps),
+                        dim3(kJoinWarps * 32), stream, w);
 }
 
 }  // namespace dsv4

@@ -25,4 +25,60 @@ inline int launch_kernel(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, 
                : DSV4_ERR_CUDA;
 }
 
+// the same in clusters of `cluster` CTAs
+template <typename P>
+inline int launch_cluster(void (*kernel)(P), dim3 grid, dim3 block, unsigned cluster,
+                          cudaStream_t stream, const P &p)
+{
+    void *args[] = {const_cast<P *>(&p)};
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = grid;
+    config.blockDim = block;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    return cudaLaunchKernelExC(&config, reinterpret_cast<const void *>(kernel), args) == cudaSuccess
+               ? DSV4_OK
+               : DSV4_ERR_CUDA;
+}
+
+// A launch that may begin while the kernel before it on the stream still runs, once
+// every CTA of that one has ended or called let_kernel_after_begin().  Every thread
+// of it that reads what that kernel writes, and at least one thread of every CTA,
+// calls wait_for_kernel_before() first.
+template <typename P>
+inline int launch_after(void (*kernel)(P), dim3 grid, dim3 block, cudaStream_t stream, const P &p)
+{
+    void *args[] = {const_cast<P *>(&p)};
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = grid;
+    config.blockDim = block;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    return cudaLaunchKernelExC(&config, reinterpret_cast<const void *>(kernel), args) == cudaSuccess
+               ? DSV4_OK
+               : DSV4_ERR_CUDA;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void let_kernel_after_begin()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// until the kernel before it has ended and its writes are visible
+__device__ __forceinline__ void wait_for_kernel_before()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
+
 }  // namespace dsv4
