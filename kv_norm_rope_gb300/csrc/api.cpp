@@ -90,7 +90,7 @@ int resident_ctas(int kind, int64_t *resident)
 // flags of insert()
 constexpr int kKvNorm = 1;  // normalise the KV row with the weight
 constexpr int kNoQ = 2;     // num_heads may be 0 (KV rows only)
-constexpr int kFp4 = 4;     // the 4-bit store, whose layouts are SMALL and STREAM
+constexpr int kFp4 = 4;     // the 4-bit store, which has no HALF layout
 
 int insert(int store_mode, int variant, int flags, void *q, const void *kv, const void *w,
            const int64_t *positions, const float *cos_sin, int64_t max_position,
@@ -140,10 +140,8 @@ int insert(int store_mode, int variant, int flags, void *q, const void *kv, cons
     st = dsv4_launch_plan(num_tokens, num_heads, sms, ctas, variant, &plan);
     if (st != DSV4_OK)
         return st;
-    if (fp4 && plan.variant != DSV4_VARIANT_SMALL) {
-        // the whole-warp stream for any number of heads; with none, a warp per KV row
-        st = dsv4_launch_plan(num_tokens, num_heads > 0 ? num_heads : 1, sms, ctas,
-                              DSV4_VARIANT_STREAM, &plan);
+    if (fp4 && plan.variant == DSV4_VARIANT_HALF) {
+        st = dsv4_launch_plan(num_tokens, num_heads, sms, ctas, DSV4_VARIANT_STREAM, &plan);
         if (st != DSV4_OK)
             return st;
     }
@@ -176,7 +174,7 @@ int insert(int store_mode, int variant, int flags, void *q, const void *kv, cons
     a.kv_norm = kv_norm;
     if (plan.variant == DSV4_VARIANT_HALF)
         return dsv4::launch_half(store_mode, a, plan.ctas, static_cast<cudaStream_t>(stream));
-    if (num_heads == 0 && plan.variant == DSV4_VARIANT_STREAM && !fp4) {
+    if (num_heads == 0 && plan.variant == DSV4_VARIANT_STREAM) {
         // KV rows only: the quarter-warp-per-row kernel
         int64_t resident = 0;
         if (resident_ctas(kOccKvRows, &resident) != DSV4_OK)

@@ -256,6 +256,60 @@ __device__ __forceinline__ void quarter_row_fp8(const KParams &p, int lane, bool
     }
 }
 
+// The 4-bit store of a quarter-warp row.  Lanes 0..3 and 4..7 of the quarter share a
+// group of 32 dims in every vector u (groups 2u and 2u + 1).  The maxima of 8
+// vectors are reduce-scattered over 4 lanes: lane g ends with those of u = 2(g & 3)
+// and the next, derives their exponents, and all share them back.  A row that fp32
+// cannot settle is stored as it is and then again by the whole warp (fp4_row_exact).
+__device__ __forceinline__ void quarter_row_fp4(const KParams &p, int lane, bool active, int64_t t,
+                                                int64_t slot, const uint4 *x, const uint4 *w_smem,
+                                                const float *tmax, float r, const float *rope)
+{
+    const int g = lane & 7;
+    float b[4], c[2];
+    const bool b2 = (g & 2) != 0, b1 = (g & 1) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        b[i] = fmaxf(b2 ? tmax[i + 4] : tmax[i],
+                     __shfl_xor_sync(kFull, b2 ? tmax[i] : tmax[i + 4], 2));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        c[i] = fmaxf(b1 ? b[i + 2] : b[i], __shfl_xor_sync(kFull, b1 ? b[i] : b[i + 2], 1));
+    const Fp4Scale e0 = fp4_scale(__fmul_rn(c[0], r)), e1 = fp4_scale(__fmul_rn(c[1], r));
+    const bool last = (g & 3) == 3;  // its second vector is the rope dims, tmax[7] = 0
+    bool exact = e0.exact || (!last && e1.exact);
+    const Fp4Slot at = fp4_slot(p, active ? slot : 0);
+    const Span cspan = cache_span<kStoreFp4>(p);
+#pragma unroll
+    for (int u = 0; u < 7; ++u) {
+        const int s = __shfl_sync(kFull, (u & 1) ? e1.s : e0.s, (lane & ~3) | (u >> 1));
+        float xw[8];
+        quarter_vec<true>(x, w_smem, g, u, xw);
+        const uint32_t codes = fp4_codes(xw, r, s, exact);
+        if (active)
+            st_stream4_in(at.data + 32 * u + 4 * g, codes, cspan, p.err);
+    }
+    // bytes 4q..4q+3 (q = g & 3): the groups of u = 2q, then of u = 2q + 1
+    const uint32_t pair = uint32_t(e0.s + 127) | (last ? 0u : uint32_t(e1.s + 127) << 16);
+    const uint32_t word = pair | (__shfl_xor_sync(kFull, pair, 4) << 8);
+    if (active) {
+        if (g < 4)
+            st_stream4_in(at.scale + 4 * g, word, cspan, p.err);
+        st_stream16_in(at.data + DSV4_NOPE_DIM / 2 + 16 * g, bf16x8_rn(rope), cspan, p.err);
+    }
+    const unsigned rows = __ballot_sync(kFull, exact && active);
+    if (rows != 0u) {
+        __syncwarp();  // the stores above come first
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            if (((rows >> (8 * q)) & 0xffu) == 0u)
+                continue;
+            const Fp4Lane l = fp4_row_exact(kv_src(p), lane, __shfl_sync(kFull, t, 8 * q));
+            fp4_store(p, lane, __shfl_sync(kFull, slot, 8 * q), l);
+        }
+    }
+}
+
 // One KV row per quarter-warp: this quarter holds token t's row in x (zeros
 // when t >= T) with its metadata pos and slot.  It flags an out-of-range
 // position or slot and writes the cache row when both are in range.  All
@@ -278,7 +332,7 @@ __device__ __forceinline__ void kv_quad_row(const KParams &p, int lane, int64_t 
     const bool active = live && pos_ok && slot >= 0 && slot < p.num_slots;
     if (!__any_sync(kFull, active))
         return;
-    if constexpr (kStore == DSV4_STORE_FP8) {
+    if constexpr (kStore != DSV4_STORE_BF16) {
         // (the bf16 kernel has its cos/sin from the caller, loaded before the kv wait)
         if (active) {
             const float *cs = p.cs + pos * DSV4_ROPE_DIM + 4 * g;
@@ -306,6 +360,8 @@ __device__ __forceinline__ void kv_quad_row(const KParams &p, int lane, int64_t 
             }
             st16_in(row + 64 * 7 + 8 * g, bf16x8_rn(rope), cache_span<kStore>(p), p.err);
         }
+    } else if constexpr (kStore == kStoreFp4) {
+        quarter_row_fp4(p, lane, active, t, slot, x, w_smem, tmax, r, rope);
     } else {
         quarter_row_fp8<kKvNorm>(p, lane, active, t, slot, x, w_smem, tmax, r, rope);
     }
@@ -439,7 +495,8 @@ int configure_smem()
     const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
     if (bit != 0 && (configured.load(std::memory_order_relaxed) & bit) != 0)
         return DSV4_OK;
-    const void *kernels[4] = {reinterpret_cast<const void *>(kv_rows_kernel<DSV4_STORE_FP8, true>),
+    const void *kernels[] = {reinterpret_cast<const void *>(kv_rows_kernel<kStoreFp4, true>),
+                              reinterpret_cast<const void *>(kv_rows_kernel<DSV4_STORE_FP8, true>),
                               reinterpret_cast<const void *>(kv_rows_kernel<DSV4_STORE_FP8, false>),
                               reinterpret_cast<const void *>(kv_rows_kernel<DSV4_STORE_BF16, true>),
                               reinterpret_cast<const void *>(kv_rows_kernel<DSV4_STORE_BF16, false>)};
@@ -500,6 +557,9 @@ int launch_kv_rows(int store_mode, const LaunchArgs &a, int64_t max_ctas, cudaSt
     const int64_t quads = (a.num_tokens + 3) / 4;
     const int64_t need = quads > 0 ? (quads + kKvWarps - 1) / kKvWarps : 1;
     const unsigned grid = static_cast<unsigned>(need < max_ctas ? need : max_ctas);
+    if (store_mode == kStoreFp4)  // always with the norm
+        return launch_kernel(kv_rows_kernel<kStoreFp4, true>, dim3(grid), dim3(kKvThreads), kKvSmemBytes,
+                             stream, p);
     return store_mode == DSV4_STORE_BF16 ? launch_store<DSV4_STORE_BF16>(a.kv_norm, grid, stream, p)
                                          : launch_store<DSV4_STORE_FP8>(a.kv_norm, grid, stream, p);
 }

@@ -686,13 +686,17 @@ __device__ __forceinline__ float kv_products(const KParams &p, int lane, int64_t
 // E2M1_rn(v * 2^-s).  4-bit codes are so coarse that a value on the other side
 // of a border moves by a whole step, so both decisions follow the exact v =
 // x * w * r.  fp32 settles nearly all: its v is within 2^-20 of the exact one,
-// so an element whose code is the same at v * (1 - 2^-18) and v * (1 + 2^-18),
+// so an element whose code is the same at v * (1 - kFp4Band) and v * (1 + kFp4Band),
 // and an amax outside kNearBand of 1.5 * 2^k, are decided.  A row with any other
-// element (about 4 in 1000 on Gaussian data), or with a group too small for
-// fp32 to hold to full precision, is evaluated again in fp64 by its warp.
+// element (about one in 100 on Gaussian data) is evaluated again by its warp with r
+// in float-float arithmetic (above), which decides what is more than 2^-38 from a
+// border; ties, and groups too small for fp32 to hold to full precision, are
+// evaluated in fp64.  (With all such rows in fp64, 100003 rows of KV alone took 85 us
+// instead of 45: the fp64 pipe was busy 28% of the time and the rest waited for it.)
 
 constexpr uint32_t kMant1p5 = 0x400000u;  // mantissa field of 1.5 (6 = 1.5 * 2^2)
 constexpr float kFp4Tiny = 0x1p-100f;     // a group amax below this goes to fp64
+constexpr float kFp4Band = 0x1p-19f;
 
 // max over the 4 lanes that hold one 32-dim group
 template <typename F>
@@ -752,14 +756,14 @@ __device__ __forceinline__ uint32_t fp4_codes(const float *xw, float r, int s, b
     float u[8], lo[8], hi[8];
     scale8(xw, r, u);
     scale8(u, k, u);
-    scale8(u, 1.0f - 0x1p-18f, lo);
-    scale8(u, 1.0f + 0x1p-18f, hi);
+    scale8(u, 1.0f - kFp4Band, lo);
+    scale8(u, 1.0f + kFp4Band, hi);
     const uint32_t c = e2m1x8_rn(lo);
     exact = exact || c != e2m1x8_rn(hi);
     return c;
 }
 
-// The row of token t in fp64: the lane's two code words and its groups' s.
+// The lane's two code words and its groups' s.
 struct Fp4Lane {
     uint32_t c0, c1;
     int s0, s1;
@@ -785,6 +789,7 @@ __device__ __forceinline__ uint32_t e2m1_fp64(double u)
     return c | (u < 0.0 ? 8u : 0u);
 }
 
+// The row of token t in fp64.
 __device__ __noinline__ Fp4Lane fp4_row_fp64(KvSrc p, int lane, int64_t t)
 {
     const uint4 *row = reinterpret_cast<const uint4 *>(p.kv + t * kHead);
@@ -831,6 +836,123 @@ __device__ __noinline__ Fp4Lane fp4_row_fp64(KvSrc p, int lane, int64_t t)
     return out;
 }
 
+// E2M1 magnitude code of a >= 0, and the border above code c < 7
+__device__ __forceinline__ int e2m1_code(float a)
+{
+    return (a > 0.25f ? 1 : 0) + (a >= 0.75f ? 1 : 0) + (a > 1.25f ? 1 : 0) + (a >= 1.75f ? 1 : 0) +
+           (a > 2.5f ? 1 : 0) + (a >= 3.5f ? 1 : 0) + (a > 5.0f ? 1 : 0);
+}
+__device__ __forceinline__ float e2m1_border(int c)
+{
+    return c < 4 ? 0.25f + 0.5f * float(c) : c == 4 ? 2.5f : c == 5 ? 3.5f : 5.0f;
+}
+
+// The row of token t with the decisions that fp32 leaves open taken in float-float
+// arithmetic, or in fp64 where that is too close as well.
+__device__ __noinline__ Fp4Lane fp4_row_exact(KvSrc p, int lane, int64_t t)
+{
+    const uint4 *row = reinterpret_cast<const uint4 *>(p.kv + t * kHead);
+    const uint4 *wv = reinterpret_cast<const uint4 *>(p.w);
+    const uint4 xa = ldg16_in(row + lane, kv_span(p), p.err);
+    const uint4 xb = ldg16_in(row + 32 + lane, kv_span(p), p.err);
+    const uint4 wa = ldg16_in(wv + lane, w_span(p), p.err);
+    const uint4 wb = ldg16_in(wv + 32 + lane, w_span(p), p.err);
+    bool ok = true;
+    FF sq[2] = {FF{0.0f, 0.0f}, FF{0.0f, 0.0f}};
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+        const float a = bf16_at(xa, k), b = bf16_at(xb, k);
+        ok = ok && square_exact(a) && square_exact(b);
+        sq[0] = ff_add(sq[0], __fmul_rn(a, a));
+        sq[1] = ff_add(sq[1], __fmul_rn(b, b));
+    }
+    FF s = ff_add(sq[0], sq[1]);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        s = ff_add_xor(s, m);
+    const FF r = ff_inv_rms(s, p.eps, ok);
+    Fp4Lane out = {0u, 0u, 0, 0};
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        const uint4 x = h ? xb : xa, w = h ? wb : wa;
+        float xw[8];
+        prod8(x, w, xw);
+        const float top = group4_max(absmax8(xw)), amax = __fmul_rn(top, r.hi);
+        const Fp4Scale g = fp4_scale(amax);
+        int e = g.s;
+        if (g.exact) {
+            const int ef = int(__float_as_uint(amax) >> 23) - 127;
+            const int up = amax < kFp4Tiny
+                               ? -1
+                               : ff_exceeds(top, r, __uint_as_float((uint32_t(ef + 127) << 23) | kMant1p5));
+            ok = ok && (up >= 0 || (h == 1 && lane >= 24));
+            e = max(ef - 2 + (up > 0 ? 1 : 0), -127);
+        }
+        uint32_t c = 0u;
+        if (e != 128 && !(h == 1 && lane >= 24)) {
+            const float k2 = pow2_neg(e), unit = __uint_as_float(uint32_t(max(e, -126) + 127) << 23);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                const float v = __fmul_rn(bf16_at(x, k), bf16_at(w, k));  // exact
+                const float a = __fmul_rn(__fmul_rn(fabsf(v), r.hi), k2);
+                int code = e2m1_code(__fmul_rn(a, 1.0f - kFp4Band));
+                if (code != e2m1_code(__fmul_rn(a, 1.0f + kFp4Band))) {
+                    const int up = ff_exceeds(fabsf(v), r, __fmul_rn(e2m1_border(code), unit));
+                    ok = ok && up >= 0;
+                    code += up > 0 ? 1 : 0;
+                }
+                c |= (uint32_t(code) | (v < 0.0f ? 8u : 0u)) << (4 * ((k >> 1) + 4 * (k & 1)));
+            }
+        }
+        if (h == 0) {
+            out.c0 = c;
+            out.s0 = e;
+        } else {
+            out.c1 = c;
+            out.s1 = e;
+        }
+    }
+    if (__any_sync(kFull, !ok))
+        return fp4_row_fp64(p, lane, t);
+    return out;
+}
+
+// Where a slot's data and scale bytes are in the 4-bit cache.
+struct Fp4Slot {
+    uint8_t *data, *scale;
+};
+
+__device__ __forceinline__ Fp4Slot fp4_slot(const KParams &p, int64_t slot)
+{
+    const uint32_t bs = static_cast<uint32_t>(p.block_size);
+    const uint32_t blk = fastdiv(static_cast<uint32_t>(slot), p.slot_div);
+    const uint32_t off = static_cast<uint32_t>(slot) - blk * bs;
+    uint8_t *base = p.cache + uint64_t(blk) * bs * DSV4_FP4_SLOT_BYTES;
+    return Fp4Slot{base + uint64_t(off) * DSV4_FP4_DATA_BYTES,
+                   base + uint64_t(bs) * DSV4_FP4_DATA_BYTES + uint64_t(off) * DSV4_FP4_SCALE_BYTES};
+}
+
+// codes and scales of a row in the whole-warp layout into its slot
+__device__ __forceinline__ void fp4_store(const KParams &p, int lane, int64_t slot, const Fp4Lane &l)
+{
+    const bool rope_lane = lane >= 24;
+    const Fp4Slot at = fp4_slot(p, slot);
+    const Span cspan = cache_span<kStoreFp4>(p);
+    st_stream4_in(at.data + 4 * lane, l.c0, cspan, p.err);
+    if (!rope_lane)
+        st_stream4_in(at.data + 128 + 4 * lane, l.c1, cspan, p.err);
+    // scale byte g (group g < 8: lanes 4g..4g+3 of half 0; g >= 8: lanes 4(g-8).. of half 1)
+    const uint32_t shift = 8u * (uint32_t(lane >> 2) & 3u);
+    const bool lead = (lane & 3) == 0, low = lane < 16;
+    const uint32_t b0 = uint32_t(l.s0 + 127) << shift, b1 = uint32_t(l.s1 + 127) << shift;
+    const uint32_t w0 = __reduce_or_sync(kFull, lead && low ? b0 : 0u);
+    const uint32_t w1 = __reduce_or_sync(kFull, lead && !low ? b0 : 0u);
+    const uint32_t w2 = __reduce_or_sync(kFull, lead && low ? b1 : 0u);
+    const uint32_t w3 = __reduce_or_sync(kFull, lead && !low && !rope_lane ? b1 : 0u);
+    if (lane == 0)
+        st_stream16_in(at.scale, make_uint4(w0, w1, w2, w3), cspan, p.err);
+}
+
 // The 4-bit store of a row in the whole-warp layout: xw, tmax, r as kv_products
 // leaves them (rope lanes hold their final dims in xw[8..15]).
 __device__ __forceinline__ void kv_row_fp4(const KParams &p, int lane, int64_t t, int64_t slot,
@@ -846,30 +968,11 @@ __device__ __forceinline__ void kv_row_fp4(const KParams &p, int lane, int64_t t
     l.c0 = fp4_codes(xw, r, g0.s, exact);
     l.c1 = rope_lane ? 0u : fp4_codes(xw + 8, r, g1.s, exact);
     if (__any_sync(kFull, exact))
-        l = fp4_row_fp64(kv_src(p), lane, t);
-
-    const uint32_t blk = fastdiv(static_cast<uint32_t>(slot), p.slot_div);
-    const uint32_t off = static_cast<uint32_t>(slot) - blk * static_cast<uint32_t>(p.block_size);
-    uint8_t *base = p.cache + uint64_t(blk) * static_cast<uint32_t>(p.block_size) * DSV4_FP4_SLOT_BYTES;
-    uint8_t *data = base + uint64_t(off) * DSV4_FP4_DATA_BYTES;
-    const Span cspan = cache_span<kStoreFp4>(p);
-    st_stream4_in(data + 4 * lane, l.c0, cspan, p.err);
-    if (!rope_lane)
-        st_stream4_in(data + 128 + 4 * lane, l.c1, cspan, p.err);
-    else
-        st_stream16_in(data + DSV4_NOPE_DIM / 2 + 16 * (lane - 24), bf16x8_rn(xw + 8), cspan, p.err);
-    // scale byte g (group g < 8: lanes 4g..4g+3 of half 0; g >= 8: lanes 4(g-8).. of half 1)
-    const uint32_t shift = 8u * (uint32_t(lane >> 2) & 3u);
-    const bool lead = (lane & 3) == 0, low = lane < 16;
-    const uint32_t b0 = uint32_t(l.s0 + 127) << shift, b1 = uint32_t(l.s1 + 127) << shift;
-    const uint32_t w0 = __reduce_or_sync(kFull, lead && low ? b0 : 0u);
-    const uint32_t w1 = __reduce_or_sync(kFull, lead && !low ? b0 : 0u);
-    const uint32_t w2 = __reduce_or_sync(kFull, lead && low ? b1 : 0u);
-    const uint32_t w3 = __reduce_or_sync(kFull, lead && !low && !rope_lane ? b1 : 0u);
-    if (lane == 0)
-        st_stream16_in(base + uint64_t(p.block_size) * DSV4_FP4_DATA_BYTES +
-                           uint64_t(off) * DSV4_FP4_SCALE_BYTES,
-                       make_uint4(w0, w1, w2, w3), cspan, p.err);
+        l = fp4_row_exact(kv_src(p), lane, t);
+    fp4_store(p, lane, slot, l);
+    if (rope_lane)
+        st_stream16_in(fp4_slot(p, slot).data + DSV4_NOPE_DIM / 2 + 16 * (lane - 24), bf16x8_rn(xw + 8),
+                       cache_span<kStoreFp4>(p), p.err);
 }
 
 // The KV row of token t: v = x*w*r (or v = x when the row arrives normalised),
