@@ -120,37 +120,36 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
     const uint8_t *mine = smem + kRing + team * kRingSlot;
     const uint32_t slot = smem_addr(mine);
     KeyPlace now = key_place(p, c, true, key);
-    Fp4Row row = row_at(p, now, load_block(p, now));
+    Fp4Row row = row_at(p, now);
     copy_codes<team>(p, slot, tid, row);
     uint4 scales = load_raw(p, row.scale, row.data != nullptr);
+    const auto fill_query = [&] {
+        load_query(p, now.request, now.row0, smem + kQuery, kRows, tid + team * kTeam, 2 * kTeam);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&s.query);
+    };
+    fill_query();
     bool moved = c.advance(p);
     KeyPlace next = key_place(p, c, moved, key);
-    uint32_t next_block = load_block(p, next);
-    int segment = 0;
+    int segment = 1;
     for (int t = 0; t < count; ++t) {
-        const Fp4Row next_row = row_at(p, next, next_block);
+        const Fp4Row next_row = row_at(p, next);
         KeyPlace after = next;
-        after.entry = nullptr;
+        after.off = UINT32_MAX;
         if (c.left > 0) {
             moved = c.advance(p);
             after = key_place(p, c, moved, key);
         }
-        next_block = load_block(p, after);
         const uint4 next_scales = load_raw(p, next_row.scale, next_row.data != nullptr);
         if constexpr (team == 1)
             prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
         bool alive = true;
-        if (now.new_unit) {
-            if (segment > 0)
-                alive = __all_sync(kFull, mbar_wait(&s.query_free, (segment - 1) & 1));
-            if (alive) {
-                load_query(p, now.unit / p.row_tiles, now.unit % p.row_tiles * kRows, smem + kQuery, kRows,
-                           tid + team * kTeam, 2 * kTeam);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&s.query);
-            }
+        if (now.new_unit && t > 0) {
+            alive = __all_sync(kFull, mbar_wait(&s.query_free, (segment - 1) & 1));
+            if (alive)
+                fill_query();
             ++segment;
         }
         uint4 rope[4];
@@ -373,7 +372,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             from_tile = c.tile;
             if (warp == 0) {
                 const int r = col0 + lane;
-                const int to = r < rows ? c.n - a.q_len + 1 + (row0 + r) / a.heads : 0;
+                const int to = r < rows ? c.n - a.q_len + 1 + int(fastdiv(uint32_t(row0 + r), p.head_div)) : 0;
                 s.seen_to[r] = to;
                 s.seen_from[r] = a.window > 0 ? to - a.window : INT32_MIN;
                 s.m[r] = kUnset;
@@ -530,11 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     Shared &s = *reinterpret_cast<Shared *>(smem + kShared);
     const AParams &p = w.p;
     const int warp = threadIdx.x >> 5;
-    Cursor c;
     let_kernel_after_begin();
-    deal(p, blockIdx.x, gridDim.x, s.scratch, c);
-    if (c.left == 0)
-        return;
     if ((smem_addr(smem) & 1023u) != 0u) {  // never: there is no static shared memory
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
         return;
@@ -555,9 +550,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         }
         tmem_fence_before();
     }
-    __syncthreads();
+    Cursor c;
+    deal(p, blockIdx.x, gridDim.x, s.scratch, c);  // with barriers for the CTA
     tmem_fence_after();
-    if (warp < kConvertWarp) {
+    if (c.left == 0) {
+        // more CTAs than tiles
+    } else if (warp < kConvertWarp) {
         registers_up<kSoftmaxRegs>();
         softmax_role(w, s, smem, c);
     } else if (warp < kMultiplyWarp) {

@@ -28,7 +28,7 @@ constexpr uint32_t kChunkBytes = kTileKeys * 128;
 
 struct AParams {
     Fp4AttentionArgs a;
-    uint64_t block_div;  // fastdiv_magic(block_size)
+    uint64_t block_div, head_div, tile_div;  // fastdiv_magic of block_size, heads, row_tiles
     int all_rows;        // q_len * heads
     int tile_rows;       // of a row tile
     int row_tiles;       // of a request
@@ -73,12 +73,14 @@ struct Range {
     __device__ __forceinline__ int tiles() const { return stop() - first(); }
 };
 
-__device__ __forceinline__ Range range_of(const Fp4AttentionArgs &a, int n, int row0, int row1)
+__device__ __forceinline__ Range range_of(const AParams &p, int n, int row0, int row1)
 {
-    const int hi = n - a.q_len + 1 + (row1 - 1) / a.heads;
+    const Fp4AttentionArgs &a = p.a;
+    const int hi = n - a.q_len + 1 + int(fastdiv(uint32_t(row1 - 1), p.head_div));
     if (hi <= 0)
         return Range{0, 0};
-    const int from = a.window > 0 ? n - a.q_len + 1 + row0 / a.heads - a.window : 0;
+    const int from =
+        a.window > 0 ? n - a.q_len + 1 + int(fastdiv(uint32_t(row0), p.head_div)) - a.window : 0;
     return Range{from > 0 ? from : 0, hi};
 }
 
@@ -90,11 +92,11 @@ struct Cursor {
     // the unit's numbers, for a place inside it
     __device__ __forceinline__ void enter(const AParams &p)
     {
-        request = unit / p.row_tiles;
+        request = int(fastdiv(uint32_t(unit), p.tile_div));
         row0 = (unit - request * p.row_tiles) * p.tile_rows;
         row1 = row0 + p.tile_rows < p.all_rows ? row0 + p.tile_rows : p.all_rows;
         n = length_of(p.a.b, request);
-        range = range_of(p.a, n, row0, row1);
+        range = range_of(p, n, row0, row1);
     }
 
     // true when this tile is the last of the run or of its unit
@@ -204,40 +206,41 @@ constexpr uint32_t kRingSlot = kTeam * 32;
 
 // where a thread's key of a tile is
 struct KeyPlace {
-    const int32_t *entry;  // its block's number; null: not seen by any row
-    uint32_t off;
-    int unit;
+    uint32_t block, off;  // off = UINT32_MAX: not seen by any row
+    int request, row0;    // of the unit
     bool new_unit;
 };
 
+// the block's number is on its way when this returns
 __device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c, bool new_unit,
                                               int key)
 {
     KeyPlace k;
     const int i = c.tile * kTileKeys + key;
     k.new_unit = new_unit;
-    k.unit = c.unit;
-    k.entry = nullptr;
-    k.off = 0u;
+    k.request = c.request;
+    k.row0 = c.row0;
+    k.block = 0u;
+    k.off = UINT32_MAX;
     if (c.left > 0 && i >= c.range.lo && i < c.range.hi) {
         const uint32_t at = fastdiv(uint32_t(i), p.block_div);
         k.off = uint32_t(i) - at * uint32_t(p.a.b.block_size);
-        k.entry = p.a.b.table + c.request * p.a.b.table_stride + at;
+        k.block = ldg4_now_in(p.a.b.table + c.request * p.a.b.table_stride + at, table_span(p.a.b),
+                              p.a.b.err);
     }
     return k;
 }
 
-// the row of a placed key whose block number is `block`; data = null for none (not
-// seen, or a bad block, which is flagged)
-__device__ __forceinline__ Fp4Row row_at(const AParams &p, const KeyPlace &k, uint32_t block)
+// the row of a placed key; data = null for none (not seen, or a bad block, which is flagged)
+__device__ __forceinline__ Fp4Row row_at(const AParams &p, const KeyPlace &k)
 {
-    if (k.entry == nullptr)
+    if (k.off == UINT32_MAX)
         return Fp4Row{nullptr, nullptr};
-    if (int64_t(block) >= p.a.b.num_blocks) {
+    if (int64_t(k.block) >= p.a.b.num_blocks) {
         flag(p.a.b.err, DSV4_DEVERR_SLOT_RANGE);
         return Fp4Row{nullptr, nullptr};
     }
-    return fp4_row(p.a.b.cache, block, k.off, uint32_t(p.a.b.block_size));
+    return fp4_row(p.a.b.cache, k.block, k.off, uint32_t(p.a.b.block_size));
 }
 
 // 16 bytes to shared memory, zeros for none
@@ -274,11 +277,6 @@ __device__ __forceinline__ void prefetch64(const AParams &p, const uint8_t *at, 
 {
     if (ok && in_span(at, 64, cache_span(p.a.b), p.a.b.err))
         asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 32];" ::"l"(at));
-}
-
-__device__ __forceinline__ uint32_t load_block(const AParams &p, const KeyPlace &k)
-{
-    return k.entry != nullptr ? ldg4_now_in(k.entry, table_span(p.a.b), p.a.b.err) : 0u;
 }
 
 // 32 codes of chunk c (the thread's half) with their scale -> 32 bf16
@@ -330,9 +328,11 @@ inline AParams tile_params(const Fp4AttentionArgs &a, int tile_rows)
     AParams p;
     p.a = a;
     p.block_div = fastdiv_magic(uint32_t(a.b.block_size));
+    p.head_div = fastdiv_magic(uint32_t(a.heads));
     p.all_rows = a.q_len * a.heads;
     p.tile_rows = tile_rows;
     p.row_tiles = (p.all_rows + tile_rows - 1) / tile_rows;
+    p.tile_div = fastdiv_magic(uint32_t(p.row_tiles));
     p.units = p.row_tiles * a.b.batch;
     return p;
 }

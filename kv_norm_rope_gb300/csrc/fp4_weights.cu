@@ -118,19 +118,18 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
     const uint32_t slot = smem_addr(mine);
     KeyPlace now = key_place(p, sw.at(), true, key);
     int now_pass = 0;
-    Fp4Row row = row_at(p, now, load_block(p, now));
+    Fp4Row row = row_at(p, now);
     copy_codes<team>(p, slot, tid, row);
     uint4 scales = load_raw(p, row.scale, row.data != nullptr);
     sw.advance(w);
     KeyPlace next = key_place(p, sw.at(), sw.new_pass, key);
     bool next_live = sw.live;
     int next_pass = sw.pass;
-    uint32_t next_block = load_block(p, next);
     uint32_t passes = 0;
     for (uint32_t t = 0;; ++t) {
-        const Fp4Row next_row = row_at(p, next, next_block);
+        const Fp4Row next_row = row_at(p, next);
         KeyPlace after = next;
-        after.entry = nullptr;
+        after.off = UINT32_MAX;
         bool after_live = false;
         int after_pass = 0;
         if (next_live) {
@@ -139,7 +138,6 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
             after_live = sw.live;
             after_pass = sw.pass;
         }
-        next_block = load_block(p, after);
         const uint4 next_scales = load_raw(p, next_row.scale, next_row.data != nullptr);
         if constexpr (team == 1)
             prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
@@ -148,7 +146,7 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
             if (passes > 0)
                 alive = __all_sync(kFull, mbar_wait(&s.query_free, (passes - 1) & 1));
             if (alive) {
-                load_query(p, now.unit, now_pass * kRows, smem + kQuery, kRows, tid + team * kTeam,
+                load_query(p, now.request, now_pass * kRows, smem + kQuery, kRows, tid + team * kTeam,
                            2 * kTeam);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -285,7 +283,7 @@ __device__ __forceinline__ void sum_role(const WParams &w, Shared &s, Sweep sw)
                                               Span{a.lse, rows_of(a) * 4u}, a.b.err);
                     if (lse == -INFINITY)
                         lse = INFINITY;  // a row that saw nothing adds nothing
-                    to = n - a.q_len + 1 + r / a.heads;
+                    to = n - a.q_len + 1 + int(fastdiv(uint32_t(r), p.head_div));
                 }
                 s.lse[tid] = lse;
                 s.seen_to[tid] = to;
