@@ -19,7 +19,8 @@
 //    own, so the next tile is converted under the products of this one.
 //  * Warps 0..7 do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
 //    32 (w / 4)..; a thread has one key and 32 rows.  Warps 8..23 convert, warp 24
-//    issues the products.  Registers move from the converting warps to the softmax's.
+//    issues the products.  Registers move from that warpgroup to the softmax: a spill
+//    costs a trip to L2, as shared memory leaves little of L1.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the
 //    largest score of the first tile it saw; p = 2^(x - m) is taken against that,
 //    and only when some x exceeds m by more than kSlack is m moved and everything
@@ -50,7 +51,7 @@ constexpr int kCols = kRows / kGroups;
 constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
 constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three warps idle
 // registers a thread: 72 at launch (896 * 72 = 64512), then
-constexpr int kSoftmaxRegs = 96, kConvertRegs = 64, kMultiplyRegs = 56;
+constexpr int kSoftmaxRegs = 88, kConvertRegs = 72, kMultiplyRegs = 40;
 static_assert(128 * (kGroups * kSoftmaxRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
               "the shares exceed what the CTA was launched with");
 constexpr int kMaxCtas = 256;        // of a launch: what the workspace is for
@@ -94,6 +95,7 @@ struct Shared {
     float warp_rows[4][kRows];  // maxima or sums of the four warps' keys
     int seen_to[kRows], seen_from[kRows];
     uint8_t key_ok[kTileKeys];
+    Cursor place[4 * kGroups];  // of the softmax warps
 };
 constexpr size_t kSmemBytes = kShared + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "too much shared memory");
@@ -117,14 +119,15 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
     const int tid = threadIdx.x - kConvertWarp * 32 - team * kTeam;
     const int key = tid >> 1, half = tid & 1, lane = tid & 31;
     const int count = c.left;
-    const uint8_t *mine = smem + kRing + team * kRingSlot;
-    const uint32_t slot = smem_addr(mine);
+    const uint32_t base = smem_addr(smem), slot = base + kRing + team * kRingSlot;
+    const uint32_t place = swizzled(key, 4 * half);
     KeyPlace now = key_place(p, c, true, key);
     Fp4Row row = row_at(p, now);
     copy_codes<team>(p, slot, tid, row);
     uint4 scales = load_raw(p, row.scale, row.data != nullptr);
     const auto fill_query = [&] {
-        load_query(p, now.request, now.row0, smem + kQuery, kRows, tid + team * kTeam, 2 * kTeam);
+        const int unit = ~now.unit, request = int(fastdiv(uint32_t(unit), p.tile_div));
+        load_query(p, request, (unit - request * p.row_tiles) * kRows, smem + kQuery, kRows, tid + team * kTeam, 2 * kTeam);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
@@ -146,7 +149,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
         if constexpr (team == 1)
             prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
         bool alive = true;
-        if (now.new_unit && t > 0) {
+        if (now.unit < 0 && t > 0) {
             alive = __all_sync(kFull, mbar_wait(&s.query_free, (segment - 1) & 1));
             if (alive)
                 fill_query();
@@ -155,13 +158,12 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
         uint4 rope[4];
         const auto pair = [&](auto ci) {
             constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1
-            uint8_t *to = smem + kKeys + 2 * i * kChunkBytes;
+            const uint32_t to = base + kKeys + 2 * i * kChunkBytes;
             copy_wait();
-            uint4 a = *reinterpret_cast<const uint4 *>(mine + tid * 16), b = a, out[4];
+            const uint4 a = load_shared16(slot + tid * 16);
+            uint4 b = a, out[4];
             if constexpr (i < 3)
-                b = *reinterpret_cast<const uint4 *>(mine + 4096 + tid * 16);
-            computed(a);
-            computed(b);
+                b = load_shared16(slot + 4096 + tid * 16);
             if constexpr (i < 2)
                 copy_codes<i + 2>(p, slot, tid, row);
             else
@@ -176,7 +178,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
                 return;
             if (i == 0 && half == 0)
                 s.key_ok[key] = row.data != nullptr ? 1 : 0;
-            store_half(to, key, half, out);
+            store_half(to, place, out);
             if constexpr (i < 3) {
                 convert_codes<2 * i + 1>(scales, b, half, out);
             } else {
@@ -184,7 +186,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
                 for (int k = 0; k < 4; ++k)
                     out[k] = mul_bf16x8(rope[k], kRopeToOperand);
             }
-            store_half(to + kChunkBytes, key, half, out);
+            store_half(to + kChunkBytes, place, out);
             if constexpr (i == 1) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -355,14 +357,20 @@ __device__ __forceinline__ float finish(float m, float sum, float sink, float *l
     return w / total * kOperandUnit;
 }
 
-__device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor c)
+__device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, const Cursor &begin)
 {
     const AParams &p = w.p;
     const Fp4AttentionArgs &a = p.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
     const int key = warp * 32 + lane, col0 = group * kCols;
+    // the warp's place lives in shared memory: what the softmax holds fills its registers
+    Cursor &c = s.place[threadIdx.x >> 5];
+    if (lane == 0)
+        c = begin;
+    __syncwarp();
     const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
     const float scale = a.scale * (kLog2e * kOperandUnit);
+    const uint32_t probs = smem_addr(smem) + kProbs, row = swizzled(key, group * (kCols / 8));
     float sum[kCols];
     bool first = true;
     int segment = 0, from_tile = 0;
@@ -434,18 +442,18 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             move_references(s, v, sum, tmem, !first);
             load_scores(s.m);
         }
-        uint32_t packed[kCols / 2];
 #pragma unroll
-        for (int j = 0; j < kCols; j += 2) {
-            const float p0 = exp2_approx(v[j]), p1 = exp2_approx(v[j + 1]);
-            sum[j] += p0;
-            sum[j + 1] += p1;
-            packed[j / 2] = bf16x2_rn(p0, p1);
+        for (int k = 0; k < kCols / 8; ++k) {
+            uint32_t packed[4];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float p0 = exp2_approx(v[8 * k + j]), p1 = exp2_approx(v[8 * k + j + 1]);
+                sum[8 * k + j] += p0;
+                sum[8 * k + j + 1] += p1;
+                packed[j / 2] = bf16x2_rn(p0, p1);
+            }
+            store_shared16(probs + (row ^ (k << 4)), make_uint4(packed[0], packed[1], packed[2], packed[3]));
         }
-#pragma unroll
-        for (int k = 0; k < kCols / 8; ++k)
-            *reinterpret_cast<uint4 *>(smem + kProbs + swizzled(key, group * (kCols / 8) + k)) =
-                make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
         fence_proxy_async_smem();
         tmem_fence_before();
         __syncwarp();
@@ -519,7 +527,10 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             named_barrier(1 + group, 128);  // m, sum and factor are free for the next segment
         }
         first = last;
-        c.advance(p);
+        __syncwarp();
+        if (lane == 0)
+            c.advance(p);
+        __syncwarp();
     }
 }
 
@@ -559,7 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         registers_up<kSoftmaxRegs>();
         softmax_role(w, s, smem, c);
     } else if (warp < kMultiplyWarp) {
-        registers_down<kConvertRegs>();
         if (warp < kConvertWarp + 8)
             convert_role<0>(p, s, smem, c);
         else

@@ -207,8 +207,7 @@ constexpr uint32_t kRingSlot = kTeam * 32;
 // where a thread's key of a tile is
 struct KeyPlace {
     uint32_t block, off;  // off = UINT32_MAX: not seen by any row
-    int request, row0;    // of the unit
-    bool new_unit;
+    int unit;             // its complement on the first tile of a unit
 };
 
 // the block's number is on its way when this returns
@@ -217,9 +216,7 @@ __device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c,
 {
     KeyPlace k;
     const int i = c.tile * kTileKeys + key;
-    k.new_unit = new_unit;
-    k.request = c.request;
-    k.row0 = c.row0;
+    k.unit = new_unit ? ~c.unit : c.unit;
     k.block = 0u;
     k.off = UINT32_MAX;
     if (c.left > 0 && i >= c.range.lo && i < c.range.hi) {
@@ -297,12 +294,32 @@ __device__ __forceinline__ void computed(uint4 &v)
     asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
 }
 
-// the thread's half of a chunk's row into the operand
-__device__ __forceinline__ void store_half(uint8_t *chunk, int key, int half, const uint4 *v)
+// 16 bytes of shared memory by 32-bit address: the converting warps have no registers
+// to spare for generic ones
+__device__ __forceinline__ uint4 load_shared16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_shared16(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+// the thread's half of a chunk's row into the operand at `chunk`; `place` = swizzled(key,
+// 4 * half), so that 16-byte chunk k of the half is at place ^ 16k
+__device__ __forceinline__ void store_half(uint32_t chunk, uint32_t place, const uint4 *v)
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4 *>(chunk + swizzled(key, half * 4 + k)) = v[k];
+        store_shared16(chunk + (place ^ (k << 4)), v[k]);
 }
 
 // Query rows row0.. of a request into the K-major operand of `rows` rows (chunk j:

@@ -31,7 +31,12 @@ constexpr int kRows = 128;  // query rows of a pass
 constexpr int kGroups = 2;  // of 4 summing warps, each with half of the rows
 constexpr int kCols = kRows / kGroups;
 constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
-constexpr int kThreads = (kMultiplyWarp + 1) * 32;
+constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three warps idle
+// registers a thread: 72 at launch, then (the converting warps spill below this, and
+// spills go to L2: shared memory leaves little of L1)
+constexpr int kSumRegs = 72 /* as launched */, kConvertRegs = 80, kMultiplyRegs = 40;
+static_assert(128 * (kGroups * kSumRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
+              "the shares exceed what the CTA was launched with");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kOkTiles = 4;
 
@@ -113,9 +118,8 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
     const AParams &p = w.p;
     const int tid = threadIdx.x - kConvertWarp * 32 - team * kTeam;
     const int key = tid >> 1, half = tid & 1, lane = tid & 31;
-    const uint8_t *mine = smem + kRing + team * kRingSlot;
-    uint8_t *to = smem + team * kSlotBytes;
-    const uint32_t slot = smem_addr(mine);
+    const uint32_t base = smem_addr(smem), slot = base + kRing + team * kRingSlot;
+    const uint32_t place = swizzled(key, 4 * half), to = base + team * kSlotBytes;
     KeyPlace now = key_place(p, sw.at(), true, key);
     int now_pass = 0;
     Fp4Row row = row_at(p, now);
@@ -142,11 +146,11 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
         if constexpr (team == 1)
             prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
         bool alive = true;
-        if (now.new_unit) {
+        if (now.unit < 0) {
             if (passes > 0)
                 alive = __all_sync(kFull, mbar_wait(&s.query_free, (passes - 1) & 1));
             if (alive) {
-                load_query(p, now.request, now_pass * kRows, smem + kQuery, kRows, tid + team * kTeam,
+                load_query(p, ~now.unit, now_pass * kRows, smem + kQuery, kRows, tid + team * kTeam,
                            2 * kTeam);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -160,11 +164,10 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
             constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1, this slot's use 2t + i / 2
             const uint32_t use = 2 * t + i / 2;
             copy_wait();
-            uint4 a = *reinterpret_cast<const uint4 *>(mine + tid * 16), b = a, out[4];
+            const uint4 a = load_shared16(slot + tid * 16);
+            uint4 b = a, out[4];
             if constexpr (i < 3)
-                b = *reinterpret_cast<const uint4 *>(mine + 4096 + tid * 16);
-            computed(a);
-            computed(b);
+                b = load_shared16(slot + 4096 + tid * 16);
             if constexpr (i < 2)
                 copy_codes<i + 2>(p, slot, tid, row);
             else
@@ -179,7 +182,7 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
                 return;
             if (i == 0 && half == 0)
                 s.key_ok[t % kOkTiles][key] = row.data != nullptr ? 1 : 0;
-            store_half(to, key, half, out);
+            store_half(to, place, out);
             if constexpr (i < 3) {
                 convert_codes<2 * i + 1>(scales, b, half, out);
             } else {
@@ -187,7 +190,7 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
                 for (int k = 0; k < 4; ++k)
                     out[k] = mul_bf16x8(rope[k], kRopeToOperand);
             }
-            store_half(to + kChunkBytes, key, half, out);
+            store_half(to + kChunkBytes, place, out);
             if constexpr (i == 1) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -379,14 +382,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_weights_kernel(const __grid_c
     }
     __syncthreads();
     tmem_fence_after();
-    if (warp < kConvertWarp)
+    if (warp < kConvertWarp) {
         sum_role(w, s, sw);
-    else if (warp < kConvertWarp + 8)
-        convert_role<0>(w, s, smem, sw);
-    else if (warp < kMultiplyWarp)
-        convert_role<1>(w, s, smem, sw);
-    else
-        multiply_role(w, s, smem_addr(smem), sw);
+    } else if (warp < kMultiplyWarp) {
+        registers_up<kConvertRegs>();
+        if (warp < kConvertWarp + 8)
+            convert_role<0>(w, s, smem, sw);
+        else
+            convert_role<1>(w, s, smem, sw);
+    } else {
+        registers_down<kMultiplyRegs>();
+        if (warp == kMultiplyWarp)
+            multiply_role(w, s, smem_addr(smem), sw);
+    }
     tmem_fence_before();
     __syncthreads();
     if (warp == kMultiplyWarp) {
