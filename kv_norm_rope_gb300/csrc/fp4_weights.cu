@@ -6,12 +6,15 @@
 // its sum over rows needs no exchange.  2 * 512 multiplications a (row, key), no
 // second product, and nothing for the matrix unit to wait for but converted rows:
 //
-//  * 128 query rows a pass (N = 128: the rows' operand then costs the matrix unit no
-//    more shared-memory reads than it has time for).  More rows take more passes
-//    over the same run of keys, whose bytes then come from L2.
-//  * The tile passes through two slots of two chunks, one for each converting team,
-//    so a chunk is converted while the one before is multiplied; S^T has two
-//    places, so the sums of a tile run under the product of the next.
+//  * 128 query rows a pass (N = 128).  More rows take more passes over the same run
+//    of keys, whose bytes then come from L2.
+//  * Converted keys go to tensor memory, the left operand, a thread a key: 256 of its
+//    512 columns are a tile's 512 dims, in four pairs of chunks, each filled by its
+//    own warpgroup as soon as the product of the tile before has read it.  (Through
+//    shared memory, as the attention has to, their 128 KB a tile contended with the
+//    product's own reads: 89 us against NOW at weights_long's sizes.)
+//  * S^T has two places in the other 256 columns, so the sums of a tile run under the
+//    product of the next.
 //  * Each key's sum is finished by one thread of one CTA in a fixed order of rows
 //    and added by it: no atomics, the same bits every time.
 
@@ -31,29 +34,28 @@ constexpr int kRows = 128;  // query rows of a pass
 constexpr int kGroups = 2;  // of 4 summing warps, each with half of the rows
 constexpr int kCols = kRows / kGroups;
 constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
-constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three warps idle
-// registers a thread: 72 at launch, then (the converting warps spill below this, and
-// spills go to L2: shared memory leaves little of L1)
-constexpr int kSumRegs = 72 /* as launched */, kConvertRegs = 80, kMultiplyRegs = 40;
-static_assert(128 * (kGroups * kSumRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
-              "the shares exceed what the CTA was launched with");
+constexpr int kThreads = (kMultiplyWarp + 1) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kOkTiles = 4;
 
-// Shared memory (from a 1024-byte boundary).
-constexpr uint32_t kSlotBytes = 2 * kChunkBytes;                // a pair of chunks
-constexpr uint32_t kQuery = 2 * kSlotBytes;                     // 8 chunks of 128 rows
-constexpr uint32_t kRing = kQuery + kChunks * kRows * 128;      // codes on their way
-constexpr uint32_t kShared = kRing + 2 * kRingSlot;
+// Shared memory (from a 1024-byte boundary): 8 chunks of 128 rows, then what is on
+// its way, a tile: 64 bytes a key for pairs 0..2, 32 of codes and 128 of rope for pair 3.
+constexpr uint32_t kQuery = 0;
+constexpr uint32_t kRing = kQuery + kChunks * kRows * 128;
+constexpr uint32_t kRope = kRing + 4 * kTileKeys * 64;
+constexpr uint32_t kShared = kRope + kTileKeys * 128;
+
+// Tensor memory, 512 columns: S^T of two tiles, then the keys.
+constexpr uint32_t kKeysAt = 2 * kRows;
 
 struct Shared {
-    uint64_t full[2], free[2], scores[2], scores_free[2], query, query_free;
+    uint64_t staged[4], staged_free[4], scores[2], scores_free[2], query, query_free;
     uint32_t tmem;
     int scratch[18];
     alignas(16) float lse[kRows];
     int seen_to[kRows], seen_from[kRows];
     float part[kTileKeys];
-    uint8_t key_ok[kOkTiles][kTileKeys];
+    uint32_t key_ok[kOkTiles][4];  // a bit a key
 };
 constexpr size_t kSmemBytes = kShared + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "too much shared memory");
@@ -112,26 +114,82 @@ __device__ __forceinline__ int pass_rows(const WParams &w, int pass)
 
 // ---- Warps 8..23: cache rows and queries into operands
 
-template <int team>
-__device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_t *smem, Sweep sw)
+// `pieces` (<= kPlaces) 16-byte pieces of the warp's 32 keys into shared memory, kPlaces
+// places a key side by side, from byte `at` of each row on: neighbouring lanes copy
+// neighbouring pieces.  A key's pieces are permuted by `turn` of it, so that 8 lanes
+// reading one piece each of their own keys meet different banks.
+template <int kPlaces>
+__device__ __forceinline__ uint32_t turn(int key)
+{
+    return uint32_t(kPlaces == 8 ? key : key >> 1) & (kPlaces - 1);
+}
+
+template <int kPlaces>
+__device__ __forceinline__ void copy_pieces(const AParams &p, uint32_t to, int lane, const uint8_t *row,
+                                            int at, int pieces)
+{
+    const int piece = lane % kPlaces;
+#pragma unroll
+    for (int k = 0; k < kPlaces; ++k) {
+        const int key = lane / kPlaces + 32 / kPlaces * k;
+        const uint64_t from = __shfl_sync(kFull, reinterpret_cast<uint64_t>(row), key);
+        if (piece < pieces)
+            copy16(p, to + key * (16 * kPlaces) + ((piece ^ turn<kPlaces>(key)) << 4),
+                   reinterpret_cast<const uint8_t *>(from) + at + 16 * piece, from != 0u);
+    }
+}
+
+template <int kPlaces>
+__device__ __forceinline__ uint4 piece_of(uint32_t at, int lane, int piece)
+{
+    return load_shared16(at + lane * (16 * kPlaces) + ((piece ^ turn<kPlaces>(lane)) << 4));
+}
+
+// 32 dims of a key: 16 bytes of codes with their scale
+__device__ __forceinline__ void convert_group(uint4 codes, uint32_t scale, uint4 *out)
+{
+    const uint32_t scale2 = fp4_operand_scale(scale & 255u);
+    out[0] = mul_bf16x8(fp4x8_small(codes.x), scale2);
+    out[1] = mul_bf16x8(fp4x8_small(codes.y), scale2);
+    out[2] = mul_bf16x8(fp4x8_small(codes.z), scale2);
+    out[3] = mul_bf16x8(fp4x8_small(codes.w), scale2);
+}
+
+// A warpgroup converts one pair of chunks, a thread a key: 128 dims, pair 3's the codes
+// of chunk 6 and the rope dims.  The next tile's bytes are copied as soon as this
+// one's are read.  The pair is no template argument: the warps' loops have to fit the
+// instruction cache together.
+__device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_t *smem, Sweep sw,
+                                             const int pair)
 {
     const AParams &p = w.p;
-    const int tid = threadIdx.x - kConvertWarp * 32 - team * kTeam;
-    const int key = tid >> 1, half = tid & 1, lane = tid & 31;
-    const uint32_t base = smem_addr(smem), slot = base + kRing + team * kRingSlot;
-    const uint32_t place = swizzled(key, 4 * half), to = base + team * kSlotBytes;
+    const int tid = threadIdx.x - kConvertWarp * 32, lane = tid & 31, warp = (tid >> 5) & 3;
+    const int key = warp * 32 + lane;
+    const uint32_t ring = smem_addr(smem) + kRing + pair * (kTileKeys * 64) + warp * 2048;
+    const uint32_t rope = smem_addr(smem) + kRope + warp * 4096;
+    const uint32_t staged = s.tmem + (uint32_t(warp * 32) << 16) + kKeysAt + pair * 64;
+    const auto copy = [&](const Fp4Row &row) {
+        copy_pieces<4>(p, ring, lane, row.data, 64 * pair, pair < 3 ? 4 : 2);
+        if (pair == 3)
+            copy_pieces<8>(p, rope, lane, row.data, kFp4Codes, 8);
+    };
+    const auto load_scales = [&](const Fp4Row &row) {
+        return row.data != nullptr ? ldg4_now_in(row.scale + 4 * pair, cache_span(p.a.b), p.a.b.err) : 0u;
+    };
     KeyPlace now = key_place(p, sw.at(), true, key);
     int now_pass = 0;
     Fp4Row row = row_at(p, now);
-    copy_codes<team>(p, slot, tid, row);
-    uint4 scales = load_raw(p, row.scale, row.data != nullptr);
+    copy(row);
+    uint32_t scales = load_scales(row);
+    bool there = row.data != nullptr;
     sw.advance(w);
     KeyPlace next = key_place(p, sw.at(), sw.new_pass, key);
     bool next_live = sw.live;
     int next_pass = sw.pass;
     uint32_t passes = 0;
     for (uint32_t t = 0;; ++t) {
-        const Fp4Row next_row = row_at(p, next);
+        row = row_at(p, next);
+        const uint32_t next_scales = load_scales(row);
         KeyPlace after = next;
         after.off = UINT32_MAX;
         bool after_live = false;
@@ -142,16 +200,12 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
             after_live = sw.live;
             after_pass = sw.pass;
         }
-        const uint4 next_scales = load_raw(p, next_row.scale, next_row.data != nullptr);
-        if constexpr (team == 1)
-            prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
         bool alive = true;
         if (now.unit < 0) {
             if (passes > 0)
                 alive = __all_sync(kFull, mbar_wait(&s.query_free, (passes - 1) & 1));
             if (alive) {
-                load_query(p, ~now.unit, now_pass * kRows, smem + kQuery, kRows, tid + team * kTeam,
-                           2 * kTeam);
+                load_query(p, ~now.unit, now_pass * kRows, smem + kQuery, kRows, tid, 512);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -159,58 +213,44 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
             }
             ++passes;
         }
-        uint4 rope[4];
-        const auto pair = [&](auto ci) {
-            constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1, this slot's use 2t + i / 2
-            const uint32_t use = 2 * t + i / 2;
-            copy_wait();
-            const uint4 a = load_shared16(slot + tid * 16);
-            uint4 b = a, out[4];
-            if constexpr (i < 3)
-                b = load_shared16(slot + 4096 + tid * 16);
-            if constexpr (i < 2)
-                copy_codes<i + 2>(p, slot, tid, row);
-            else
-                copy_codes<i - 2>(p, slot, tid, next_row);
-            convert_codes<2 * i>(scales, a, half, out);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                computed(out[k]);  // before the wait for its place
-            if (use > 0 && alive)
-                alive = __all_sync(kFull, mbar_wait(&s.free[team], (use - 1) & 1));
-            if (!alive)
-                return;
-            if (i == 0 && half == 0)
-                s.key_ok[t % kOkTiles][key] = row.data != nullptr ? 1 : 0;
-            store_half(to, place, out);
-            if constexpr (i < 3) {
-                convert_codes<2 * i + 1>(scales, b, half, out);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    out[k] = mul_bf16x8(rope[k], kRopeToOperand);
-            }
-            store_half(to + kChunkBytes, place, out);
-            if constexpr (i == 1) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    rope[k] = load_raw(p, row.data + kFp4Codes + 64 * half + 16 * k, row.data != nullptr);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+        if (pair == 0) {
+            const uint32_t bits = __ballot_sync(kFull, there);
             if (lane == 0)
-                mbar_arrive(&s.full[team]);
-        };
-        pair(std::integral_constant<int, team>{});
-        pair(std::integral_constant<int, team + 2>{});
+                s.key_ok[t % kOkTiles][warp] = bits;
+        }
+        copy_wait();
+        __syncwarp();  // the copies are the warp's together
+        if (t > 0 && alive)
+            alive = __all_sync(kFull, mbar_wait(&s.staged_free[pair], (t - 1) & 1));
         if (!alive) {
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
             break;
         }
+        tmem_fence_after();
+        __syncwarp();
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+            uint4 out[4];
+            if (pair < 3 || g < 2) {
+                convert_group(piece_of<4>(ring, lane, g), scales >> (8 * g), out);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    out[k] = mul_bf16x8(piece_of<8>(rope, lane, 4 * (g - 2) + k), kRopeToOperand);
+            }
+            __syncwarp();
+            tmem_store16(staged + 16 * g, out);
+        }
+        tmem_wait_store();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&s.staged[pair]);
         if (!next_live)
             break;
+        copy(row);
         scales = next_scales;
-        row = next_row;
+        there = row.data != nullptr;
         now = next;
         now_pass = next_pass;
         next = after;
@@ -225,7 +265,7 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
 __device__ __forceinline__ void multiply_role(const WParams &w, Shared &s, uint32_t smem, Sweep sw)
 {
     const uint32_t elected = elect_one();
-    const Operand keys = operand(smem, 16, 1024), query = operand(smem + kQuery, 16, 1024);
+    const Operand query = operand(smem + kQuery, 16, 1024);
     uint32_t inst = 0, passes = 0;
     for (uint32_t t = 0; sw.live; ++t) {
         bool alive = true;
@@ -240,16 +280,16 @@ __device__ __forceinline__ void multiply_role(const WParams &w, Shared &s, uint3
         const uint32_t d = s.tmem + (t & 1) * kRows;
 #pragma unroll
         for (int i = 0; i < kChunks / 2; ++i) {
-            alive = alive && __all_sync(kFull, mbar_wait(&s.full[i & 1], (2 * t + i / 2) & 1));
+            alive = alive && __all_sync(kFull, mbar_wait(&s.staged[i], t & 1));
             if (!alive)
                 break;
             tmem_fence_after();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                mma_bf16(d, keys + ((i & 1) * kSlotBytes + (k >> 2) * kChunkBytes + 32 * (k & 3)),
-                         query + ((2 * i + (k >> 2)) * kRows * 128 + 32 * (k & 3)), inst, i > 0 || k > 0,
-                         elected);
-            mma_commit(&s.free[i & 1], elected);
+                mma_bf16_staged(d, s.tmem + kKeysAt + i * 64 + k * 8,
+                                query + ((2 * i + (k >> 2)) * kRows * 128 + 32 * (k & 3)), inst,
+                                i > 0 || k > 0, elected);
+            mma_commit(&s.staged_free[i], elected);
         }
         if (!alive) {
             flag(w.p.a.b.err, DSV4_DEVERR_TIMEOUT);
@@ -345,7 +385,7 @@ __device__ __forceinline__ void sum_role(const WParams &w, Shared &s, Sweep sw)
         if (group == 1)
             s.part[key] = total;
         named_barrier(1, 256);
-        if (add && s.key_ok[t % kOkTiles][key] != 0)
+        if (add && ((s.key_ok[t % kOkTiles][warp] >> lane) & 1u) != 0u)
             st_f32_in(to, before + (total + s.part[key]), ws, a.b.err);
         sw.advance(w);
     }
@@ -368,9 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_weights_kernel(const __grid_c
     if (warp == kMultiplyWarp) {
         tmem_alloc512(&s.tmem);
         if ((threadIdx.x & 31) == 0) {
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&s.staged[i], 4);
+                mbar_init(&s.staged_free[i], 1);
+            }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&s.full[i], 8);
-                mbar_init(&s.free[i], 1);
                 mbar_init(&s.scores[i], 1);
                 mbar_init(&s.scores_free[i], 4 * kGroups);
             }
@@ -385,15 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_weights_kernel(const __grid_c
     if (warp < kConvertWarp) {
         sum_role(w, s, sw);
     } else if (warp < kMultiplyWarp) {
-        registers_up<kConvertRegs>();
-        if (warp < kConvertWarp + 8)
-            convert_role<0>(w, s, smem, sw);
-        else
-            convert_role<1>(w, s, smem, sw);
-    } else {
-        registers_down<kMultiplyRegs>();
-        if (warp == kMultiplyWarp)
-            multiply_role(w, s, smem_addr(smem), sw);
+        convert_role(w, s, smem, sw, (warp - kConvertWarp) / 4);
+    } else if (warp == kMultiplyWarp) {
+        multiply_role(w, s, smem_addr(smem), sw);
     }
     tmem_fence_before();
     __syncthreads();

@@ -99,6 +99,17 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, Operand a, Operand b, uint3
                  : "memory");
 }
 
+// the same with a in tensor memory: 8 columns, two bf16 each, of the 128 lanes
+__device__ __forceinline__ void mma_bf16_staged(uint32_t d, uint32_t a, Operand b, uint32_t inst,
+                                                bool accumulate, uint32_t elected)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
+                 "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 e, %6, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b.low), "r"(b.high), "r"(inst), "r"(accumulate ? 1u : 0u), "r"(elected)
+                 : "memory");
+}
+
 // arrive on *bar once every matrix instruction the elected lane has issued is done
 __device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t elected)
 {
@@ -136,6 +147,18 @@ __device__ __forceinline__ void tmem_store16(uint32_t address, const float *v)
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(address),
         "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
         "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+}
+
+// 16 columns from 4 vectors
+__device__ __forceinline__ void tmem_store16(uint32_t address, const uint4 *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(address),
+        "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z),
+        "r"(v[1].w), "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y),
+        "r"(v[3].z), "r"(v[3].w)
         : "memory");
 }
 
