@@ -427,7 +427,7 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
  *  seq_lens     (device) int32 [batch]: keys of each request, its q_len new tokens included;
  *               0 is an idle request.  Token j sees keys [max(0, n - window), n) with
  *               n = seq_lens[b] - q_len + 1 + j (all of [0, n) for window 0).
- *  scale        of the scores, finite and > 0:  s = scale * (q . k).
+ *  scale        of the scores, in (0, 2^32]:  s = scale * (q . k).
  *  sinks        (device, nullable) fp32 [num_heads]: a score that takes part in the softmax
  *               of its head and has no value.
  *  out          (device) bf16 [batch, q_len, num_heads, 512], 16-byte aligned; may not overlap q.
@@ -439,7 +439,8 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
  *               that may run at the same time need two.
  *
  * Scores and sums are fp32; the probabilities are rounded to bf16 for the product with
- * the rows.  A key past every token's length, or outside every window, is not read, whatever its slot holds;
+ * the rows.  Rows are taken as they are stored while their values are below 2^83 (above,
+ * as infinite).  A key past every token's length, or outside every window, is not read, whatever its slot holds;
  * the keys that some tokens of a request see and others do not must be finite.
  * A block outside [0, num_blocks) sets DSV4_DEVERR_SLOT_RANGE and its keys take no part;
  * a length past table_width * block_size sets it too and counts as that many.

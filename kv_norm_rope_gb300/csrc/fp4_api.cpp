@@ -72,7 +72,7 @@ int check_attention(int32_t q_len, int32_t num_heads, int32_t batch, float scale
     // tiles of 64 rows and 128 keys are counted in 32 bits
     if (((int64_t(q_len) * num_heads + 63) / 64) * batch > INT32_MAX / ((most_keys + 127) / 128))
         return DSV4_ERR_SHAPE;
-    if (!(scale > 0.0f) || !std::isfinite(scale))
+    if (!(scale > 0.0f && scale <= 4294967296.0f))  // it is multiplied by 2^82 in fp32
         return DSV4_ERR_VALUE;
     return DSV4_OK;
 }

@@ -56,7 +56,7 @@ static_assert(128 * (kGroups * kSoftmaxRegs + 4 * kConvertRegs + kMultiplyRegs) 
               "the shares exceed what the CTA was launched with");
 constexpr int kMaxCtas = 256;        // of a launch: what the workspace is for
 constexpr float kSlack = 16.0f;
-constexpr float kUnset = -1e30f;     // m of a row that has seen no key
+constexpr float kUnset = -3.402823466e38f;  // m of a row that has seen no key: below any score
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -65,6 +65,7 @@ _QUERY = [
     (dict(Q=2**20, H=2**20), k.ERR_SHAPE), (dict(Q=2**15, H=2**10, batch=65535), k.ERR_SHAPE),
     (dict(scale=0.0), k.ERR_VALUE), (dict(scale=-1.0), k.ERR_VALUE),
     (dict(scale=math.inf), k.ERR_VALUE), (dict(scale=math.nan), k.ERR_VALUE),
+    (dict(scale=2.0**33), k.ERR_VALUE),
     (dict(q=None), k.ERR_NULL), (dict(q=A + 8), k.ERR_ALIGN),
 ]
 

@@ -393,6 +393,27 @@ def test_attention_values_of_the_lowest_kind():
     assert torch.isfinite(out[0, 0, 0]).all() and torch.isfinite(out[1]).all()
 
 
+def test_attention_scores_far_below_zero():
+    """Every score of a row hugely negative: the softmax is of their differences alone."""
+    s = Batch([300], 1, 4, 16, seed=25)
+    q = s.q64.copy()
+    q[...] = 0.0
+    cache = s.cache_np
+    for i in range(300):
+        data, _ = fp4.row_bytes(cache, 16, s.table_np[0, i // 16] * 16 + i % 16)
+        data[224:226] = torch.tensor([1.0]).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint8)
+    s.cache = dev(cache)
+    s.rows[0], s.ok[0] = fp4.rows_of(cache, 16, s.table_np[0], 300)
+    q[..., 448] = -np.exp2(np.array([10.0, 40.0, 80.0, 110.0]))  # the same score for every key
+    s.q, s.q64 = bf16(q)
+    out, lse = s.attention()
+    got = out.double().cpu().numpy()[0, 0]
+    want = s.rows[0].mean(0)
+    size = np.abs(s.rows[0]).mean(0)
+    assert np.all(np.abs(got - want) <= np.abs(want) * 2.0 ** -8 + size * 2.0 ** -7)
+    assert np.allclose(lse[0, 0].double().cpu().numpy(), s.scale * q[0, 0, :, 448] + np.log(300), rtol=2.0 ** -20, atol=0)
+
+
 def test_attention_bad_pages_and_lengths():
     """A block outside the cache takes no part and is flagged; so is a length past the table."""
     s = Batch([300, 100, 50], 1, 8, 16, seed=14)
