@@ -54,7 +54,7 @@ constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three w
 constexpr int kSoftmaxRegs = 88, kConvertRegs = 72, kMultiplyRegs = 40;
 static_assert(128 * (kGroups * kSoftmaxRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
               "the shares exceed what the CTA was launched with");
-constexpr int kMaxCtas = 256;        // of a launch: what the workspace is for
+constexpr int kMaxCtas = 160;        // of a launch: what the workspace is for
 constexpr float kSlack = 16.0f;
 constexpr float kUnset = -3.402823466e38f;  // m of a row that has seen no key: below any score
 constexpr float kLog2e = 1.4426950408889634f;

@@ -677,3 +677,34 @@ def test_all_in_a_graph():
     torch.cuda.synchronize()
     for name in eager:
         assert torch.equal(eager[name].view(torch.uint8), captured[name].view(torch.uint8)), name
+
+
+# ---------------------------------------------------------------- together
+
+def test_example_runs_and_keeps_the_attention_of_what_stays():
+    """The example's decoding loop: every step gives each request `heads` of attention in all,
+    and an eviction keeps the weights of the rows that stay."""
+    from examples import fp4_cache_decode
+    lens, weights, x = fp4_cache_decode.main(steps=96, batch=3, heads=16, limit=64, budget=40, recent=8)
+    assert lens == [48, 48, 48]  # 64, cut to 40, up to 64, cut to 40, and 8 more
+    assert torch.isfinite(x).all() and bool((weights[:, 48:] == 0).all())
+    # 96 steps of 16 heads, less what left with the evicted rows
+    assert bool((weights.sum(1) <= 96 * 16 * (1 + 1e-3)).all()) and bool((weights.sum(1) > 8 * 16).all())
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    """Seeded random sizes through attention, weights and eviction."""
+    rng = np.random.default_rng(1000 + seed)
+    H, Q = int(rng.integers(1, 140)), int(rng.choice([1, 1, 2, 5, 9]))
+    B, block = int(rng.integers(1, 7)), int(rng.choice([1, 3, 16, 27, 64, 200]))
+    lens = [int(x) for x in rng.integers(0, int(rng.choice([5, 140, 600])), B)]
+    window = int(rng.choice([0, 0, 1, 40, 300]))
+    s = Batch(lens, Q, H, block, seed=seed, stride=int(rng.integers(0, 3)), gain=float(rng.choice([0.1, 1, 4])))
+    sinks = dev(rng.standard_normal(H) * 3, np.float32) if rng.random() < 0.5 else None
+    out, lse = s.attention(window=window, sinks=sinks)
+    s.check(out, lse, window, sinks)
+    check_weights(s, window, stride=int(rng.integers(0, 5)))
+    n = max(max(lens), 1)
+    budget = int(rng.integers(1, n + 3))
+    check_evict(lens, budget, int(rng.integers(0, budget + 1)), block, seed=seed, alias=bool(rng.random() < 0.5))
