@@ -19,7 +19,7 @@
 //    own, so the next tile is converted under the products of this one.
 //  * Warps 0..7 do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
 //    32 (w / 4)..; a thread has one key and 32 rows.  Warps 8..23 convert, warp 24
-//    issues the products.  Registers move from that warpgroup to the softmax: a spill
+//    issues the products.  Registers move from those two to the softmax: a spill
 //    costs a trip to L2, as shared memory leaves little of L1.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the
 //    largest score of the first tile it saw; p = 2^(x - m) is taken against that,
@@ -51,7 +51,7 @@ constexpr int kCols = kRows / kGroups;
 constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
 constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three warps idle
 // registers a thread: 72 at launch (896 * 72 = 64512), then
-constexpr int kSoftmaxRegs = 88, kConvertRegs = 72, kMultiplyRegs = 40;
+constexpr int kSoftmaxRegs = 96, kConvertRegs = 64, kMultiplyRegs = 56;
 static_assert(128 * (kGroups * kSoftmaxRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
               "the shares exceed what the CTA was launched with");
 constexpr int kMaxCtas = 160;        // of a launch: what the workspace is for
@@ -89,7 +89,7 @@ struct Shared {
     uint64_t full[kChunks / 2], free[kChunks / 2];  // of a pair of chunks
     uint64_t scores, probs, query, query_free, output;
     uint32_t tmem;
-    int scratch[18];
+    int scratch[kDealWords];
     alignas(16) float m[kRows];
     alignas(16) float factor[kRows];
     float warp_rows[4][kRows];  // maxima or sums of the four warps' keys
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     Shared &s = *reinterpret_cast<Shared *>(smem + kShared);
     const AParams &p = w.p;
     const int warp = threadIdx.x >> 5;
-    let_kernel_after_begin();
+    wait_for_kernel_before();
     if ((smem_addr(smem) & 1023u) != 0u) {  // never: there is no static shared memory
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
         return;
@@ -570,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         registers_up<kSoftmaxRegs>();
         softmax_role(w, s, smem, c);
     } else if (warp < kMultiplyWarp) {
+        registers_down<kConvertRegs>();
         if (warp < kConvertWarp + 8)
             convert_role<0>(p, s, smem, c);
         else
@@ -744,8 +745,8 @@ int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_
     int runs = sms < kMaxCtas ? sms : kMaxCtas;
     runs = most < runs ? int(most) : runs;
     w.runs = runs;
-    const int st = launch_kernel(fp4_attention_kernel, dim3(unsigned(runs)), dim3(kThreads), kSmemBytes,
-                                 stream, w);
+    const int st = launch_after(fp4_attention_kernel, dim3(unsigned(runs)), dim3(kThreads), stream, w,
+                                kSmemBytes);
     if (st != DSV4_OK)
         return st;
     const unsigned rows = unsigned(w.p.all_rows < kRows ? w.p.all_rows : kRows);

@@ -82,6 +82,7 @@ __device__ __forceinline__ int64_t load_slot(const GParams &p, int64_t n)
 
 __global__ void __launch_bounds__(kThreads, 12) fp4_gather_kernel(const GParams p)
 {
+    wait_for_kernel_before();
     const int lane = threadIdx.x & 31;
     const int64_t stride = int64_t(gridDim.x) * (kThreads / 32);
     int64_t n = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -131,8 +132,8 @@ int launch_fp4_gather(const uint8_t *cache, int64_t num_blocks, int32_t block_si
     p.out = out;
     p.err = err;
     const int64_t need = (rows + kThreads / 32 - 1) / (kThreads / 32);
-    return launch_kernel(fp4_gather_kernel, dim3(unsigned(need < max_ctas ? need : max_ctas)),
-                         dim3(kThreads), 0, stream, p);
+    return launch_after(fp4_gather_kernel, dim3(unsigned(need < max_ctas ? need : max_ctas)),
+                        dim3(kThreads), stream, p);
 }
 
 }  // namespace dsv4

@@ -133,25 +133,43 @@ __device__ __forceinline__ int tiles_of(const AParams &p, int unit)
 }
 
 // Places c at the start of CTA x's run.  All threads of the CTA (at least
-// kDealThreads) call it.  scratch: 18 words of shared memory.
+// kDealThreads) call it.  scratch: kDealWords words of shared memory.
 constexpr int kDealThreads = 512;
+constexpr int kDealWarps = kDealThreads / 32;
+constexpr int kDealWords = 2 * kDealWarps + 2;
 
 __device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratch, Cursor &c)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const auto count = [&](int base) {
-        return tid < kDealThreads && base + tid < p.units ? tiles_of(p, base + tid) : 0;
+    // the units from `base` on, one a thread: their tiles up to and with the thread's
+    // own, and all of them; `half` of the scratch words, so that calls in turn need
+    // one barrier each
+    int upto = 0, mine = 0, all = 0;
+    const auto scan = [&](int base, int half) {
+        mine = tid < kDealThreads && base + tid < p.units ? tiles_of(p, base + tid) : 0;
+        upto = mine;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int o = __shfl_up_sync(kFull, upto, s);
+            if (lane >= s)
+                upto += o;
+        }
+        int *sums = scratch + half * kDealWarps;
+        if (lane == 31 && warp < kDealWarps)
+            sums[warp] = upto;
+        __syncthreads();
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < kDealWarps; ++w) {
+            if (w < warp)
+                upto += sums[w];
+            all += sums[w];
+        }
     };
-    int total = 0, mine = 0;
-    for (int base = 0; base < p.units; base += kDealThreads) {
-        mine = count(base);
-        const int sum = __reduce_add_sync(kFull, mine);
-        if (lane == 0 && warp < kDealThreads / 32)
-            scratch[warp] = sum;
-        __syncthreads();
-        for (int w = 0; w < kDealThreads / 32; ++w)
-            total += scratch[w];
-        __syncthreads();
+    int total = 0, half = 0;
+    for (int base = 0; base < p.units; base += kDealThreads, half ^= 1) {
+        scan(base, half);
+        total += all;
     }
     const int share = (total + X - 1) / X;
     const int64_t begin = int64_t(x) * share;
@@ -159,37 +177,19 @@ __device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratc
     if (c.left == 0)
         return;
     const int t0 = int(begin);
-    int before = 0;
-    for (int base = 0; base < p.units && before <= t0; base += kDealThreads) {
+    for (int base = 0, before = 0; base < p.units && before <= t0; base += kDealThreads, half ^= 1) {
         if (p.units > kDealThreads)
-            mine = count(base);
-        int upto = mine;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int o = __shfl_up_sync(kFull, upto, s);
-            if (lane >= s)
-                upto += o;
+            scan(base, half);
+        if (mine > 0 && before + upto - mine <= t0 && t0 < before + upto) {
+            scratch[2 * kDealWarps] = base + tid;
+            scratch[2 * kDealWarps + 1] = t0 - (before + upto - mine);
         }
-        if (lane == 31 && warp < kDealThreads / 32)
-            scratch[warp] = upto;
-        __syncthreads();
-        int start = before;
-        for (int w = 0; w < kDealThreads / 32; ++w) {
-            if (w < warp)
-                start += scratch[w];
-            before += scratch[w];
-        }
-        upto += start;
-        if (mine > 0 && upto - mine <= t0 && t0 < upto) {
-            scratch[16] = base + tid;
-            scratch[17] = t0 - (upto - mine);
-        }
-        __syncthreads();
+        before += all;
     }
-    c.unit = scratch[16];
+    __syncthreads();
+    c.unit = scratch[2 * kDealWarps];
     c.enter(p);
-    c.tile = c.range.first() + scratch[17];
-    __syncthreads();  // scratch may be used again
+    c.tile = c.range.first() + scratch[2 * kDealWarps + 1];
 }
 
 // ---- Cache rows -> operand

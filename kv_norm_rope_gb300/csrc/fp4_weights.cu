@@ -51,7 +51,7 @@ constexpr uint32_t kKeysAt = 2 * kRows;
 struct Shared {
     uint64_t staged[4], staged_free[4], scores[2], scores_free[2], query, query_free;
     uint32_t tmem;
-    int scratch[18];
+    int scratch[kDealWords];
     alignas(16) float lse[kRows];
     int seen_to[kRows], seen_from[kRows];
     float part[kTileKeys];
@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_weights_kernel(const __grid_c
     Shared &s = *reinterpret_cast<Shared *>(smem + kShared);
     const int warp = threadIdx.x >> 5;
     Sweep sw;
+    wait_for_kernel_before();
     deal(w.p, blockIdx.x, gridDim.x, s.scratch, sw.c);
     if (sw.c.left == 0)
         return;
@@ -469,8 +470,8 @@ int launch_fp4_weights(const Fp4AttentionArgs &a, cudaStream_t stream)
     w.p = tile_params(a, a.q_len * a.heads);
     w.passes = (w.p.all_rows + kRows - 1) / kRows;
     const int64_t most = (int64_t(a.b.width) * a.b.block_size + kTileKeys - 1) / kTileKeys * w.p.units;
-    return launch_kernel(fp4_weights_kernel, dim3(unsigned(most < sms ? most : sms)), dim3(kThreads),
-                         kSmemBytes, stream, w);
+    return launch_after(fp4_weights_kernel, dim3(unsigned(most < sms ? most : sms)), dim3(kThreads),
+                        stream, w, kSmemBytes);
 }
 
 }  // namespace dsv4

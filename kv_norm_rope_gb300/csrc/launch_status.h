@@ -51,7 +51,8 @@ inline int launch_cluster(void (*kernel)(P), dim3 grid, dim3 block, unsigned clu
 // of it that reads what that kernel writes, and at least one thread of every CTA,
 // calls wait_for_kernel_before() first.
 template <typename P>
-inline int launch_after(void (*kernel)(P), dim3 grid, dim3 block, cudaStream_t stream, const P &p)
+inline int launch_after(void (*kernel)(P), dim3 grid, dim3 block, cudaStream_t stream, const P &p,
+                        size_t smem = 0)
 {
     void *args[] = {const_cast<P *>(&p)};
     cudaLaunchAttribute attr = {};
@@ -60,6 +61,7 @@ inline int launch_after(void (*kernel)(P), dim3 grid, dim3 block, cudaStream_t s
     cudaLaunchConfig_t config = {};
     config.gridDim = grid;
     config.blockDim = block;
+    config.dynamicSmemBytes = smem;
     config.stream = stream;
     config.attrs = &attr;
     config.numAttrs = 1;
