@@ -19,8 +19,10 @@
 //    own, so the next tile is converted under the products of this one.
 //  * Warps 0..7 do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
 //    32 (w / 4)..; a thread has one key and 32 rows.  Warps 8..23 convert, warp 24
-//    issues the products.  Registers move from those two to the softmax: a spill
-//    costs a trip to L2, as shared memory leaves little of L1.
+//    issues the products.  The teams of converting warps share one code path, so
+//    that all loops fit the instruction cache together, and warp 24's warpgroup gives
+//    registers to the softmax: a spill costs a trip to L2, as shared memory leaves
+//    little of L1.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the
 //    largest score of the first tile it saw; p = 2^(x - m) is taken against that,
 //    and only when some x exceeds m by more than kSlack is m moved and everything
@@ -51,7 +53,7 @@ constexpr int kCols = kRows / kGroups;
 constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
 constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three warps idle
 // registers a thread: 72 at launch (896 * 72 = 64512), then
-constexpr int kSoftmaxRegs = 96, kConvertRegs = 64, kMultiplyRegs = 56;
+constexpr int kSoftmaxRegs = 88, kConvertRegs = 72, kMultiplyRegs = 40;
 static_assert(128 * (kGroups * kSoftmaxRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
               "the shares exceed what the CTA was launched with");
 constexpr int kMaxCtas = 160;        // of a launch: what the workspace is for
@@ -113,8 +115,8 @@ __device__ __forceinline__ float unordered(int i)
 
 // ---- Warps 8..23: cache rows and queries into operands
 
-template <int team>
-__device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c)
+__device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c,
+                                             const int team)
 {
     const int tid = threadIdx.x - kConvertWarp * 32 - team * kTeam;
     const int key = tid >> 1, half = tid & 1, lane = tid & 31;
@@ -123,7 +125,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
     const uint32_t place = swizzled(key, 4 * half);
     KeyPlace now = key_place(p, c, true, key);
     Fp4Row row = row_at(p, now);
-    copy_codes<team>(p, slot, tid, row);
+    copy_codes(p, slot, tid, row, team);
     uint4 scales = load_raw(p, row.scale, row.data != nullptr);
     const auto fill_query = [&] {
         const int unit = ~now.unit, request = int(fastdiv(uint32_t(unit), p.tile_div));
@@ -146,7 +148,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
             after = key_place(p, c, moved, key);
         }
         const uint4 next_scales = load_raw(p, next_row.scale, next_row.data != nullptr);
-        if constexpr (team == 1)
+        if (team == 1)
             prefetch64(p, row.data + kFp4Codes + 64 * half, row.data != nullptr);
         bool alive = true;
         if (now.unit < 0 && t > 0) {
@@ -156,38 +158,36 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
             ++segment;
         }
         uint4 rope[4];
-        const auto pair = [&](auto ci) {
-            constexpr int i = decltype(ci)::value;  // chunks 2i and 2i + 1
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = team + 2 * u;  // chunks 2i and 2i + 1
             const uint32_t to = base + kKeys + 2 * i * kChunkBytes;
             copy_wait();
-            const uint4 a = load_shared16(slot + tid * 16);
-            uint4 b = a, out[4];
-            if constexpr (i < 3)
-                b = load_shared16(slot + 4096 + tid * 16);
-            if constexpr (i < 2)
-                copy_codes<i + 2>(p, slot, tid, row);
-            else
-                copy_codes<i - 2>(p, slot, tid, next_row);
-            convert_codes<2 * i>(scales, a, half, out);
+            const uint4 a = load_shared16(slot + tid * 16), b = load_shared16(slot + 4096 + tid * 16);
+            uint4 out[4];
+            copy_codes(p, slot, tid, u == 0 ? row : next_row, u == 0 ? i + 2 : team);
+            const uint32_t four = (i < 2 ? (i == 0 ? scales.x : scales.y) : i == 2 ? scales.z : scales.w) >>
+                                  (8 * half);
+            convert_group(a, four, out);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 computed(out[k]);  // before the wait for its place
             if (t > 0 && alive)
                 alive = __all_sync(kFull, mbar_wait(&s.free[i], (t - 1) & 1));
             if (!alive)
-                return;
+                break;
             if (i == 0 && half == 0)
                 s.key_ok[key] = row.data != nullptr ? 1 : 0;
             store_half(to, place, out);
-            if constexpr (i < 3) {
-                convert_codes<2 * i + 1>(scales, b, half, out);
+            if (i < 3) {
+                convert_group(b, four >> 16, out);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     out[k] = mul_bf16x8(rope[k], kRopeToOperand);
             }
             store_half(to + kChunkBytes, place, out);
-            if constexpr (i == 1) {
+            if (i == 1) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     rope[k] = load_raw(p, row.data + kFp4Codes + 64 * half + 16 * k, row.data != nullptr);
@@ -196,9 +196,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&s.full[i]);
-        };
-        pair(std::integral_constant<int, team>{});
-        pair(std::integral_constant<int, team + 2>{});
+        }
         if (!alive) {
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
             break;
@@ -570,11 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         registers_up<kSoftmaxRegs>();
         softmax_role(w, s, smem, c);
     } else if (warp < kMultiplyWarp) {
-        registers_down<kConvertRegs>();
-        if (warp < kConvertWarp + 8)
-            convert_role<0>(p, s, smem, c);
-        else
-            convert_role<1>(p, s, smem, c);
+        convert_role(p, s, smem, c, (warp - kConvertWarp) / 8);
     } else {
         registers_down<kMultiplyRegs>();
         if (warp == kMultiplyWarp)

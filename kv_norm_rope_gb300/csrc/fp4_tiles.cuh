@@ -250,13 +250,11 @@ __device__ __forceinline__ void copy16(const AParams &p, uint32_t to, const uint
 }
 
 // the thread's codes of pair i of chunks on their way into its place of a slot
-template <int i>
-__device__ __forceinline__ void copy_codes(const AParams &p, uint32_t slot, int tid, const Fp4Row &row)
+__device__ __forceinline__ void copy_codes(const AParams &p, uint32_t slot, int tid, const Fp4Row &row, int i)
 {
     const uint8_t *from = row.data + 64 * i + 16 * (tid & 1);
     copy16(p, slot + tid * 16, from, row.data != nullptr);
-    if constexpr (i < 3)
-        copy16(p, slot + 4096 + tid * 16, from + 32, row.data != nullptr);
+    copy16(p, slot + 4096 + tid * 16, from + 32, row.data != nullptr && i < 3);
 }
 
 // the thread's copies have landed
@@ -276,12 +274,10 @@ __device__ __forceinline__ void prefetch64(const AParams &p, const uint8_t *at, 
         asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 32];" ::"l"(at));
 }
 
-// 32 codes of chunk c (the thread's half) with their scale -> 32 bf16
-template <int c>
-__device__ __forceinline__ void convert_codes(uint4 scales, uint4 codes, int half, uint4 *out)
+// 32 dims of a key: 16 bytes of codes with their scale
+__device__ __forceinline__ void convert_group(uint4 codes, uint32_t scale, uint4 *out)
 {
-    const uint32_t four = c < 2 ? scales.x : c < 4 ? scales.y : c < 6 ? scales.z : scales.w;
-    const uint32_t scale2 = fp4_operand_scale((four >> (16 * (c & 1) + 8 * half)) & 255u);
+    const uint32_t scale2 = fp4_operand_scale(scale & 255u);
     out[0] = mul_bf16x8(fp4x8_small(codes.x), scale2);
     out[1] = mul_bf16x8(fp4x8_small(codes.y), scale2);
     out[2] = mul_bf16x8(fp4x8_small(codes.z), scale2);

@@ -145,16 +145,6 @@ __device__ __forceinline__ uint4 piece_of(uint32_t at, int lane, int piece)
     return load_shared16(at + lane * (16 * kPlaces) + ((piece ^ turn<kPlaces>(lane)) << 4));
 }
 
-// 32 dims of a key: 16 bytes of codes with their scale
-__device__ __forceinline__ void convert_group(uint4 codes, uint32_t scale, uint4 *out)
-{
-    const uint32_t scale2 = fp4_operand_scale(scale & 255u);
-    out[0] = mul_bf16x8(fp4x8_small(codes.x), scale2);
-    out[1] = mul_bf16x8(fp4x8_small(codes.y), scale2);
-    out[2] = mul_bf16x8(fp4x8_small(codes.z), scale2);
-    out[3] = mul_bf16x8(fp4x8_small(codes.w), scale2);
-}
-
 // A warpgroup converts one pair of chunks, a thread a key: 128 dims, pair 3's the codes
 // of chunk 6 and the rope dims.  The next tile's bytes are copied as soon as this
 // one's are read.  The pair is no template argument: the warps' loops have to fit the
