@@ -30,8 +30,8 @@
  *  - Conditions that need device data (a slot or a position out of range) are
  *    reported by OR-ing DSV4_DEVERR_* bits into *device_error (device int32,
  *    may be NULL) and skipping the affected writes.  Nothing traps or asserts
- *    on the device; the one kernel that waits on its own bulk copies bounds
- *    every wait (DSV4_DEVERR_TIMEOUT).
+ *    on the device; the kernels that wait inside (for their own copies and matrix
+ *    products) bound every wait (DSV4_DEVERR_TIMEOUT).
  *  - Preconditions that are not checked: non-negative slots are distinct (if
  *    two tokens share a slot, which one's row lands is unspecified); q does
  *    not overlap kv, the cache or the metadata arrays; inputs are finite and
@@ -87,9 +87,9 @@ enum {
 enum {
     DSV4_DEVERR_SLOT_RANGE = 1, /* slot_mapping[t] >= num_blocks*block_size: cache row not written */
     DSV4_DEVERR_POS_RANGE = 2,  /* positions[t] < 0 or >= max_position: token not written at all */
-    DSV4_DEVERR_TIMEOUT = 4,    /* the KV-row kernel (num_heads 0, STREAM): a bounded wait on a
-                                   bulk copy inside the kernel ran out (never expected); the
-                                   outputs of that launch are undefined */
+    DSV4_DEVERR_TIMEOUT = 4,    /* the KV-row kernel (num_heads 0, STREAM), the 4-bit attention or
+                                   its weights: a bounded wait inside the kernel ran out (never
+                                   expected); the outputs of that launch are undefined */
     DSV4_DEVERR_BOUNDS = 8      /* the checked build only (libdsv4kv_checked.so, compiled with
                                    DSV4_CHECK_BOUNDS): an access would have touched bytes outside
                                    the buffer it belongs to; it was skipped (never expected) */

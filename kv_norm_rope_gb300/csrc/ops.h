@@ -2,8 +2,8 @@
 // operations beside the whole-warp fused kernels: the half-warp fused kernel
 // (qnorm_rope_kv_insert_half.cu), the KV-row kernel for calls with no q
 // (kv_rows.cu), the MXFP8 activation quantiser (gemma_rmsnorm_mxfp8.cu), the
-// indexer-K insert and gather (indexer_k.cu) and the check of the bounded waits
-// (wait_check.cu).
+// indexer-K insert and gather (indexer_k.cu), the check of the bounded waits
+// (wait_check.cu) and the 4-bit cache's operators (fp4_*.cu).
 // Not installed; not part of the ABI.
 #pragma once
 
