@@ -3,6 +3,7 @@
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--workload stress]
     python bench.py --impl reference ...      # the CPU oracle on a bounded sample
+    python bench.py --op fp4 --case attention_long   # a case of the 4-bit cache
 
 A step is one pass of the whole fused step (one launch) over one batch: by default
 the "stress" workload, 131072 tokens x 128 q heads (q is 17.2 GB of bf16), FP8 cache
@@ -250,6 +251,7 @@ IO_OF_OP = {
     "indexer_gather": "indexer cache rows in; contiguous e4m3 [T, 128] + fp32 [T] out",
 }
 MXFP8_HIDDEN = 7168
+FP4_FLUSH_BYTES = 256 << 20  # larger than the 129 MB of L2
 VARIANTS = {"auto": 0, "small": 1, "stream": 2, "half": 4}
 
 
@@ -1121,6 +1123,45 @@ def run_ours(args):
     return 0
 
 
+def run_fp4(args):
+    """One case of perf/operators.py through the package's entry points: the median over
+    K passes of the time between events around a pass, each after a write larger than L2
+    (which also lets the host run ahead of the device)."""
+    import torch
+
+    from perf import operators
+
+    cases = {c["name"]: c for c in operators.listed()}
+    if args.case not in cases:
+        raise SystemExit("--case must be one of " + ", ".join(cases))
+    case, work = cases[args.case], operators.work(cases[args.case])
+    operators.own = True
+    torch.cuda.set_device(0)
+    state = operators.prepare(case, 1)
+    flush = torch.empty(FP4_FLUSH_BYTES, dtype=torch.uint8, device="cuda")
+    for _ in range(args.warmup):
+        operators.run(state)
+    torch.cuda.synchronize()
+    sampler = ClockSampler(bus_id_of(0))
+    sampler.start()
+    events = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in range(args.steps)]
+    for i, (begin, end) in enumerate(events):
+        flush.fill_(i & 0xFF)
+        begin.record()
+        operators.run(state)
+        end.record()
+    torch.cuda.synchronize()
+    clocks = sampler.stop()
+    us = statistics.median(b.elapsed_time(e) * 1e3 for b, e in events)
+    print(json.dumps({
+        "metric": "us a pass, cold L2", "value": us, "unit": "us", "higher_is_better": False,
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "data": "synthetic",
+        "gbs": work["bytes"] / us / 1e3, "tflops": work["flops"] / us / 1e6,
+        "config": {"op": "fp4", "case": case, "l2": f"{FP4_FLUSH_BYTES >> 20} MB written before each pass"},
+        "clocks": clocks}), flush=True)
+    return 0
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -1130,11 +1171,14 @@ def main(argv=None):
     ap.add_argument("--workload", choices=sorted(configs.WORKLOADS), default="stress")
     ap.add_argument("--variant", choices=sorted(VARIANTS), default="auto",
                     help="launch variant of the fused op (default: the library's choice)")
-    ap.add_argument("--op", choices=OPS, default="fused",
+    ap.add_argument("--op", choices=OPS + ("fp4",), default="fused",
                     help="fused (default); prenorm: KV arrives normalised; kv_only: no q; "
                          "gather: read the FP8 cache back out; mxfp8: residual add + Gemma "
                          "RMSNorm + MXFP8 of [T, 7168] activation rows; indexer: indexer-K "
-                         "quant-insert of [T, 128] rows; indexer_gather: read them back out")
+                         "quant-insert of [T, 128] rows; indexer_gather: read them back out; "
+                         "fp4: a case of the 4-bit cache (--case)")
+    ap.add_argument("--case", default="attention_decode",
+                    help="case of --op fp4, by its name in perf/operators.py")
     ap.add_argument("--hidden", type=int, default=MXFP8_HIDDEN,
                     help="row width of --op mxfp8 (a multiple of 128 up to 16384)")
     ap.add_argument("--tokens", type=int, default=0,
@@ -1149,6 +1193,10 @@ def main(argv=None):
     args = ap.parse_args(argv)
     if args.warmup < 3:
         ap.error("--warmup must be at least 3")
+    if args.op == "fp4":
+        if args.impl == "reference" or args.gpus != 1 or dist_env()[1] != 1:
+            ap.error("--op fp4 runs this library on one GPU")
+        return run_fp4(args)
     if args.impl == "reference":
         return run_reference(args)
     return run_ours(args)
