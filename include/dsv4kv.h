@@ -439,9 +439,10 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
  *               that may run at the same time need two.
  *
  * Scores and sums are fp32; the probabilities are rounded to bf16 for the product with
- * the rows.  Rows are taken as they are stored while their values are below 2^83 (above,
- * as infinite).  A key past every token's length, or outside every window, is not read, whatever its slot holds;
- * the keys that some tokens of a request see and others do not must be finite.
+ * the rows.  Rows are taken as they are stored while their values are below 2^83.  One
+ * that holds a value that is not finite, or a group with e_g > 208, gives NaN (all dims and
+ * lse) to the tokens that see it and nothing to the others.  A key past every token's
+ * length, or outside every window, is not read, whatever its slot holds.
  * A block outside [0, num_blocks) sets DSV4_DEVERR_SLOT_RANGE and its keys take no part;
  * a length past table_width * block_size sets it too and counts as that many.
  */

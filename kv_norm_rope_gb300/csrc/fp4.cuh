@@ -69,6 +69,27 @@ __device__ __forceinline__ uint4 mul_bf16x8(uint4 v, uint32_t k2)
                       mul_bf16x2(v.w, k2));
 }
 
+// 8 bf16, what is not finite as a finite value
+__device__ __forceinline__ uint4 finite_bf16x8(uint4 v)
+{
+    const auto one = [](uint32_t a) {
+        // the lesser magnitude, with a's sign; of a NaN and a number the number
+        asm("min.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0x7F7F7F7Fu));
+        return a;
+    };
+    return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
+}
+
+// a + 0 * v over the 8 bf16 of v: what was 0 stays 0 unless a value is not finite
+__device__ __forceinline__ uint32_t zero_of_bf16x8(uint4 v, uint32_t a)
+{
+    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(a) : "r"(words[i]), "r"(0u));
+    return a;
+}
+
 // the 8 codes of a word times the group's scale -> 8 bf16 in dim order, exact
 __device__ __forceinline__ uint4 fp4x8_to_bf16(uint32_t w, uint32_t scale2)
 {
@@ -76,14 +97,24 @@ __device__ __forceinline__ uint4 fp4x8_to_bf16(uint32_t w, uint32_t scale2)
 }
 
 // As matrix operands the rows are held times 2^-80: then 2^126 and the scale are one
-// factor, 2^(e - 81), a bf16 for e <= 208 (values to 2^83; above, it is infinite, as
-// it is for e = 255).  What becomes subnormal was below 2^-46, far under the fp32
+// factor, 2^(e - 81), a bf16 for e <= 208 (values to 2^83; what stands above, e = 255
+// among it, is `above`: infinite, or 0 where the row is marked instead).  What becomes subnormal was below 2^-46, far under the fp32
 // rounding of any sum with a normalised row.  Products take the 2^80 back in fp32.
 constexpr float kOperandUnit = 0x1p80f;
 
-__device__ __forceinline__ uint32_t fp4_operand_scale(uint32_t e)
+constexpr uint32_t kOperandTop = 208u;
+
+__device__ __forceinline__ uint32_t fp4_operand_scale(uint32_t e, uint32_t above)
 {
-    return (e > 208u ? 0x7F80u : (e + 46u) << 7) * 0x00010001u;
+    return (e > kOperandTop ? above : (e + 46u) << 7) * 0x00010001u;
+}
+
+// whether one of a row's 14 exponents is above kOperandTop
+__device__ __forceinline__ bool fp4_row_above(uint4 scales)
+{
+    const uint32_t top = __vmaxu4(__vmaxu4(scales.x, scales.y),
+                                  __vmaxu4(scales.z, scales.w & 0xFFFFu));
+    return __vcmpgtu4(top, kOperandTop * 0x01010101u) != 0u;
 }
 
 constexpr uint32_t kRopeToOperand = 0x17801780u;  // bf16x2 (2^-80, 2^-80)

@@ -32,6 +32,11 @@
 //    unnormalised O, m and the sum go to the workspace and a second kernel joins
 //    them in the order of the runs.
 //
+// A key whose row is not finite may be masked for some rows of the tile, and 0 times
+// an infinity is NaN in the second product.  So what is not finite of it enters the
+// operands as a finite value and the key is marked: rows that see it get NaN as its score, whose P
+// makes all of their dims NaN, and the others are left alone.
+//
 // P is rounded to bf16 as an operand (half a step, at most 2^-8 of the value, to
 // either side); the sum that divides it is of the unrounded p.
 //
@@ -47,6 +52,7 @@
 // softmax (352 us), a warpgroup a pair (286), all warps on one pair at a time (270).
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -107,10 +113,14 @@ struct Shared {
     alignas(16) float factor[kRows];
     float warp_rows[4][kRows];  // maxima or sums of the four warps' keys
     int seen_to[kRows], seen_from[kRows];
-    uint8_t key_ok[kTileKeys];
+    // a key of the tile: kMissing, kTaken or kNotFinite; and whether the halves of its
+    // rope dims hold a value that is not finite
+    uint8_t key_state[kTileKeys];
+    alignas(2) uint8_t rope_state[2 * kTileKeys];
     Cursor place[4 * kGroups];  // of the softmax warps
 };
 constexpr size_t kSmemBytes = kShared + sizeof(Shared);
+enum : uint8_t { kMissing = 0, kTaken = 1, kNotFinite = 2 };
 static_assert(kSmemBytes <= 227 * 1024, "too much shared memory");
 
 // monotone map of a float to an int, for integer maxima; NaN counts as -infinity
@@ -126,6 +136,14 @@ __device__ __forceinline__ float unordered(int i)
 
 // ---- Warps 8..23: cache rows and queries into operands
 
+// a row's exponents; the two bytes without one become 1 where the row is not finite
+// (found as they are loaded: among the conversion it costs 34 us of 251, in registers)
+__device__ __forceinline__ uint4 marked(uint4 scales)
+{
+    scales.w = (scales.w & 0xFFFFu) | (fp4_row_above(scales) ? 0x10000u : 0u);
+    return scales;
+}
+
 __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c,
                                              const int team)
 {
@@ -137,7 +155,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
     KeyPlace now = key_place(p, c, true, key);
     Fp4Row row = row_at(p, now);
     copy_codes(p, slot, tid, row, team);
-    uint4 scales = load_raw(p, row.scale, row.data != nullptr);
+    uint4 scales = marked(load_raw(p, row.scale, row.data != nullptr));
     const auto fill_query = [&] {
         const int unit = ~now.unit, request = int(fastdiv(uint32_t(unit), p.tile_div));
         load_query(p, request, (unit - request * p.row_tiles) * kRows, smem + kQuery, kRows, tid + team * kTeam, 2 * kTeam);
@@ -179,7 +197,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
             copy_codes(p, slot, tid, u == 0 ? row : next_row, u == 0 ? i + 2 : team);
             const uint32_t four = (i < 2 ? (i == 0 ? scales.x : scales.y) : i == 2 ? scales.z : scales.w) >>
                                   (8 * half);
-            convert_group(a, four, out);
+            convert_group<true>(a, four, out);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 computed(out[k]);  // before the wait for its place
@@ -188,14 +206,22 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
             if (!alive)
                 break;
             if (i == 0 && half == 0)
-                s.key_ok[key] = row.data != nullptr ? 1 : 0;
+                store_shared1(base + kShared + uint32_t(offsetof(Shared, key_state)) + key,
+                              row.data == nullptr ? uint32_t(kMissing) : kTaken + (scales.w >> 16));
             store_half(to, place, out);
             if (i < 3) {
-                convert_group(b, four >> 16, out);
+                convert_group<true>(b, four >> 16, out);
             } else {
+                // before the conversion: within it, its registers cost 20 us of 253
+                uint32_t zero = 0u;  // or NaN, 0x7FFF, where a value is not finite
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    out[k] = mul_bf16x8(rope[k], kRopeToOperand);
+                    zero = zero_of_bf16x8(rope[k], zero);
+                store_shared1(base + kShared + uint32_t(offsetof(Shared, rope_state)) + tid,
+                              zero | (zero >> 16));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    out[k] = finite_bf16x8(mul_bf16x8(rope[k], kRopeToOperand));
             }
             store_half(to + kChunkBytes, place, out);
             if (i == 1) {
@@ -212,7 +238,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
             break;
         }
-        scales = next_scales;
+        scales = marked(next_scales);
         row = next_row;
         now = next;
         next = after;
@@ -407,7 +433,8 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, const C
         // fewest at the end, the last one the fewest at the start
         const bool whole = rows >= col0 + kCols && (c.tile + 1) * kTileKeys <= s.seen_to[col0] &&
                            c.tile * kTileKeys >= s.seen_from[col0 + kCols - 1];
-        const bool ok = s.key_ok[key] != 0;
+        const int state = s.key_state[key];
+        const bool ok = state == kTaken && reinterpret_cast<const uint16_t *>(s.rope_state)[key] == 0;
         float v[kCols];
         // v = the scores less `reference` (a row each; null: none), -infinity where unseen
         const auto load_scores = [&](const float *reference) {
@@ -425,16 +452,17 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, const C
                 v[j + 2] = __fmaf_rn(v[j + 2], scale, -m.z);
                 v[j + 3] = __fmaf_rn(v[j + 3], scale, -m.w);
             }
+            if (!ok) {
+                const float stand_in = state == kMissing ? -INFINITY : __int_as_float(0x7FFFFFFF);
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    v[j] = stand_in;
+            }
             if (!whole) {
 #pragma unroll
                 for (int j = 0; j < kCols; ++j)
                     if (i >= s.seen_to[col0 + j] || i < s.seen_from[col0 + j])
                         v[j] = -INFINITY;
-            }
-            if (!ok) {
-#pragma unroll
-                for (int j = 0; j < kCols; ++j)
-                    v[j] = -INFINITY;
             }
         };
         load_scores(s.m);

@@ -274,10 +274,12 @@ __device__ __forceinline__ void prefetch64(const AParams &p, const uint8_t *at, 
         asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 32];" ::"l"(at));
 }
 
-// 32 dims of a key: 16 bytes of codes with their scale
+// 32 dims of a key: 16 bytes of codes with their scale.  kMarked: an exponent past
+// the operands' range gives zeros, for the caller to mark the row
+template <bool kMarked>
 __device__ __forceinline__ void convert_group(uint4 codes, uint32_t scale, uint4 *out)
 {
-    const uint32_t scale2 = fp4_operand_scale(scale & 255u);
+    const uint32_t scale2 = fp4_operand_scale(scale & 255u, kMarked ? 0u : 0x7F80u);
     out[0] = mul_bf16x8(fp4x8_small(codes.x), scale2);
     out[1] = mul_bf16x8(fp4x8_small(codes.y), scale2);
     out[2] = mul_bf16x8(fp4x8_small(codes.z), scale2);
@@ -300,6 +302,11 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t at)
                  : "r"(at)
                  : "memory");
     return v;
+}
+
+__device__ __forceinline__ void store_shared1(uint32_t at, uint32_t v)
+{
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void store_shared16(uint32_t at, uint4 v)

@@ -228,7 +228,7 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
         for (int g = 0; g < 4; ++g) {
             uint4 out[4];
             if (pair < 3 || g < 2) {
-                convert_group(piece_of<4>(ring, lane, g), scales >> (8 * g), out);
+                convert_group<false>(piece_of<4>(ring, lane, g), scales >> (8 * g), out);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)

@@ -414,6 +414,40 @@ def test_attention_scores_far_below_zero():
     assert np.allclose(lse[0, 0].double().cpu().numpy(), s.scale * q[0, 0, :, 448] + np.log(300), rtol=2.0 ** -20, atol=0)
 
 
+@pytest.mark.parametrize("kind", ["group", "large", "rope nan", "rope inf", "rope -inf"])
+@pytest.mark.parametrize("n,Q,H,window", [(300, 3, 4, 0), (258, 3, 40, 0), (300, 3, 4, 100), (500, 3, 64, 200)])
+def test_attention_rows_not_finite(kind, n, Q, H, window):
+    """A row that is not finite makes NaN of the tokens that see it and of no others."""
+    bad = [n - 1] if window == 0 else [n - Q + 1 - window]  # seen by the last token alone, or the first
+    s = Batch([n, 40], Q, H, 16, seed=26)
+    cache = s.cache_np
+    for i in bad:
+        data, scale = fp4.row_bytes(cache, 16, s.table_np[0, i // 16] * 16 + i % 16)
+        if kind == "group":
+            scale[9], data[9 * 16:10 * 16] = 255, 0
+        elif kind == "large":
+            scale[13] = 230
+        else:
+            value = {"rope nan": np.nan, "rope inf": np.inf, "rope -inf": -np.inf}[kind]
+            tail = torch.tensor([value]).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint8)
+            data[224 + 2 * 45:226 + 2 * 45] = tail
+    s.cache = dev(cache)
+    out, lse = s.attention(window=window)
+    hit = Q - 1 if window == 0 else 0
+    assert torch.isnan(out[0, hit]).all() and torch.isnan(lse[0, hit]).all()
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, length in enumerate(s.lens):
+        rows = s.rows[b].copy()
+        want, wlse, size, reach = fp4.attention(s.q64[b], rows, s.ok[b], length, s.scale, window)
+        ds = s.scale * reach * 2.0 ** -15 + 2.0 ** -18
+        for j in range(Q):
+            if b == 0 and j == hit:
+                continue
+            tol = np.abs(want[j]) * 2.0 ** -8 + size[j] * (2.0 ** -8 + 2 * ds[j][:, None])
+            assert np.all(np.abs(out[b, j] - want[j]) <= tol + 1e-30)
+            assert np.all(np.abs(lse[b, j] - wlse[j]) <= ds[j] + np.abs(wlse[j]) * 2.0 ** -22)
+
+
 def test_attention_bad_pages_and_lengths():
     """A block outside the cache takes no part and is flagged; so is a length past the table."""
     s = Batch([300, 100, 50], 1, 8, 16, seed=14)
