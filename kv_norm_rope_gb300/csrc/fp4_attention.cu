@@ -113,10 +113,10 @@ struct Shared {
     alignas(16) float factor[kRows];
     float warp_rows[4][kRows];  // maxima or sums of the four warps' keys
     int seen_to[kRows], seen_from[kRows];
-    // a key of the tile: kMissing, kTaken or kNotFinite; and whether the halves of its
-    // rope dims hold a value that is not finite
-    uint8_t key_state[kTileKeys];
-    alignas(2) uint8_t rope_state[2 * kTileKeys];
+    uint8_t key_state[kTileKeys];  // kMissing, kTaken or kNotFinite, by its exponents
+    // bits of the keys whose rope dims are not finite: a word for each softmax warp,
+    // which clears it
+    uint32_t rope_marks[kGroups][4];
     Cursor place[4 * kGroups];  // of the softmax warps
 };
 constexpr size_t kSmemBytes = kShared + sizeof(Shared);
@@ -142,6 +142,13 @@ __device__ __forceinline__ uint4 marked(uint4 scales)
 {
     scales.w = (scales.w & 0xFFFFu) | (fp4_row_above(scales) ? 0x10000u : 0u);
     return scales;
+}
+
+__device__ __forceinline__ void mark_key(Shared &s, int key)
+{
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+        atomicOr(&s.rope_marks[g][key >> 5], 1u << (key & 31));
 }
 
 __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c,
@@ -212,18 +219,20 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint8_
             if (i < 3) {
                 convert_group<true>(b, four >> 16, out);
             } else {
-                // before the conversion: within it, its registers cost 20 us of 253
-                uint32_t zero = 0u;  // or NaN, 0x7FFF, where a value is not finite
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    zero = zero_of_bf16x8(rope[k], zero);
-                store_shared1(base + kShared + uint32_t(offsetof(Shared, rope_state)) + tid,
-                              zero | (zero >> 16));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     out[k] = finite_bf16x8(mul_bf16x8(rope[k], kRopeToOperand));
             }
             store_half(to + kChunkBytes, place, out);
+            if (i == 3) {
+                // after the stores: its registers before them cost 15 us of 258
+                uint32_t zero = 0u;  // or NaN, 0x7FFF, where a value is not finite
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    zero = zero_of_bf16x8(rope[k], zero);
+                if ((zero & 0x7FFF7FFFu) != 0u)
+                    mark_key(s, key);
+            }
             if (i == 1) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -434,7 +443,13 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, const C
         const bool whole = rows >= col0 + kCols && (c.tile + 1) * kTileKeys <= s.seen_to[col0] &&
                            c.tile * kTileKeys >= s.seen_from[col0 + kCols - 1];
         const int state = s.key_state[key];
-        const bool ok = state == kTaken && reinterpret_cast<const uint16_t *>(s.rope_state)[key] == 0;
+        const uint32_t marks = s.rope_marks[group][warp];
+        const bool ok = state == kTaken && ((marks >> lane) & 1u) == 0u;
+        if (marks != 0u) {
+            __syncwarp();
+            if (lane == 0)
+                s.rope_marks[group][warp] = 0u;
+        }
         float v[kCols];
         // v = the scores less `reference` (a row each; null: none), -infinity where unseen
         const auto load_scores = [&](const float *reference) {
@@ -598,6 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
         }
         tmem_fence_before();
     }
+    if (threadIdx.x < 4 * kGroups)
+        s.rope_marks[threadIdx.x >> 2][threadIdx.x & 3] = 0u;
     Cursor c;
     deal(p, blockIdx.x, gridDim.x, s.scratch, c);  // with barriers for the CTA
     tmem_fence_after();
