@@ -41,7 +41,7 @@
 // either side); the sum that divides it is of the unrounded p.
 //
 // One request of 262147 keys, 128 heads: 119 us, 579 TFLOP/s; 128 requests of 1024 to
-// 8192 keys, 128 heads: 254 us, 571 TFLOP/s; 48 of up to 4096, 64 heads: 49 us.  By
+// 8192 keys, 128 heads: 257 us, 564 TFLOP/s; 48 of up to 4096, 64 heads: 49 us.  By
 // arithmetic, an instruction of either product reads 6 KB of shared memory for 32
 // cycles of the matrix unit, so at 128 bytes a cycle shared memory bounds them at two
 // thirds of the unit's rate, and the converted rows are written through it as well.
@@ -137,7 +137,7 @@ __device__ __forceinline__ float unordered(int i)
 // ---- Warps 8..23: cache rows and queries into operands
 
 // a row's exponents; the two bytes without one become 1 where the row is not finite
-// (found as they are loaded: among the conversion it costs 34 us of 251, in registers)
+// (found as they are loaded: among the conversion it cost 34 us more than 251)
 __device__ __forceinline__ uint4 marked(uint4 scales)
 {
     scales.w = (scales.w & 0xFFFFu) | (fp4_row_above(scales) ? 0x10000u : 0u);
