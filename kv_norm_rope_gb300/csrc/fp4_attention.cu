@@ -648,7 +648,7 @@ constexpr int kJoinWarps = 8;
 template <bool kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32) fp4_join_kernel(const __grid_constant__ WParams w)
 {
-    __shared__ int before_s[kJoinWarps], total_s[kJoinWarps];
+    __shared__ int4 sums_s[kJoinWarps];
     __shared__ float4 o_s[kSplit ? kJoinWarps : 1][4][32];
     __shared__ float sum_s[kJoinWarps];
     const AParams &p = w.p;
@@ -658,36 +658,45 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fp4_join_kernel(const __grid_
     c.unit = blockIdx.x;
     c.enter(p);
     const int r = kSplit ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
-    int before = 0, total = 0;
+    // tiles, and units with some, before this one and in all
+    int before = 0, units_before = 0, total = 0, units = 0;
     for (int i = threadIdx.x; i < p.units; i += kJoinWarps * 32) {
-        const int tiles = tiles_of(p, i);
+        const int tiles = tiles_of(p, i), some = tiles > 0 ? 1 : 0;
         total += tiles;
+        units += some;
         before += i < c.unit ? tiles : 0;
+        units_before += i < c.unit ? some : 0;
     }
     before = __reduce_add_sync(kFull, before);
+    units_before = __reduce_add_sync(kFull, units_before);
     total = __reduce_add_sync(kFull, total);
-    if (lane == 0) {
-        before_s[warp] = before;
-        total_s[warp] = total;
-    }
+    units = __reduce_add_sync(kFull, units);
+    if (lane == 0)
+        sums_s[warp] = make_int4(before, units_before, total, units);
     __syncthreads();
-    before = total = 0;
+    before = units_before = total = units = 0;
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i) {
-        before += before_s[i];
-        total += total_s[i];
+        before += sums_s[i].x;
+        units_before += sums_s[i].y;
+        total += sums_s[i].z;
+        units += sums_s[i].w;
     }
     wait_for_kernel_before();
     const int tiles = c.range.tiles();
-    const int share = (total + w.runs - 1) / w.runs;
-    const int x0 = tiles > 0 ? before / share : 0, x1 = tiles > 0 ? (before + tiles - 1) / share : -1;
+    // the line as it was dealt
+    const int cost = start_cost(p, total, w.runs);
+    const int share = (total + cost * units + w.runs - 1) / w.runs;
+    const int start = before + cost * units_before, first_tile = start + cost;
+    const int x0 = tiles > 0 ? first_tile / share : 0;
+    const int x1 = tiles > 0 ? (first_tile + tiles - 1) / share : -1;
     // written by its run, or no row (with kSplit the same for the whole block)
     if ((tiles > 0 && x0 == x1) || c.row0 + r >= c.row1)
         return;
     const Span ps = partial_span(w);
     const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
     // the first run may have begun with an earlier unit
-    const int slot0 = before == x0 * share ? 0 : 1;
+    const int slot0 = x0 * share >= start ? 0 : 1;
     const float *ms = w.partials + kRows * DSV4_HEAD_DIM + r;
     const auto part = [&](int x) { return (size_t(x) * 2 + (x == x0 ? slot0 : 0)) * kPartialFloats; };
     float m = kUnset;

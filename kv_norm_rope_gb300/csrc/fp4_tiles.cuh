@@ -132,20 +132,36 @@ __device__ __forceinline__ int tiles_of(const AParams &p, int unit)
     return c.range.tiles();
 }
 
+// The line that is dealt to the CTAs: the units' tiles, and before those of each
+// start_cost() positions without one, for what it takes to begin a unit (its queries,
+// its first reference, its results), so that a run of many short units has fewer tiles.
+// With fewer tiles than CTAs, or few units, a run has one or two units anyway, and the
+// positions would only make some runs a tile longer.  0, 1, 2, 3, 4, 6 positions:
+// attention over 48 requests of 64 to 4096 keys 47.9, 47.3, 41.0, 40.3, 40.1, 43.3 us;
+// 24 of 1 to 6000 in windows of 2048 with three tokens 68, 47, 43, 46, 47, 51; 128 of
+// 1024 to 8192 258, 252, 240, 245, 246, 248; the weights over the first, 0 and 2:
+// 25.5, 23.4.
+constexpr int kStartCost = 2;
+
+__device__ __forceinline__ int start_cost(const AParams &p, int total, int X)
+{
+    return total > X && p.units > X / 8 ? kStartCost : 0;
+}
+
 // Places c at the start of CTA x's run.  All threads of the CTA (at least
 // kDealThreads) call it.  scratch: kDealWords words of shared memory.
 constexpr int kDealThreads = 512;
 constexpr int kDealWarps = kDealThreads / 32;
-constexpr int kDealWords = 2 * kDealWarps + 2;
+constexpr int kDealWords = 4 * kDealWarps + 4;
 
 __device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratch, Cursor &c)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // the units from `base` on, one a thread: their tiles up to and with the thread's
-    // own, and all of them; `half` of the scratch words, so that calls in turn need
-    // one barrier each
-    int upto = 0, mine = 0, all = 0;
-    const auto scan = [&](int base, int half) {
+    // own, and all of them, and of the units themselves those with tiles; `half` of the
+    // scratch words, so that calls in turn need one barrier each
+    int upto = 0, mine = 0, all = 0, units_upto = 0, units_all = 0, half = 0;
+    const auto scan = [&](int base) {
         mine = tid < kDealThreads && base + tid < p.units ? tiles_of(p, base + tid) : 0;
         upto = mine;
 #pragma unroll
@@ -154,42 +170,63 @@ __device__ __forceinline__ void deal(const AParams &p, int x, int X, int *scratc
             if (lane >= s)
                 upto += o;
         }
-        int *sums = scratch + half * kDealWarps;
-        if (lane == 31 && warp < kDealWarps)
+        units_upto = __popc(__ballot_sync(kFull, mine > 0) & (kFull >> (31 - lane)));
+        int *sums = scratch + half * 2 * kDealWarps;
+        if (lane == 31 && warp < kDealWarps) {
             sums[warp] = upto;
+            sums[kDealWarps + warp] = units_upto;
+        }
         __syncthreads();
-        all = 0;
+        all = units_all = 0;
 #pragma unroll
         for (int w = 0; w < kDealWarps; ++w) {
-            if (w < warp)
+            if (w < warp) {
                 upto += sums[w];
+                units_upto += sums[kDealWarps + w];
+            }
             all += sums[w];
+            units_all += sums[kDealWarps + w];
         }
+        half ^= 1;
     };
-    int total = 0, half = 0;
-    for (int base = 0; base < p.units; base += kDealThreads, half ^= 1) {
-        scan(base, half);
+    int total = 0, units = 0;
+    for (int base = 0; base < p.units; base += kDealThreads) {
+        scan(base);
         total += all;
+        units += units_all;
     }
-    const int share = (total + X - 1) / X;
-    const int64_t begin = int64_t(x) * share;
-    c.left = begin < total ? (total - int(begin) < share ? total - int(begin) : share) : 0;
-    if (c.left == 0)
+    const int cost = start_cost(p, total, X), positions = total + cost * units;
+    const int share = (positions + X - 1) / X;
+    const int64_t from = int64_t(x) * share;
+    c.left = 0;
+    if (from >= positions)
         return;
-    const int t0 = int(begin);
-    for (int base = 0, before = 0; base < p.units && before <= t0; base += kDealThreads, half ^= 1) {
+    const int begin = int(from), end = positions - begin < share ? positions : begin + share;
+    int *found = scratch + 4 * kDealWarps;  // unit, tile in it, tiles before the run, and with it
+    for (int base = 0, before = 0, units_before = 0;
+         base < p.units && before + cost * units_before < end; base += kDealThreads) {
         if (p.units > kDealThreads)
-            scan(base, half);
-        if (mine > 0 && before + upto - mine <= t0 && t0 < before + upto) {
-            scratch[2 * kDealWarps] = base + tid;
-            scratch[2 * kDealWarps + 1] = t0 - (before + upto - mine);
+            scan(base);
+        const int tiles = before + upto - mine;  // before the thread's unit
+        const int first = tiles + cost * (units_before + units_upto), last = first + mine;
+        if (mine > 0 && first - cost <= begin && begin < last) {
+            const int in = begin > first ? begin - first : 0;
+            found[0] = base + tid;
+            found[1] = in;
+            found[2] = tiles + in;
         }
+        if (mine > 0 && first - cost < end && end <= last)
+            found[3] = tiles + (end > first ? end - first : 0);
         before += all;
+        units_before += units_all;
     }
     __syncthreads();
-    c.unit = scratch[2 * kDealWarps];
+    c.left = found[3] - found[2];
+    if (c.left == 0)
+        return;
+    c.unit = found[0];
     c.enter(p);
-    c.tile = c.range.first() + scratch[2 * kDealWarps + 1];
+    c.tile = c.range.first() + found[1];
 }
 
 // ---- Cache rows -> operand

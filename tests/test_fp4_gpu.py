@@ -377,6 +377,29 @@ def test_attention_scores_far_apart(order):
     s.check(out, lse)
 
 
+def _ragged(count, seed):
+    rng = np.random.default_rng(seed)
+    lens = np.where(rng.random(count) < 0.2, 0, rng.integers(1, 60, count))
+    lens[rng.choice(count, 5, replace=False)] = rng.integers(200, 900, 5)
+    return [int(n) for n in lens]
+
+
+@pytest.mark.parametrize("count,Q,H", [(25, 1, 70), (160, 2, 3), (511, 1, 2), (513, 1, 2), (300, 1, 130)])
+def test_many_short_requests_among_longer_ones(count, Q, H):
+    """Runs of several requests, some of them idle, and requests over several runs."""
+    lens = _ragged(count, count)
+    s = Batch(lens, Q, H, 16, seed=27)
+    out, lse = s.attention()
+    s.check(out, lse)
+    again, _ = s.attention()
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("count,Q,H", [(25, 1, 70), (160, 2, 3), (513, 1, 2)])
+def test_weights_of_many_short_requests(count, Q, H):
+    check_weights(Batch(_ragged(count, count), Q, H, 16, seed=28))
+
+
 def test_attention_values_of_the_lowest_kind():
     """Scores that overflow to -infinity are masked; a row of them alone has no value."""
     s = Batch([30, 200], 1, 2, 16, seed=13)
