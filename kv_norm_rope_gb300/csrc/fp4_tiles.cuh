@@ -139,8 +139,8 @@ __device__ __forceinline__ int tiles_of(const AParams &p, int unit)
 // positions would only make some runs a tile longer.  0, 1, 2, 3, 4, 6 positions:
 // attention over 48 requests of 64 to 4096 keys 47.9, 47.3, 41.0, 40.3, 40.1, 43.3 us;
 // 24 of 1 to 6000 in windows of 2048 with three tokens 68, 47, 43, 46, 47, 51; 128 of
-// 1024 to 8192 258, 252, 240, 245, 246, 248; the weights over the first, 0 and 2:
-// 25.5, 23.4.
+// 1024 to 8192 258, 252, 240, 245, 246, 248; the weights over the first gain
+// nothing (24.2 without and 23.4 with it on one resident input, 24.9 and 25.3 on changing ones).
 constexpr int kStartCost = 2;
 
 __device__ __forceinline__ int start_cost(const AParams &p, int total, int X)

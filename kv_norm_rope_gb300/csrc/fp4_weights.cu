@@ -18,7 +18,7 @@
 //  * Each key's sum is finished by one thread of one CTA in a fixed order of rows
 //    and added by it: no atomics, the same bits every time.
 //
-// 3 requests of up to 131072 keys, 2 x 128 rows: 85 us, 807 TFLOP/s; 48 of up to 4096,
+// 3 requests of up to 131072 keys, 2 x 128 rows: 85 us, 805 TFLOP/s; 48 of up to 4096,
 // 64 rows: 25 us.  What bounds it is the conversion: the schedulers issue in 67% of the
 // cycles (23 instructions for the 8 codes of a word), the matrix unit is busy in 37%.
 // All converting warps run one code path: a copy of the loop for each pair did not fit
