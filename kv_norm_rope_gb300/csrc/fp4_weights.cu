@@ -42,6 +42,9 @@ constexpr int kCols = kRows / kGroups;
 constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
 constexpr int kThreads = (kMultiplyWarp + 1) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
+// Places for the words of which keys are there.  A tile's is written behind the wait for the
+// product of the tile before, t - 1, which began after every summing warp had given back the
+// scores of tile t - 3, and so after all of them had read the words of tile t - 4.
 constexpr int kOkTiles = 4;
 
 // Shared memory (from a 1024-byte boundary): 8 chunks of 128 rows, then what is on
@@ -209,11 +212,6 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
             }
             ++passes;
         }
-        if (pair == 0) {
-            const uint32_t bits = __ballot_sync(kFull, there);
-            if (lane == 0)
-                s.key_ok[t % kOkTiles][warp] = bits;
-        }
         copy_wait();
         __syncwarp();  // the copies are the warp's together
         if (t > 0 && alive)
@@ -224,6 +222,11 @@ __device__ __forceinline__ void convert_role(const WParams &w, Shared &s, uint8_
         }
         tmem_fence_after();
         __syncwarp();
+        if (pair == 0) {
+            const uint32_t bits = __ballot_sync(kFull, there);
+            if (lane == 0)
+                s.key_ok[t % kOkTiles][warp] = bits;
+        }
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
             uint4 out[4];
