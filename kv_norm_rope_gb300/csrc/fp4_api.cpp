@@ -69,8 +69,10 @@ int check_attention(int32_t q_len, int32_t num_heads, int32_t batch, float scale
         int64_t(q_len) * num_heads * batch > INT64_MAX / 4096 ||
         (batch > 0 && int64_t(q_len) * num_heads > INT32_MAX / batch))
         return DSV4_ERR_SHAPE;
-    // tiles of 64 rows and 128 keys are counted in 32 bits
-    if (((int64_t(q_len) * num_heads + 63) / 64) * batch > INT32_MAX / ((most_keys + 127) / 128))
+    // The line of tiles of 64 rows and 128 keys with what is added to it is counted in 32
+    // bits, up to a multiple of the CTAs (fewer than 1024).
+    if (((int64_t(q_len) * num_heads + 63) / 64) * batch >
+        (INT32_MAX - 1024) / ((most_keys + 127) / 128 + dsv4::kFp4StartCost))
         return DSV4_ERR_SHAPE;
     if (!(scale > 0.0f && scale <= 4294967296.0f))  // it is multiplied by 2^82 in fp32
         return DSV4_ERR_VALUE;

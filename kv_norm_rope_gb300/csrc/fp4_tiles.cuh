@@ -141,7 +141,7 @@ __device__ __forceinline__ int tiles_of(const AParams &p, int unit)
 // 24 of 1 to 6000 in windows of 2048 with three tokens 68, 47, 43, 46, 47, 51; 128 of
 // 1024 to 8192 258, 252, 240, 245, 246, 248; the weights over the first gain
 // nothing (24.2 without and 23.4 with it on one resident input, 24.9 and 25.3 on changing ones).
-constexpr int kStartCost = 2;
+constexpr int kStartCost = kFp4StartCost;
 
 __device__ __forceinline__ int start_cost(const AParams &p, int total, int X)
 {

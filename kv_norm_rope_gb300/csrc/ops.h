@@ -61,6 +61,10 @@ struct Fp4Batch {
     int32_t *err;
 };
 
+// Positions that a row tile with keys may take on the line that is dealt to the CTAs,
+// beside one for each of its tiles of keys (fp4_tiles.cuh).
+constexpr int kFp4StartCost = 2;
+
 struct Fp4AttentionArgs {
     Fp4Batch b;
     const uint16_t *q;      // [batch, q_len, heads, 512]
