@@ -389,8 +389,8 @@ const char *dsv4_status_string(int status);
  * (lowest first) are dims 8i + (0, 2, 4, 6, 1, 3, 5, 7).  A code is a sign bit over an
  * E2M1 magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6; the value is code * 2^(e_g - 127).
  * e_g = s_g + 127 with s_g the smallest integer such that max|v| over the group
- * <= 6 * 2^s_g (at least -127), code = E2M1_rn(v * 2^-s_g) (ties to the even code), v
- * as for the other stores: both follow the exact v = x * w * r, not an fp32 rounding
+ * <= 6 * 2^s_g (at least -127), code = E2M1_rn(v * 2^-s_g) (ties to the even code; the
+ * sign bit is v's, also where v is -0 or becomes 0), v as for the other stores: both follow the exact v = x * w * r, not an fp32 rounding
  * of it.  A group whose maximum is not finite has e_g = 255 and reads back as NaN.
  */
 

@@ -683,7 +683,8 @@ __device__ __forceinline__ float kv_products(const KParams &p, int lane, int64_t
 // ---- The 4-bit store (fp4.cuh: the row's format)
 //
 // Per group of 32 dims: s = the least integer with amax <= 6 * 2^s, codes
-// E2M1_rn(v * 2^-s).  4-bit codes are so coarse that a value on the other side
+// E2M1_rn(v * 2^-s) with v's sign, a zero's too, as the conversion instruction gives
+// it.  4-bit codes are so coarse that a value on the other side
 // of a border moves by a whole step, so both decisions follow the exact v =
 // x * w * r.  fp32 settles nearly all: its v is within 2^-20 of the exact one,
 // so an element whose code is the same at v * (1 - kFp4Band) and v * (1 + kFp4Band),
@@ -786,7 +787,7 @@ __device__ __forceinline__ uint32_t e2m1_fp64(double u)
     const uint32_t c = (a > 0.25 ? 1u : 0u) + (a >= 0.75 ? 1u : 0u) + (a > 1.25 ? 1u : 0u) +
                        (a >= 1.75 ? 1u : 0u) + (a > 2.5 ? 1u : 0u) + (a >= 3.5 ? 1u : 0u) +
                        (a > 5.0 ? 1u : 0u);
-    return c | (u < 0.0 ? 8u : 0u);
+    return c | (__double2hiint(u) < 0 ? 8u : 0u);
 }
 
 // The row of token t in fp64.
@@ -901,7 +902,7 @@ __device__ __noinline__ Fp4Lane fp4_row_exact(KvSrc p, int lane, int64_t t)
                     ok = ok && up >= 0;
                     code += up > 0 ? 1 : 0;
                 }
-                c |= (uint32_t(code) | (v < 0.0f ? 8u : 0u)) << (4 * ((k >> 1) + 4 * (k & 1)));
+                c |= (uint32_t(code) | (signbit(v) ? 8u : 0u)) << (4 * ((k >> 1) + 4 * (k & 1)));
             }
         }
         if (h == 0) {

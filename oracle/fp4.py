@@ -50,7 +50,7 @@ def quantise(v: np.ndarray):
         s = exponent(np.abs(x).max())
         c = e2m1_rne(np.ldexp(x, -s))
         exps[g] = s
-        codes[32 * g:32 * g + 32] = c + 8 * (x < 0)
+        codes[32 * g:32 * g + 32] = c + 8 * np.signbit(x)
         held[32 * g:32 * g + 32] = np.sign(x) * np.ldexp(MAGNITUDES[c], s)
     return held, exps, codes
 
