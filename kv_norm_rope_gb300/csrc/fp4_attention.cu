@@ -19,7 +19,7 @@
 //    own, so the next tile is converted under the products of this one.
 //  * Warps 0..7 do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
 //    32 (w / 4)..; a thread has one key and 32 rows.  Warps 8..23 convert, warp 24
-//    issues the products.  The teams of converting warps share one code path, so
+//    issues the products, warp 25 notes the run's ends.  The teams of converting warps share one code path, so
 //    that all loops fit the instruction cache together, and warp 24's warpgroup gives
 //    registers to the softmax: a spill costs a trip to L2, as shared memory leaves
 //    little of L1.
@@ -30,7 +30,7 @@
 //    nothing).  Sums stay per thread, in fp32, until the segment ends.
 //  * A run that covers all tiles of a request writes the output; else the
 //    unnormalised O, m and the sum go to the workspace and a second kernel joins
-//    them in the order of the runs.
+//    them in the order of the runs, each of which has noted (warp 25) what it left.
 //
 // A key whose row is not finite may be masked for some rows of the tile, and 0 times
 // an infinity is NaN in the second product.  So what is not finite of it enters the
@@ -68,7 +68,7 @@ constexpr int kRows = 64;            // query rows of a CTA
 constexpr int kGroups = 2;           // of 4 softmax warps
 constexpr int kCols = kRows / kGroups;
 constexpr int kConvertWarp = 4 * kGroups, kMultiplyWarp = kConvertWarp + 16;
-constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: three warps idle
+constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: the last two warps idle
 // registers a thread: 72 at launch (896 * 72 = 64512), then
 constexpr int kSoftmaxRegs = 88, kConvertRegs = 72, kMultiplyRegs = 40;
 static_assert(128 * (kGroups * kSoftmaxRegs + 4 * kConvertRegs + kMultiplyRegs) <= kThreads * 72,
@@ -79,13 +79,24 @@ constexpr float kUnset = -3.402823466e38f;  // m of a row that has seen no key: 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Workspace: two partial results a CTA, O [64, 512] then m [64] and sum [64].
+// Workspace: two partial results a CTA, O [64, 512] then m [64] and sum [64]; after all
+// of them, a RunEnds a CTA.
 constexpr size_t kPartialFloats = size_t(kRows) * DSV4_HEAD_DIM + 2 * kRows;
+
+// The units whose partial results a run left, for the join; -1 for none.
+struct alignas(16) RunEnds {
+    int continued;  // one that an earlier run began, in slot 0
+    int left_open;  // one that this run began and later ones go on with
+    int slot;       // of left_open
+    int unused;
+};
 
 struct WParams {
     AParams p;
     float *partials;
-    int runs;  // CTAs
+    RunEnds *ends;
+    int runs;    // CTAs
+    int splits;  // columns of the join's blocks that join; the others serve rows without keys
 };
 
 __device__ __forceinline__ float *partial_at(const WParams &w, int x, int slot)
@@ -95,6 +106,10 @@ __device__ __forceinline__ float *partial_at(const WParams &w, int x, int slot)
 __device__ __forceinline__ Span partial_span(const WParams &w)
 {
     return Span{w.partials, uint64_t(w.runs) * 2u * kPartialFloats * 4u};
+}
+__device__ __forceinline__ Span ends_span(const WParams &w)
+{
+    return Span{w.ends, uint64_t(w.runs) * sizeof(RunEnds)};
 }
 
 // Shared memory (from a 1024-byte boundary).
@@ -314,6 +329,29 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
     }
     if (c.left > 0)
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+}
+
+// ---- Warp 25: what the join has to know, found by following the run from unit to unit
+
+__device__ void note_ends(const WParams &w, Cursor c)
+{
+    int continued = -1, left_open = -1, slot = 0;
+    if (c.left > 0 && c.tile > c.range.first())
+        continued = c.unit;
+    while (c.left > 0) {
+        const int rest = c.range.stop() - c.tile;  // of the unit's tiles
+        if (c.left < rest && c.tile == c.range.first())
+            left_open = c.unit;
+        if (c.left <= rest)
+            break;
+        slot = 1;  // of any but the first unit
+        c.left -= rest - 1;
+        c.tile = c.range.stop() - 1;
+        c.advance(w.p);
+    }
+    if ((threadIdx.x & 31) == 0)
+        st16_in(w.ends + blockIdx.x, make_uint4(uint32_t(continued), uint32_t(left_open), uint32_t(slot), 0u),
+                ends_span(w), w.p.a.b.err);
 }
 
 // ---- Warps 0..7: softmax and results
@@ -618,17 +656,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
     Cursor c;
     deal(p, blockIdx.x, gridDim.x, s.scratch, c);  // with barriers for the CTA
     tmem_fence_after();
-    if (c.left == 0) {
+    if (warp >= kMultiplyWarp) {
+        registers_down<kMultiplyRegs>();
+        if (warp == kMultiplyWarp)
+            multiply_role(p, s, smem_addr(smem), c);
+        else if (warp == kMultiplyWarp + 1)
+            note_ends(w, c);
+    } else if (c.left == 0) {
         // more CTAs than tiles
     } else if (warp < kConvertWarp) {
         registers_up<kSoftmaxRegs>();
         softmax_role(w, s, smem, c);
-    } else if (warp < kMultiplyWarp) {
-        convert_role(p, s, smem, c, (warp - kConvertWarp) / 8);
     } else {
-        registers_down<kMultiplyRegs>();
-        if (warp == kMultiplyWarp)
-            multiply_role(p, s, smem_addr(smem), c);
+        convert_role(p, s, smem, c, (warp - kConvertWarp) / 8);
     }
     tmem_fence_before();
     __syncthreads();
@@ -639,70 +679,153 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
 }
 
 // Joins the partial results of the units whose tiles more than one run took, and
-// writes the rows that see no key.  A row goes to one warp, or, where a few long
+// writes the rows of units that see no key.  A row goes to one warp, or, where a few long
 // requests are spread over many runs, to the eight warps of a block (kSplit), each
-// with every eighth run.  It is launched while the attention ends, and finds its
-// place among the runs meanwhile.
+// with every eighth run.  It is launched while the attention ends.
+//
+// Column x < splits of the blocks joins the x-th unit that some run left open, which the
+// runs have noted, so the cost goes by the runs and not by the units.  The other columns
+// look through the units for those without keys, each at its share of them.  (A column a
+// unit, each finding its runs by a look at all lengths, took 6.1 ms for 64000 idle
+// requests, against 0.3.)  What the first two runs left of a row is loaded before the maximum
+// is known: 17.5 us instead of 18.5 for two requests of 8 heads, 41.0 instead of 42.7 for 48.
 constexpr int kJoinWarps = 8;
+constexpr int kIdleColumns = 64;
+static_assert(kMaxCtas % 32 == 0, "the join's lanes hold the ends of kMaxCtas / 32 runs each");
+
+__device__ __forceinline__ int row_of_block(bool split)
+{
+    return split ? blockIdx.y : blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+}
+
+// Row r of a unit from its m, its sum and the unnormalised o (kSplit: o[0] is dims 128
+// times the warp on).
+template <bool kSplit>
+__device__ __forceinline__ void write_row(const AParams &p, int unit, int r, float m, float sum,
+                                          const float4 *o)
+{
+    const Fp4AttentionArgs &a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int request = int(fastdiv(uint32_t(unit), p.tile_div));
+    const int in_request = (unit - request * p.row_tiles) * kRows + r;
+    const int64_t row = int64_t(request) * p.all_rows + in_request;
+    const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
+    float lse;
+    const float f = finish(m, sum, sink_of(a, in_request), &lse);
+    const int first = kSplit ? warp : 0, last = kSplit ? warp : 3;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (k < first || k > last)
+            continue;
+        const float4 v = kSplit ? o[0] : o[k];
+        st8_in(a.out + row * DSV4_HEAD_DIM + 128 * k + 4 * lane,
+               f == 0.0f ? make_uint2(0u, 0u)
+                         : make_uint2(bf16x2_rn(v.x * f, v.y * f), bf16x2_rn(v.z * f, v.w * f)),
+               os, a.b.err);
+    }
+    if (lane == 0 && first == 0 && a.lse != nullptr)
+        st_f32_in(a.lse + row, lse, Span{a.lse, rows_of(a) * 4u}, a.b.err);
+}
+
+// whether row r of the unit is one of its request's
+__device__ __forceinline__ bool has_row(const AParams &p, int unit, int r)
+{
+    return (unit - int(fastdiv(uint32_t(unit), p.tile_div)) * p.row_tiles) * kRows + r < p.all_rows;
+}
+
+template <bool kSplit>
+__device__ __forceinline__ void rows_without_keys(const AParams &p, int column, int columns)
+{
+    const int lane = threadIdx.x & 31, r = row_of_block(kSplit);
+    if (kSplit && (threadIdx.x >> 5) >= 4)
+        return;
+    const float4 none[4] = {};
+    for (int base = column; base < p.units; base += 32 * columns) {
+        const int mine = base + lane * columns;
+        unsigned idle = __ballot_sync(kFull, mine < p.units && tiles_of(p, mine) == 0);
+        for (; idle != 0u; idle &= idle - 1u) {
+            const int unit = base + (__ffs(idle) - 1) * columns;
+            if (has_row(p, unit, r))
+                write_row<kSplit>(p, unit, r, kUnset, 0.0f, none);
+        }
+    }
+}
 
 template <bool kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32) fp4_join_kernel(const __grid_constant__ WParams w)
 {
-    __shared__ int4 sums_s[kJoinWarps];
     __shared__ float4 o_s[kSplit ? kJoinWarps : 1][4][32];
     __shared__ float sum_s[kJoinWarps];
     const AParams &p = w.p;
-    const Fp4AttentionArgs &a = p.a;
+    int32_t *err = p.a.b.err;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Cursor c;
-    c.unit = blockIdx.x;
-    c.enter(p);
-    const int r = kSplit ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
-    // tiles, and units with some, before this one and in all
-    int before = 0, units_before = 0, total = 0, units = 0;
-    for (int i = threadIdx.x; i < p.units; i += kJoinWarps * 32) {
-        const int tiles = tiles_of(p, i), some = tiles > 0 ? 1 : 0;
-        total += tiles;
-        units += some;
-        before += i < c.unit ? tiles : 0;
-        units_before += i < c.unit ? some : 0;
-    }
-    before = __reduce_add_sync(kFull, before);
-    units_before = __reduce_add_sync(kFull, units_before);
-    total = __reduce_add_sync(kFull, total);
-    units = __reduce_add_sync(kFull, units);
-    if (lane == 0)
-        sums_s[warp] = make_int4(before, units_before, total, units);
-    __syncthreads();
-    before = units_before = total = units = 0;
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
-        before += sums_s[i].x;
-        units_before += sums_s[i].y;
-        total += sums_s[i].z;
-        units += sums_s[i].w;
-    }
     wait_for_kernel_before();
-    const int tiles = c.range.tiles();
-    // the line as it was dealt
-    const int cost = start_cost(p, total, w.runs);
-    const int share = (total + cost * units + w.runs - 1) / w.runs;
-    const int start = before + cost * units_before, first_tile = start + cost;
-    const int x0 = tiles > 0 ? first_tile / share : 0;
-    const int x1 = tiles > 0 ? (first_tile + tiles - 1) / share : -1;
-    // written by its run, or no row (with kSplit the same for the whole block)
-    if ((tiles > 0 && x0 == x1) || c.row0 + r >= c.row1)
+    if (int(blockIdx.x) >= w.splits) {
+        rows_without_keys<kSplit>(p, int(blockIdx.x) - w.splits, int(gridDim.x) - w.splits);
         return;
+    }
+    // the run that left this block's unit open, and the last one that goes on with it
+    int continued[kMaxCtas / 32], unit = -1, x0 = 0, slot0 = 0, count = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxCtas / 32; ++i) {
+        const int x = 32 * i + lane;
+        const uint4 e = x < w.runs ? ld16_in(w.ends + x, ends_span(w), err)
+                                   : make_uint4(~0u, ~0u, 0u, 0u);
+        continued[i] = int(e.x);
+        const unsigned open = __ballot_sync(kFull, int(e.y) >= 0);
+        const int nth = int(blockIdx.x) - count;
+        count += __popc(open);
+        if (nth >= 0 && nth < __popc(open)) {
+            const unsigned before = open & ((1u << lane) - 1u);
+            const int from = __ffs(__ballot_sync(kFull, ((open >> lane) & 1u) && __popc(before) == nth)) - 1;
+            x0 = 32 * i + from;
+            unit = __shfl_sync(kFull, int(e.y), from);
+            slot0 = __shfl_sync(kFull, int(e.z), from);
+        }
+    }
+    const int r = row_of_block(kSplit);
+    // fewer units are open, or no row (with kSplit the same for the whole block)
+    if (unit < 0 || !has_row(p, unit, r))
+        return;
+    int x1 = x0;
+#pragma unroll
+    for (int i = 0; i < kMaxCtas / 32; ++i)
+        x1 = continued[i] == unit ? max(x1, 32 * i + lane) : x1;
+    x1 = __reduce_max_sync(kFull, x1);
     const Span ps = partial_span(w);
-    const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
-    // the first run may have begun with an earlier unit
-    const int slot0 = x0 * share >= start ? 0 : 1;
-    const float *ms = w.partials + kRows * DSV4_HEAD_DIM + r;
-    const auto part = [&](int x) { return (size_t(x) * 2 + (x == x0 ? slot0 : 0)) * kPartialFloats; };
+    const auto part = [&](int x) {
+        return w.partials + (size_t(x) * 2 + (x == x0 ? slot0 : 0)) * kPartialFloats;
+    };
+    // a run's m and sum for the row, and the lane's share of its O
+    struct Part {
+        float m, n;
+        float4 o[4];
+    };
+    const auto load = [&](int x) {
+        const float *from = x <= x1 ? part(x) : nullptr;
+        Part q;
+        q.m = q.n = 0.0f;
+        if (from != nullptr) {
+            q.m = ld_f32_in(from + kRows * DSV4_HEAD_DIM + r, ps, err);
+            q.n = ld_f32_in(from + kRows * DSV4_HEAD_DIM + kRows + r, ps, err);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            q.o[k] = from != nullptr ? ld_f4_in(from + r * DSV4_HEAD_DIM + 4 * lane + 128 * k, ps, err)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        return q;
+    };
+    const int step = kSplit ? kJoinWarps : 1;
+    int x = x0 + (kSplit ? warp : 0);
+    // what most rows need, on its way before the maximum is known
+    const Part a = load(x), b = load(x + step);
     float m = kUnset;
-    for (int x = x0 + lane; x <= x1; x += 32)
-        if (ld_f32_in(ms + part(x) + kRows, ps, a.b.err) != 0.0f)
-            m = fmaxf(m, ld_f32_in(ms + part(x), ps, a.b.err));
+    for (int y = x0 + lane; y <= x1; y += 32) {
+        const float *at = part(y) + kRows * DSV4_HEAD_DIM + r;
+        const float own = ld_f32_in(at, ps, err);
+        if (ld_f32_in(at + kRows, ps, err) != 0.0f)
+            m = fmaxf(m, own);
+    }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1)
         m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
@@ -711,21 +834,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fp4_join_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = x0 + (kSplit ? warp : 0); x <= x1; x += kSplit ? kJoinWarps : 1) {
-        const float n = ld_f32_in(ms + part(x) + kRows, ps, a.b.err);
-        const float f = n == 0.0f ? 0.0f : exp2_approx(ld_f32_in(ms + part(x), ps, a.b.err) - m);
-        const float *from = w.partials + part(x) + r * DSV4_HEAD_DIM + 4 * lane;
-        sum += n * f;
+    const auto add = [&](const Part &q) {
+        const float f = q.n == 0.0f ? 0.0f : exp2_approx(q.m - m);
+        sum += q.n * f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float4 v = ld_f4_in(from + 128 * k, ps, a.b.err);
-            o[k].x += v.x * f;
-            o[k].y += v.y * f;
-            o[k].z += v.z * f;
-            o[k].w += v.w * f;
+            o[k].x += q.o[k].x * f;
+            o[k].y += q.o[k].y * f;
+            o[k].z += q.o[k].z * f;
+            o[k].w += q.o[k].w * f;
         }
-    }
+    };
+    add(a);
+    add(b);
+    x += 2 * step;
+#pragma unroll 4
+    for (; x <= x1; x += step)
+        add(load(x));
     if constexpr (kSplit) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -748,22 +873,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fp4_join_kernel(const __grid_
             o[0].w += v.w;
         }
     }
-    const int64_t row = int64_t(c.request) * p.all_rows + c.row0 + r;
-    float lse;
-    const float f = finish(m, sum, sink_of(a, c.row0 + r), &lse);
-    const int first = kSplit ? warp : 0, last = kSplit ? warp : 3;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (k < first || k > last)
-            continue;
-        const float4 v = kSplit ? o[0] : o[k];
-        st8_in(a.out + row * DSV4_HEAD_DIM + 128 * k + 4 * lane,
-               f == 0.0f ? make_uint2(0u, 0u)
-                         : make_uint2(bf16x2_rn(v.x * f, v.y * f), bf16x2_rn(v.z * f, v.w * f)),
-               os, a.b.err);
-    }
-    if (lane == 0 && first == 0 && a.lse != nullptr)
-        st_f32_in(a.lse + row, lse, Span{a.lse, rows_of(a) * 4u}, a.b.err);
+    write_row<kSplit>(p, unit, r, m, sum, o);
 }
 
 int configure(int *sms)
@@ -789,7 +899,7 @@ int configure(int *sms)
 
 size_t fp4_attention_workspace()
 {
-    return size_t(kMaxCtas) * 2 * kPartialFloats * sizeof(float);
+    return size_t(kMaxCtas) * (2 * kPartialFloats * sizeof(float) + sizeof(RunEnds));
 }
 
 int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_t stream)
@@ -800,21 +910,24 @@ int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_
     WParams w;
     w.p = tile_params(a, kRows);
     w.partials = static_cast<float *>(workspace);
+    w.ends = reinterpret_cast<RunEnds *>(w.partials + size_t(kMaxCtas) * 2 * kPartialFloats);
     const int64_t most = (int64_t(a.b.width) * a.b.block_size + kTileKeys - 1) / kTileKeys * w.p.units;
     int runs = sms < kMaxCtas ? sms : kMaxCtas;
     runs = most < runs ? int(most) : runs;
     w.runs = runs;
+    // each is begun by a run that is not the last
+    w.splits = w.p.units < runs - 1 ? w.p.units : runs - 1;
     const int st = launch_after(fp4_attention_kernel, dim3(unsigned(runs)), dim3(kThreads), stream, w,
                                 kSmemBytes);
     if (st != DSV4_OK)
         return st;
+    const int idle = w.p.units < kIdleColumns ? w.p.units : kIdleColumns;
+    const unsigned columns = unsigned(w.splits + idle);
     const unsigned rows = unsigned(w.p.all_rows < kRows ? w.p.all_rows : kRows);
     // a unit spans runs / units of them and at most two more
     if (runs / w.p.units >= kJoinWarps)
-        return launch_after(fp4_join_kernel<true>, dim3(unsigned(w.p.units), rows),
-                            dim3(kJoinWarps * 32), stream, w);
-    return launch_after(fp4_join_kernel<false>,
-                        dim3(unsigned(w.p.units), (rows + kJoinWarps - 1) / kJoinWarps),
+        return launch_after(fp4_join_kernel<true>, dim3(columns, rows), dim3(kJoinWarps * 32), stream, w);
+    return launch_after(fp4_join_kernel<false>, dim3(columns, (rows + kJoinWarps - 1) / kJoinWarps),
                         dim3(kJoinWarps * 32), stream, w);
 }
 
