@@ -210,7 +210,8 @@ int dsv4_fp4_evict(uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
         weights_stride > INT64_MAX / 4096 / 65536 || budget < 1 || recent < 0 || recent > budget ||
         new_table_width < 1 || new_table_stride < new_table_width ||
         new_table_stride > INT64_MAX / 4096 / 65536 ||
-        int64_t(new_table_width) * block_size < budget)
+        int64_t(new_table_width) * block_size < budget ||
+        int64_t(batch) * budget > int64_t(INT32_MAX) * dsv4::kFp4MoveRows)  // a grid's CTAs
         return DSV4_ERR_SHAPE;
     if (batch == 0)
         return DSV4_OK;

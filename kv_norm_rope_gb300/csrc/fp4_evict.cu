@@ -45,7 +45,7 @@ constexpr int kMaxCluster = 16;  // more than the portable 8, where the device a
 constexpr int kWeightsPerCta = 16384;
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 64;              // of a CTA
+constexpr int kMoveRows = kFp4MoveRows;    // of a CTA
 constexpr int kPieces = kFp4Slot / 16;     // of a row: 22 of data, one of scales
 constexpr int kMovePieces = (kMoveRows * kPieces + kMoveThreads - 1) / kMoveThreads;
 
@@ -136,8 +136,9 @@ __global__ void __launch_bounds__(kSelectThreads) fp4_select_kernel(const EParam
     // the recent rows, or all there are
     const int candidates = n <= a.budget ? 0 : n - a.recent;
     const int chosen = n <= a.budget ? 0 : a.budget - a.recent;
-    for (int i = rank * kSelectThreads + tid; i < a.budget - chosen; i += ctas * kSelectThreads)
-        st_i32_in(kept + chosen + i, i < n - candidates ? candidates + i : -1, kept_span(a), a.b.err);
+    // (in 64 bits: a budget may be less than a step below 2^31)
+    for (int64_t i = rank * kSelectThreads + tid; i < a.budget - chosen; i += ctas * kSelectThreads)
+        st_i32_in(kept + chosen + i, i < n - candidates ? candidates + int(i) : -1, kept_span(a), a.b.err);
     if (chosen == 0)
         return;  // the same in every CTA of the cluster
 

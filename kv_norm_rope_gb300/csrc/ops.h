@@ -80,6 +80,8 @@ struct Fp4AttentionArgs {
     int32_t weights_width;
 };
 
+constexpr int kFp4MoveRows = 64;  // kept rows that a CTA of the eviction moves
+
 struct Fp4EvictArgs {
     Fp4Batch b;             // b.cache is written too
     const float *weights;
