@@ -590,25 +590,27 @@ def fp4_attention(q, kv_cache, num_blocks: int, block_size: int, block_table, se
 
     block_table: int32 [B, W] (rows may be strided); seq_lens: int32 [B], the Q new tokens
     included; lse: optional fp32 [B, Q, H]; sinks: optional fp32 [H]; window: keys a token
-    sees, 0 for all.  workspace: uint8 of fp4_attention_workspace_bytes(); None takes one
-    from torch's allocator for the call, on ``stream``, which is then torch's current one,
-    or a torch stream."""
+    sees, 0 for all.  workspace: uint8 of fp4_attention_workspace_bytes(), or the address of
+    that many; None takes one from torch's allocator for the call, on ``stream``, which is
+    then torch's current one, or a torch stream."""
     B, Q, H, (stride, width) = _check_attention(q, kv_cache, num_blocks, block_size, block_table,
                                                 seq_lens)
     _check("out", out, "bf16", q.numel())
     _check("lse", lse, "f32", B * Q * H)
     _check("sinks", sinks, "f32", H)
     _check("device_error", device_error, "i32")
+    workspace_bytes = fp4_attention_workspace_bytes()
     if workspace is None:
-        workspace = _workspace(fp4_attention_workspace_bytes(), q.device, stream)
-    else:
+        workspace = _workspace(workspace_bytes, q.device, stream)
+    elif not isinstance(workspace, int):
         _check("workspace", workspace, "bytes")
+        workspace_bytes = workspace.numel() * workspace.element_size()
     _on_cuda(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
              sinks=sinks, workspace=workspace, device_error=device_error)
     st = lib().dsv4_fp4_attention(
         q.data_ptr(), _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
         _ptr(seq_lens), B, Q, H, scale, window, _ptr(sinks), _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(device_error), _stream_handle(stream))
+        workspace_bytes, _ptr(device_error), _stream_handle(stream))
     if st != OK:
         raise Dsv4Error(st, "dsv4_fp4_attention")
 
