@@ -312,10 +312,12 @@ __device__ __forceinline__ void sum_role(const WParams &w, Shared &s, Sweep sw)
     const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
     const float scale = a.scale * (kLog2e * kOperandUnit);
     const Span ws{a.weights, (uint64_t(a.b.batch - 1) * a.weights_stride + a.weights_width) * 4u};
+    bool some_out = false;  // some row of the pass is left out
     for (uint32_t t = 0; sw.live; ++t) {
         const int rows = pass_rows(w, sw.pass), n = sw.c.n;
         if (sw.new_pass) {
             named_barrier(1, 256);  // the rows before are done with
+            bool out = false;
             if (tid < kRows) {
                 const int r = sw.pass * kRows + tid;
                 float lse = INFINITY;  // no row: its exponentials are 0
@@ -323,15 +325,18 @@ __device__ __forceinline__ void sum_role(const WParams &w, Shared &s, Sweep sw)
                 if (tid < rows) {
                     lse = kLog2e * ldg_f32_in(a.lse + int64_t(sw.c.request) * p.all_rows + r,
                                               Span{a.lse, rows_of(a) * 4u}, a.b.err);
-                    if (lse == -INFINITY)
-                        lse = INFINITY;  // a row that saw nothing adds nothing
                     to = n - a.q_len + 1 + int(fastdiv(uint32_t(r), p.head_div));
+                    // a row without a sum adds nothing, and sees no key: one that is
+                    // not finite would make NaN of its exponential
+                    out = lse == -INFINITY;
+                    if (out)
+                        to = 0;
                 }
                 s.lse[tid] = lse;
                 s.seen_to[tid] = to;
                 s.seen_from[tid] = a.window > 0 ? to - a.window : INT32_MIN;
             }
-            named_barrier(1, 256);
+            some_out = named_barrier_any(1, 256, out);
         }
         const int tile = sw.c.tile + sw.k, i = tile * kTileKeys + key;
         const bool mine = group == 0 && i >= sw.c.range.lo && i < sw.c.range.hi;
@@ -347,7 +352,7 @@ __device__ __forceinline__ void sum_role(const WParams &w, Shared &s, Sweep sw)
         }
         tmem_fence_after();
         // every row of the group sees every key of the tile
-        const bool whole = rows >= col0 + kCols && (tile + 1) * kTileKeys <= s.seen_to[col0] &&
+        const bool whole = !some_out && rows >= col0 + kCols && (tile + 1) * kTileKeys <= s.seen_to[col0] &&
                            tile * kTileKeys >= s.seen_from[col0 + kCols - 1];
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
