@@ -439,9 +439,11 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
  *               that may run at the same time need two.
  *
  * Scores and sums are fp32; the probabilities are rounded to bf16 for the product with
- * the rows.  Rows are taken as they are stored while their values are below 2^83.  One
- * that holds a value that is not finite, or a group with e_g > 208, gives NaN (all dims and
- * lse) to the tokens that see it and nothing to the others.  A key past every token's
+ * the rows.  A score below fp32's range is -infinity: its key takes no part.  Rows are taken
+ * as they are stored while their values are from 2^-46 to 2^83 in magnitude, or 0; a
+ * smaller one may be taken as any other that small, 0 among them.  A row that holds a value
+ * that is not finite, or a group with e_g > 208, gives NaN (all dims and lse) to the tokens
+ * that see it and nothing to the others.  A key past every token's
  * length, or outside every window, is not read, whatever its slot holds.
  * A block outside [0, num_blocks) sets DSV4_DEVERR_SLOT_RANGE and its keys take no part;
  * a length past table_width * block_size sets it too and counts as that many.
@@ -457,7 +459,7 @@ int dsv4_fp4_attention(const void *q, const uint8_t *kv_cache, int64_t num_block
 /*
  * The attention each key got: weights[b][i] += sum over the tokens and heads of request b
  * that see key i of exp(scale * (q . k_i) - lse).  Arguments as above, lse as
- * dsv4_fp4_attention left it (-infinity: the token adds nothing); weights (device) fp32,
+ * dsv4_fp4_attention left it (-infinity: the token adds nothing, whatever it sees); weights (device) fp32,
  * row b weights_stride elements after row b - 1.  Row b has at least seq_lens[b] elements:
  * weights_width of them are the caller's, and a longer request sets
  * DSV4_DEVERR_SLOT_RANGE and adds to those only.  Each sum is taken in a fixed order:
