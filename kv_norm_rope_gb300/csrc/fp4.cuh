@@ -98,8 +98,9 @@ __device__ __forceinline__ uint4 fp4x8_to_bf16(uint32_t w, uint32_t scale2)
 
 // As matrix operands the rows are held times 2^-80: then 2^126 and the scale are one
 // factor, 2^(e - 81), a bf16 for e <= 208 (values to 2^83; what stands above, e = 255
-// among it, is `above`: infinite, or 0 where the row is marked instead).  What becomes subnormal was below 2^-46, far under the fp32
-// rounding of any sum with a normalised row.  Products take the 2^80 back in fp32.
+// among it, is `above`: infinite, or 0 where the row is marked instead).  What becomes
+// subnormal was below 2^-46, far under the fp32 rounding of any sum with a normalised
+// row.  Products take the 2^80 back in fp32.
 constexpr float kOperandUnit = 0x1p80f;
 
 constexpr uint32_t kOperandTop = 208u;

@@ -19,10 +19,10 @@
 //    own, so the next tile is converted under the products of this one.
 //  * Warps 0..7 do the softmax: warp w has the keys of lanes 32 (w % 4).. and rows
 //    32 (w / 4)..; a thread has one key and 32 rows.  Warps 8..23 convert, warp 24
-//    issues the products, warp 25 notes the run's ends.  The teams of converting warps share one code path, so
-//    that all loops fit the instruction cache together, and warp 24's warpgroup gives
-//    registers to the softmax: a spill costs a trip to L2, as shared memory leaves
-//    little of L1.
+//    issues the products, warp 25 notes the run's ends.  The teams of converting
+//    warps share one code path, so that all loops fit the instruction cache together,
+//    and warp 24's warpgroup gives registers to the softmax: a spill costs a trip to
+//    L2, as shared memory leaves little of L1.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the
 //    largest score of the first tile it saw; p = 2^(x - m) is taken against that,
 //    and only when some x exceeds m by more than kSlack is m moved and everything
@@ -40,8 +40,9 @@
 // P is rounded to bf16 as an operand (half a step, at most 2^-8 of the value, to
 // either side); the sum that divides it is of the unrounded p.
 //
-// One request of 262147 keys, 128 heads: 117 us, 590 TFLOP/s; 128 requests of 1024 to
-// 8192 keys, 128 heads: 240 us, 604 TFLOP/s; 48 of up to 4096, 64 heads: 42 us.  By
+// One request of 262147 keys, 128 heads: 115.5 to 119.4 us in several runs, 576 to 595
+// TFLOP/s; 128 requests of 1024 to 8192 keys, 128 heads: 239 us, 607 TFLOP/s; 48 of up
+// to 4096, 64 heads: 41 us (their results joined included).  By
 // arithmetic, an instruction of either product reads 6 KB of shared memory for 32
 // cycles of the matrix unit, so at 128 bytes a cycle shared memory bounds them at two
 // thirds of the unit's rate, and the converted rows are written through it as well.
@@ -688,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attention_kernel(const __grid
 // look through the units for those without keys, each at its share of them.  (A column a
 // unit, each finding its runs by a look at all lengths, took 6.1 ms for 64000 idle
 // requests, against 0.3.)  What the first two runs left of a row is loaded before the maximum
-// is known: 17.5 us instead of 18.5 for two requests of 8 heads, 41.0 instead of 42.7 for 48.
+// is known: 17.3 us instead of 18.4 for two requests of 8 heads, 41.0 instead of 42.8 for
+// 48 of 64.
 constexpr int kJoinWarps = 8;
 constexpr int kIdleColumns = 64;
 static_assert(kMaxCtas % 32 == 0, "the join's lanes hold the ends of kMaxCtas / 32 runs each");

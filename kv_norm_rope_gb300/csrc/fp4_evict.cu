@@ -20,7 +20,7 @@
 //
 // The move is bound by memory, 368 bytes read and written a row: a CTA looks up where
 // 64 rows are and go, then copies them 16 bytes a thread with all its loads in flight
-// (98304 rows: 14 us, 5.2 TB/s; a warp a row took 25); it is launched while the
+// (98304 rows: 14 us, 5.2 TB/s, in a list of launches; a warp a row took 25); it is launched while the
 // selection ends.
 
 #include <cooperative_groups.h>

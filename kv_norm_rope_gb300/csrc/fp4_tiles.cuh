@@ -3,8 +3,8 @@
 // dealt out to CTAs, and how a tile of cache rows becomes a bf16 matrix operand.
 //
 // A tile is 128 keys, aligned in the request.  The tiles that some row of a row
-// tile sees, over all requests in order, form one line; each CTA takes an equal
-// run of it.  So a long request is shared by many CTAs and short ones share a
+// tile sees, over all requests in order, form one line; each CTA takes a run of it of
+// equal cost (start_cost() below).  So a long request is shared by many CTAs and short ones share a
 // CTA, whatever the lengths, which only the device knows.
 #pragma once
 
