@@ -572,6 +572,12 @@ def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens)
     return B, Q, H, _check_rows("block_table", block_table, "i32", B)
 
 
+def _int32(n: int) -> int:
+    """n in 32 bits, which ctypes would cut to its low ones: past the largest the largest
+    (a window of all keys, a number past any limit), below 0 the -1 that is refused."""
+    return max(-1, min(n, 2 ** 31 - 1))
+
+
 _workspace_bytes = 0
 
 
@@ -609,7 +615,7 @@ def fp4_attention(q, kv_cache, num_blocks: int, block_size: int, block_table, se
              sinks=sinks, workspace=workspace, device_error=device_error)
     st = lib().dsv4_fp4_attention(
         q.data_ptr(), _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
-        _ptr(seq_lens), B, Q, H, scale, window, _ptr(sinks), _ptr(out), _ptr(lse), _ptr(workspace),
+        _ptr(seq_lens), B, Q, H, scale, _int32(window), _ptr(sinks), _ptr(out), _ptr(lse), _ptr(workspace),
         workspace_bytes, _ptr(device_error), _stream_handle(stream))
     if st != OK:
         raise Dsv4Error(st, "dsv4_fp4_attention")
@@ -641,7 +647,7 @@ def fp4_attention_weights(q, kv_cache, num_blocks: int, block_size: int, block_t
              weights=weights, device_error=device_error)
     st = lib().dsv4_fp4_attention_weights(
         q.data_ptr(), _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
-        _ptr(seq_lens), B, Q, H, scale, window, _ptr(lse), weights.data_ptr(), w_stride, w_width,
+        _ptr(seq_lens), B, Q, H, scale, _int32(window), _ptr(lse), weights.data_ptr(), w_stride, w_width,
         _ptr(device_error), _stream_handle(stream))
     if st != OK:
         raise Dsv4Error(st, "dsv4_fp4_attention_weights")
@@ -671,7 +677,7 @@ def fp4_evict(kv_cache, num_blocks: int, block_size: int, block_table, seq_lens,
              new_weights=new_weights, device_error=device_error)
     st = lib().dsv4_fp4_evict(
         _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
-        _ptr(seq_lens), B, weights.data_ptr(), w_stride, w_width, budget, recent,
+        _ptr(seq_lens), B, weights.data_ptr(), w_stride, w_width, budget, _int32(recent),
         new_block_table.data_ptr(), n_stride, n_width, _ptr(kept), _ptr(new_seq_lens),
         _ptr(new_weights), _ptr(device_error), _stream_handle(stream))
     if st != OK:
