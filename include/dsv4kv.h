@@ -447,6 +447,9 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
  * length, or outside every window, is not read, whatever its slot holds.
  * A block outside [0, num_blocks) sets DSV4_DEVERR_SLOT_RANGE and its keys take no part;
  * a length past table_width * block_size sets it too and counts as that many.
+ * batch <= 65535 and num_blocks < 2^31; what is counted in 32 bits (tiles of 64 query rows by
+ * tiles of 128 keys, and two more a row tile) has to stay below 2^31 - 1024, else
+ * DSV4_ERR_SHAPE.
  */
 size_t dsv4_fp4_attention_workspace_bytes(void);
 int dsv4_fp4_attention(const void *q, const uint8_t *kv_cache, int64_t num_blocks,
@@ -490,6 +493,7 @@ int dsv4_fp4_attention_weights(const void *q, const uint8_t *kv_cache, int64_t n
  *  new_seq_lens     (device) int32 [batch].  May be seq_lens itself.
  *  new_weights      (device) fp32 [batch, budget]: the kept rows' weights; 0 after them.  May not
  *                   overlap weights.
+ * batch <= 65535, num_blocks < 2^31 and batch * budget <= 2^37 - 64.
  * A block outside [0, num_blocks) in either table sets DSV4_DEVERR_SLOT_RANGE and the row
  * is not copied.  Scale bytes, codes and rope dims are moved as they are.
  */
