@@ -61,7 +61,8 @@ typedef enum {
     DSV4_ERR_NULL = 1,   /* a required pointer is NULL */
     DSV4_ERR_SHAPE = 2,  /* a size is out of range */
     DSV4_ERR_ALIGN = 3,  /* a pointer is not aligned as documented */
-    DSV4_ERR_VALUE = 4,  /* eps negative or not finite; unknown store mode or variant */
+    DSV4_ERR_VALUE = 4,  /* eps or another number outside its range; unknown store mode, variant,
+                            type, layout or scaling */
     DSV4_ERR_CUDA = 5    /* the CUDA runtime reported an error while launching */
 } dsv4_status;
 
@@ -87,16 +88,17 @@ enum {
 enum {
     DSV4_DEVERR_SLOT_RANGE = 1, /* slot_mapping[t] >= num_blocks*block_size: cache row not written */
     DSV4_DEVERR_POS_RANGE = 2,  /* positions[t] < 0 or >= max_position: token not written at all */
-    DSV4_DEVERR_TIMEOUT = 4,    /* the KV-row kernel (num_heads 0, STREAM), the 4-bit attention or
-                                   its weights: a bounded wait inside the kernel ran out (never
-                                   expected); the outputs of that launch are undefined */
+    DSV4_DEVERR_TIMEOUT = 4,    /* the KV-row kernel (num_heads 0, STREAM), an attention or the
+                                   attention weights: a bounded wait inside the kernel ran out
+                                   (never expected); the outputs of that launch are undefined */
     DSV4_DEVERR_BOUNDS = 8      /* the checked build only (libdsv4kv_checked.so, compiled with
                                    DSV4_CHECK_BOUNDS): an access would have touched bytes outside
                                    the buffer it belongs to; it was skipped (never expected) */
 };
 
-/* store modes and launch variants of dsv4_qnorm_rope_kv_insert_variant */
-enum { DSV4_STORE_FP8 = 0, DSV4_STORE_BF16 = 1 };
+/* store modes and launch variants of dsv4_qnorm_rope_kv_insert_variant; of the stores the
+ * 4-bit and the indexer one are taken by dsv4_tree_keep only */
+enum { DSV4_STORE_FP8 = 0, DSV4_STORE_BF16 = 1, DSV4_STORE_FP4 = 2, DSV4_STORE_INDEXER = 3 };
 enum {
     DSV4_VARIANT_AUTO = 0,    /* pick from the row count and the SM count (below) */
     DSV4_VARIANT_SMALL = 1,   /* one row per warp, 2-warp CTAs, one wave: small batches */
@@ -504,6 +506,156 @@ int dsv4_fp4_evict(uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
                    int32_t recent, const int32_t *new_block_table, int64_t new_table_stride,
                    int32_t new_table_width, int32_t *kept, int32_t *new_seq_lens,
                    float *new_weights, int32_t *device_error, void *stream);
+
+/*
+ * ---- Attention over the FP8 and bf16 caches, for chains of new tokens and trees of drafted ones
+ *
+ * Every head of a new token attends to its request's latent rows, which are keys and values in
+ * one: s_i = scale * (q . k_i), out = sum of softmax(s)_i k_i over the visible keys.
+ *
+ *  store_mode   DSV4_STORE_FP8 (kv_cache uint8, layout of dsv4_qnorm_rope_kv_quant_insert, 8-byte
+ *               aligned) or DSV4_STORE_BF16 (kv_cache bf16 [num_blocks, block_size, 512], 16-byte
+ *               aligned).  Reads and products are the same for either.
+ *  q            (device) bf16 [batch, q_len, num_heads, 512], contiguous, 16-byte aligned.
+ *               q_len <= 2^24.
+ *  block_table  (device) int32: row b (table_stride elements after row b - 1) lists the
+ *               table_width blocks of request b in order.  Key i of request b is slot
+ *               i % block_size of block block_table[b][i / block_size].  Entries that no
+ *               length reaches are not read.  table_width * block_size <= 2^30.
+ *  seq_lens     (device) int32 [batch]: keys of each request, its q_len new tokens included;
+ *               0 is an idle request.
+ *  scale        of the scores, in (0, 2^32].
+ *  window       0 or the keys that a token sees at most.
+ *  tree         (device, nullable) uint64 [batch, q_len], q_len <= 64.  Without it token j sees keys
+ *               [max(0, n - window), n) with n = seq_lens[b] - q_len + 1 + j (all of [0, n) for
+ *               window 0).  With it the last q_len keys of a request are those of its drafted
+ *               tokens, in any order that suits the caller, and bit i of tree[b][j] says that token
+ *               j sees drafted key i: its ancestors' and its own.  With c = seq_lens[b] - q_len keys
+ *               before them and d bits set, token j also sees keys [max(0, c + d - window), c) (all
+ *               of [0, c) for window 0); window is 0 or at least q_len.  A token without a bit is
+ *               padding and sees nothing.  Bits of q_len and above, and those of keys before
+ *               the request's first (seq_lens[b] < q_len), name no key.
+ *  sinks        (device, nullable) fp32 [num_heads]: a score that takes part in the softmax
+ *               of its head and has no value.
+ *  out          (device) bf16 [batch, q_len, num_heads, 512], 16-byte aligned; may not overlap q.
+ *               A token that sees no key gives zeros.
+ *  lse          (device, nullable) fp32 [batch, q_len, num_heads]: log of the sum of exp over
+ *               the visible scores and the sink (-infinity where there is neither).
+ *  workspace    (device) at least dsv4_latent_attention_workspace_bytes() bytes, 16-byte aligned.
+ *               Its contents need no preparation and mean nothing after the call; two calls
+ *               that may run at the same time need two.
+ *
+ * Scores and sums are fp32; the probabilities are rounded to bf16 for the product with the
+ * rows.  A score below fp32's range is -infinity (its key takes no part), one above it gives NaN.  FP8
+ * rows are taken as they are stored while their values are from 2^-78 to 2^63 in magnitude, or
+ * 0; a smaller one may be taken as any other that small, 0 among them.  A row that holds a value
+ * that is not finite (or, in the FP8 cache, a block with an exponent byte above 182) gives NaN (all
+ * dims and lse) to the tokens that see it and nothing to the others.  A key that no length or window
+ * reaches is not read, whatever its slot holds.
+ * A block outside [0, num_blocks) sets DSV4_DEVERR_SLOT_RANGE and its keys take no part;
+ * a length past table_width * block_size sets it too and counts as that many.
+ * The same call gives the same bits.
+ * batch <= 65535 and num_blocks < 2^31; what is counted in 32 bits (tiles of 64 query rows by
+ * tiles of 64 keys, and four more a row tile) has to stay below 2^31 - 1024, else
+ * DSV4_ERR_SHAPE.
+ */
+size_t dsv4_latent_attention_workspace_bytes(void);
+int dsv4_latent_attention(int store_mode, const void *q, const void *kv_cache, int64_t num_blocks,
+                          int32_t block_size, const int32_t *block_table, int64_t table_stride,
+                          int32_t table_width, const int32_t *seq_lens, int32_t batch, int32_t q_len,
+                          int32_t num_heads, float scale, int32_t window, const uint64_t *tree,
+                          const float *sinks, void *out, float *lse, void *workspace,
+                          size_t workspace_bytes, int32_t *device_error, void *stream);
+
+/*
+ * After the verification of a tree: of a request's last q_len keys those of the accepted path are
+ * kept, moved together behind the keys before them, in place.  With c = seq_lens[b] - q_len, row
+ * c + path[b][i] goes to c + i for i < path_lens[b], and new_seq_lens[b] = c + path_lens[b].
+ * (Rows were rotated for their depth in the tree, which is their place on the path.)
+ *
+ *  store_mode    DSV4_STORE_FP8, DSV4_STORE_BF16, DSV4_STORE_FP4 or DSV4_STORE_INDEXER: kv_cache is a
+ *                cache of that store, aligned to 8, 16, 16 or 4 bytes.  A server with several caches
+ *                calls it for each (new_seq_lens apart from seq_lens until the last).
+ *  path          (device) int32 [batch, q_len], q_len <= 64: entries rise and are in [0, q_len).
+ *  path_lens     (device) int32 [batch], in [0, q_len].
+ *  new_seq_lens  (device) int32 [batch].  May be seq_lens itself.
+ * Other arguments as in dsv4_latent_attention.  Requests of one call share no block that a
+ * drafted key lies in.  Rows that do not move, rows behind the kept ones among them, are not written.
+ * A path that does not rise, leaves the drafted keys or is longer than q_len ends before the first
+ * such entry and sets DSV4_DEVERR_SLOT_RANGE, and so does a negative length, which counts as 0; a
+ * request of fewer than q_len keys is left as it is, with that bit, an idle one (seq_lens[b] 0)
+ * without.  A move from or to a block outside [0, num_blocks) is left out and sets it too.
+ */
+int dsv4_tree_keep(int store_mode, void *kv_cache, int64_t num_blocks, int32_t block_size,
+                   const int32_t *block_table, int64_t table_stride, int32_t table_width,
+                   const int32_t *seq_lens, int32_t batch, int32_t q_len, const int32_t *path,
+                   const int32_t *path_lens, int32_t *new_seq_lens, int32_t *device_error, void *stream);
+
+/*
+ * ---- Rotary positions
+ *
+ * Frequencies (host arithmetic, no CUDA call): frequencies[i], i < rope_dim / 2, is the angle per
+ * position of pair i in radians, f_i = theta^(-2i / rope_dim), stretched for long contexts:
+ *   DSV4_ROPE_PLAIN   f_i;
+ *   DSV4_ROPE_LINEAR  f_i / factor;
+ *   DSV4_ROPE_NTK     theta * factor^(rope_dim / (rope_dim - 2)) for theta;
+ *   DSV4_ROPE_YARN    f_i (1 - r_i) + f_i / factor r_i, r_i rising from 0 to 1 between the pair that
+ *                     makes turns_fast turns over original_positions and the one that makes
+ *                     turns_slow (Peng et al., "YaRN", 2023; the ramp goes by the pair's index, its
+ *                     ends rounded outwards).
+ * rope_dim even, 2 to 256; theta in (1, 10^12]; factor in [1, 10^6] (not looked at for PLAIN); the last
+ * three for YARN only: positive, turns_fast > turns_slow.
+ */
+enum { DSV4_ROPE_PLAIN = 0, DSV4_ROPE_LINEAR = 1, DSV4_ROPE_NTK = 2, DSV4_ROPE_YARN = 3 };
+int dsv4_rope_frequencies(int scaling, int32_t rope_dim, double theta, double factor,
+                          double original_positions, double turns_fast, double turns_slow,
+                          double *frequencies);
+
+/*
+ * The table that every insert and dsv4_rope_rows take: row r, for position p = positions[r], or
+ * first + r where positions is NULL, holds magnitude * cos(p f_i) in columns i < rope_dim / 2 and
+ * magnitude * sin(p f_i) in columns rope_dim / 2 + i.  Angles are exact to 2^-32 turns for every
+ * position below 2^32, values to 0.6 fp32 steps at the row's magnitude.
+ *
+ *  frequencies   (host) double [rope_dim / 2], in [0, 65536); read before the call returns.
+ *  magnitude     0 or 2^-16 to 2^16 in absolute value (a stretched context's scale of q and k).
+ *  positions     (device, nullable) int64 [num_positions], 8-byte aligned.  One outside [0, 2^32)
+ *                sets DSV4_DEVERR_POS_RANGE and its row is not written.
+ *  first         >= 0, first + num_positions <= 2^32 (not looked at with positions).
+ *  cos_sin       (device) fp32 [num_positions, rope_dim], 4-byte aligned.  (Calls that take the
+ *                table want it 16-byte aligned, and 64 wide for the inserts.)
+ */
+int dsv4_rope_table(const double *frequencies, int32_t rope_dim, double magnitude,
+                    const int64_t *positions, int64_t first, int64_t num_positions, float *cos_sin,
+                    int32_t *device_error, void *stream);
+
+/*
+ * Rotation of rows: the pairs of dims [offset, offset + rope_dim) of every head of token t are turned by
+ * the angles of row positions[t] of the table: (a, b) -> (a cos - b sin, b cos + a sin), or back,
+ * (a cos + b sin, b cos - a sin), with inverse 1, which is also the gradient: that of x is the
+ * inverse of the gradient of out.  An attention's output is turned back by its token's position: its
+ * trailing dims are sums of rows that were turned by theirs.
+ *
+ *  type       DSV4_TYPE_BF16, DSV4_TYPE_FP16 or DSV4_TYPE_FP32, of x and out; the arithmetic is
+ *             fp32, rounded once.
+ *  x, out     (device) [num_tokens, num_heads, width] with strides in elements (0 to 2^31), the
+ *             innermost 1; aligned to their element.  out is x itself, with the same strides: only
+ *             the rotated dims are read and written; or apart from it: the other dims are copied.  The
+ *             rows of out do not overlap; those of x may (stride 0).
+ *  layout     DSV4_ROPE_PAIRS: pair i is dims (offset + 2i, offset + 2i + 1);
+ *             DSV4_ROPE_HALF: dims (offset + i, offset + rope_dim / 2 + i).
+ *  positions  (device) int64 [num_tokens], 8-byte aligned.  One outside [0, max_position) sets
+ *             DSV4_DEVERR_POS_RANGE and its token's rows are not written.
+ *  cos_sin    (device) fp32 [max_position, rope_dim]: columns 0.. cos, rope_dim / 2.. sin.  16-byte aligned.
+ * rope_dim even, 2 to 256; width <= 65536; num_tokens * num_heads < 2^31; num_tokens >= 0 (0: no launch).
+ */
+enum { DSV4_TYPE_BF16 = 0, DSV4_TYPE_FP16 = 1, DSV4_TYPE_FP32 = 2 };
+enum { DSV4_ROPE_PAIRS = 0, DSV4_ROPE_HALF = 1 };
+int dsv4_rope_rows(int type, const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+                   int64_t out_token_stride, int64_t out_head_stride, int64_t num_tokens,
+                   int32_t num_heads, int32_t width, int32_t offset, int32_t rope_dim, int layout,
+                   int inverse, const int64_t *positions, const float *cos_sin, int64_t max_position,
+                   int32_t *device_error, void *stream);
 
 #ifdef __cplusplus
 }

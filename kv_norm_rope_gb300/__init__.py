@@ -26,22 +26,23 @@ CHECKED_LIB_PATH = os.path.join(_HERE, "libdsv4kv_checked.so")
 _SOURCES = ["qnorm_rope_kv_insert.cu", "dequant_gather.cu",
             "gemma_rmsnorm_mxfp8.cu", "indexer_k.cu", "kv_rows.cu", "qnorm_rope_kv_insert_half.cu",
             "wait_check.cu", "fp4_gather.cu", "fp4_attention.cu", "fp4_weights.cu",
-            "fp4_evict.cu",
-            "api.cpp", "fp4_api.cpp"]
+            "fp4_evict.cu", "latent_attention.cu", "tree_keep.cu", "rope_table.cu", "rope_rows.cu",
+            "api.cpp", "fp4_api.cpp", "latent_api.cpp", "rope_api.cpp"]
 _HEADERS = [os.path.join(_INCLUDE, "dsv4kv.h")] + [
     os.path.join(_CSRC, h)
     for h in ("launch.h", "ops.h", "fastdiv.h", "convert.cuh", "launch_status.h", "rowmath.cuh",
               "halfrow.cuh", "bulkcopy.cuh", "bounds.cuh", "bounds_range.h", "fp4.cuh",
-              "fp4_tiles.cuh", "tcgen05.cuh", "hostcheck.h")]
+              "fp4_tiles.cuh", "fp8_rows.cuh", "key_tiles.cuh", "run_join.cuh", "tcgen05.cuh", "hostcheck.h")]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # status codes and constants (mirrors include/dsv4kv.h)
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_VALUE, ERR_CUDA = range(6)
 DEVERR_SLOT_RANGE, DEVERR_POS_RANGE, DEVERR_TIMEOUT, DEVERR_BOUNDS = 1, 2, 4, 8
-STORE_FP8, STORE_BF16 = 0, 1
-_STORE_FP4 = 2  # of the checks below; the 4-bit store has its own entry point
+STORE_FP8, STORE_BF16, STORE_FP4, STORE_INDEXER = range(4)
 VARIANT_AUTO, VARIANT_SMALL, VARIANT_STREAM, VARIANT_HALF = 0, 1, 2, 4
 FP8_SLOT_BYTES, BF16_SLOT_BYTES, FP4_SLOT_BYTES = 584, 1024, 368
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = range(4)  # scalings of the frequencies
+ROPE_PAIRS, ROPE_HALF = range(2)                         # layouts of the rotated dims
 
 EXPORTS = ("dsv4_qnorm_rope_kv_quant_insert", "dsv4_qnorm_rope_kv_bf16_insert",
            "dsv4_qnorm_rope_kv_insert_variant", "dsv4_qnorm_rope_kv_rope_quant_insert",
@@ -52,7 +53,9 @@ EXPORTS = ("dsv4_qnorm_rope_kv_quant_insert", "dsv4_qnorm_rope_kv_bf16_insert",
            "dsv4_debug_bounds_flags", "dsv4_status_string", "dsv4_fp4_cache_bytes",
            "dsv4_qnorm_rope_kv_fp4_insert", "dsv4_fp4_dequant_gather",
            "dsv4_fp4_attention_workspace_bytes", "dsv4_fp4_attention",
-           "dsv4_fp4_attention_weights", "dsv4_fp4_evict")
+           "dsv4_fp4_attention_weights", "dsv4_fp4_evict",
+           "dsv4_latent_attention_workspace_bytes", "dsv4_latent_attention", "dsv4_tree_keep",
+           "dsv4_rope_frequencies", "dsv4_rope_table", "dsv4_rope_rows")
 
 
 class Dsv4Error(RuntimeError):
@@ -202,6 +205,21 @@ def _load(path: str):
     L.dsv4_fp4_attention_weights.restype = c_int
     L.dsv4_fp4_evict.argtypes = batch + [vp, i64, i32, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp]
     L.dsv4_fp4_evict.restype = c_int
+    L.dsv4_latent_attention_workspace_bytes.argtypes = []
+    L.dsv4_latent_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.dsv4_latent_attention.argtypes = ([c_int, vp] + batch + [i32, i32, f32, i32, vp, vp, vp, vp, vp,
+                                                               ctypes.c_size_t, vp, vp])
+    L.dsv4_latent_attention.restype = c_int
+    L.dsv4_tree_keep.argtypes = [c_int] + batch + [i32, vp, vp, vp, vp, vp]
+    L.dsv4_tree_keep.restype = c_int
+    f64, doubles = ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+    L.dsv4_rope_frequencies.argtypes = [c_int, i32, f64, f64, f64, f64, f64, doubles]
+    L.dsv4_rope_frequencies.restype = c_int
+    L.dsv4_rope_table.argtypes = [doubles, i32, f64, vp, i64, i64, vp, vp, vp]
+    L.dsv4_rope_table.restype = c_int
+    L.dsv4_rope_rows.argtypes = [c_int, vp, i64, i64, vp, i64, i64, i64, i32, i32, i32, i32, c_int,
+                                 c_int, vp, vp, i64, vp, vp]
+    L.dsv4_rope_rows.restype = c_int
     L.dsv4_check_bounded_wait.argtypes = [i64, vp, vp]
     L.dsv4_check_bounded_wait.restype = c_int
     L.dsv4_debug_bounds_flags.argtypes = [c_int]
@@ -312,7 +330,7 @@ def _check_step(store_mode, q, kv, w, positions, cos_sin_cache, slot_mapping, kv
     _check("cos_sin_cache", cos_sin_cache, "f32")
     if not isinstance(cos_sin_cache, int) and cos_sin_cache.numel() % 64:
         raise ValueError("cos_sin_cache must hold rows of 64 fp32 (32 cos, 32 sin)")
-    need = {STORE_FP8: fp8_cache_bytes, _STORE_FP4: fp4_cache_bytes}.get(
+    need = {STORE_FP8: fp8_cache_bytes, STORE_FP4: fp4_cache_bytes}.get(
         store_mode, bf16_cache_bytes)(num_blocks, block_size)
     _check("kv_cache", kv_cache, "bytes", min_bytes=need)
     _check("device_error", device_error, "i32")
@@ -524,7 +542,7 @@ def qnorm_rope_kv_fp4_insert(q, kv, kv_norm_weight, positions, cos_sin_cache, sl
     """dsv4_qnorm_rope_kv_fp4_insert: 4-bit (448 E2M1 + 14 UE8M0 + 64 bf16) cache rows;
     q may be None (KV rows only)."""
     T, H, max_pos = _shape_args(q, kv, positions, cos_sin_cache)
-    _check_step(_STORE_FP4, q, kv, kv_norm_weight, positions, cos_sin_cache, slot_mapping, kv_cache,
+    _check_step(STORE_FP4, q, kv, kv_norm_weight, positions, cos_sin_cache, slot_mapping, kv_cache,
                 num_blocks, block_size, device_error, T, H)
     st = lib().dsv4_qnorm_rope_kv_fp4_insert(
         _ptr(q), _ptr(kv), _ptr(kv_norm_weight), _ptr(positions), _ptr(cos_sin_cache), max_pos,
@@ -562,12 +580,17 @@ def _check_rows(name: str, t, kind: str, batch: int) -> tuple:
     return (t.stride(0) if batch > 1 else t.shape[1]), t.shape[1]
 
 
-def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens):
+def _cache_bytes(store_mode, num_blocks, block_size):
+    return {STORE_BF16: bf16_cache_bytes, STORE_FP4: fp4_cache_bytes, STORE_INDEXER: indexer_cache_bytes}.get(
+        store_mode, fp8_cache_bytes)(num_blocks, block_size)
+
+
+def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens, store_mode=STORE_FP4):
     if q.dim() != 4 or q.shape[3] != 512:
         raise ValueError(f"q: expected [batch, q_len, heads, 512], got {tuple(q.shape)}")
     B, Q, H, _ = q.shape
     _check("q", q, "bf16")
-    _check("kv_cache", kv_cache, "bytes", min_bytes=fp4_cache_bytes(num_blocks, block_size))
+    _check("kv_cache", kv_cache, "bytes", min_bytes=_cache_bytes(store_mode, num_blocks, block_size))
     _check("seq_lens", seq_lens, "i32", B)
     return B, Q, H, _check_rows("block_table", block_table, "i32", B)
 
@@ -682,3 +705,161 @@ def fp4_evict(kv_cache, num_blocks: int, block_size: int, block_table, seq_lens,
         _ptr(new_weights), _ptr(device_error), _stream_handle(stream))
     if st != OK:
         raise Dsv4Error(st, "dsv4_fp4_evict")
+
+
+# ---- attention over the FP8 and bf16 caches, trees of drafted tokens
+
+_latent_workspace_bytes = 0
+
+
+def latent_attention_workspace_bytes() -> int:
+    global _latent_workspace_bytes
+    if _latent_workspace_bytes == 0:
+        _latent_workspace_bytes = int(lib().dsv4_latent_attention_workspace_bytes())
+    return _latent_workspace_bytes
+
+
+def _launch(what: str, device, stream, call) -> None:
+    """call(stream handle) on ``device``, which need not be torch's current one."""
+    import torch
+    if not isinstance(stream, int) and stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, the tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        st = call(_stream_handle(stream))
+    else:
+        with torch.cuda.device(device):
+            st = call(_stream_handle(stream))
+    if st != OK:
+        raise Dsv4Error(st, what)
+
+
+def latent_attention(store_mode: int, q, kv_cache, num_blocks: int, block_size: int, block_table, seq_lens,
+                     scale: float, out, lse=None, sinks=None, window: int = 0, tree=None, workspace=None,
+                     device_error=None, stream=None) -> None:
+    """dsv4_latent_attention: out (bf16 [B, Q, H, 512]) = attention of q (bf16, same shape) over
+    the rows of each request in an FP8 (STORE_FP8) or bf16 (STORE_BF16) cache, key and value in one.
+
+    block_table: int32 [B, W] (rows may be strided); seq_lens: int32 [B], the Q new tokens
+    included; lse: optional fp32 [B, Q, H]; sinks: optional fp32 [H]; window: keys a token
+    sees, 0 for all.  tree: int64 [B, Q], Q at most 64, for drafted tokens that form a tree instead of
+    a chain: bit i of tree[b, j] says that token j sees drafted token i, its ancestors and itself; 0 for a
+    token that is padding.  workspace: uint8 of latent_attention_workspace_bytes(), or the address
+    of that many; None takes one from torch's allocator for the call, on ``stream``, which is
+    then torch's current one, or a torch stream."""
+    B, Q, H, (stride, width) = _check_attention(q, kv_cache, num_blocks, block_size, block_table,
+                                                seq_lens, store_mode)
+    _check("out", out, "bf16", q.numel())
+    _check("lse", lse, "f32", B * Q * H)
+    _check("sinks", sinks, "f32", H)
+    _check("tree", tree, "i64", B * Q)
+    _check("device_error", device_error, "i32")
+    workspace_bytes = latent_attention_workspace_bytes()
+    if workspace is None:
+        workspace = _workspace(workspace_bytes, q.device, stream)
+    elif not isinstance(workspace, int):
+        _check("workspace", workspace, "bytes")
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _on_cuda(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
+             sinks=sinks, tree=tree, workspace=workspace, device_error=device_error)
+    _launch("dsv4_latent_attention", q.device, stream, lambda handle: lib().dsv4_latent_attention(
+        store_mode, q.data_ptr(), _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride,
+        width, _ptr(seq_lens), B, Q, H, scale, _int32(window), _ptr(tree), _ptr(sinks), _ptr(out),
+        _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(device_error), handle))
+
+
+def tree_keep(store_mode: int, kv_cache, num_blocks: int, block_size: int, block_table, seq_lens, path,
+              path_lens, new_seq_lens, device_error=None, stream=None) -> None:
+    """dsv4_tree_keep: of each request's last Q rows (the drafted tokens') those of the accepted
+    path move together, in place: path (int32 [B, Q]) holds path_lens[b] of their indices, rising;
+    new_seq_lens (int32 [B], may be seq_lens) = what is left.  store_mode: STORE_FP8, STORE_BF16,
+    STORE_FP4 or STORE_INDEXER."""
+    if path.dim() != 2:
+        raise ValueError(f"path: expected [batch, q_len], got {tuple(path.shape)}")
+    B, Q = path.shape
+    _check("kv_cache", kv_cache, "bytes", min_bytes=_cache_bytes(store_mode, num_blocks, block_size))
+    _check("seq_lens", seq_lens, "i32", B)
+    stride, width = _check_rows("block_table", block_table, "i32", B)
+    _check("path", path, "i32")
+    _check("path_lens", path_lens, "i32", B)
+    _check("new_seq_lens", new_seq_lens, "i32", B)
+    _check("device_error", device_error, "i32")
+    _on_cuda(kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, path=path, path_lens=path_lens,
+             new_seq_lens=new_seq_lens, device_error=device_error)
+    _launch("dsv4_tree_keep", path.device, stream, lambda handle: lib().dsv4_tree_keep(
+        store_mode, _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
+        _ptr(seq_lens), B, Q, path.data_ptr(), _ptr(path_lens), _ptr(new_seq_lens), _ptr(device_error),
+        handle))
+
+
+# ---- rotary positions
+
+
+def rope_frequencies(rope_dim: int, theta: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                     original_positions: float = 0.0, turns_fast: float = 32.0,
+                     turns_slow: float = 1.0) -> tuple:
+    """dsv4_rope_frequencies: the rope_dim / 2 angles per position (floats, on the host), plain or
+    stretched for long contexts (ROPE_LINEAR, ROPE_NTK, ROPE_YARN)."""
+    out = (ctypes.c_double * (max(2, min(rope_dim, 256)) // 2))()
+    st = lib().dsv4_rope_frequencies(scaling, _int32(rope_dim), theta, factor, original_positions, turns_fast,
+                                     turns_slow, out)
+    if st != OK:
+        raise Dsv4Error(st, "dsv4_rope_frequencies")
+    return tuple(out)
+
+
+def rope_table(frequencies, out, positions=None, first: int = 0, magnitude: float = 1.0, device_error=None,
+               stream=None) -> None:
+    """dsv4_rope_table: out (fp32 [n, 2 * len(frequencies)]) = magnitude times the cosines and sines
+    of the angles of positions (int64 [n]), or of first, first + 1, ...: the cos_sin_cache that the
+    inserts and rope_rows take."""
+    pairs = len(frequencies)
+    if out.dim() != 2 or out.shape[1] != 2 * pairs:
+        raise ValueError(f"out: expected [n, {2 * pairs}], got {tuple(out.shape)}")
+    _check("out", out, "f32")
+    _check("positions", positions, "i64", out.shape[0])
+    _check("device_error", device_error, "i32")
+    _on_cuda(out=out, positions=positions, device_error=device_error)
+    angles = (ctypes.c_double * pairs)(*frequencies)
+    _launch("dsv4_rope_table", out.device, stream, lambda handle: lib().dsv4_rope_table(
+        angles, 2 * pairs, magnitude, _ptr(positions), first, out.shape[0], out.data_ptr(),
+        _ptr(device_error), handle))
+
+
+def _row_strides(name: str, t):
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: its innermost stride must be 1")
+    return (t.stride(0), t.stride(1)) if t.dim() == 3 else (t.stride(0), t.shape[1])
+
+
+def rope_rows(x, positions, cos_sin_cache, out=None, offset: int | None = None, inverse: bool = False,
+              layout: int = ROPE_PAIRS, device_error=None, stream=None) -> None:
+    """dsv4_rope_rows: dims [offset, offset + d) of x ([T, H, D] or [T, D]; bf16, fp16 or fp32; the
+    outer dims may be strided) turned by the angles of each token's position into out (None: x
+    itself), d being the width of cos_sin_cache (fp32 [max_position, d]) and offset D - d (the
+    trailing dims) unless given.  inverse: turned back, which is also the gradient's way.  layout:
+    ROPE_PAIRS (neighbouring dims) or ROPE_HALF (i and i + d / 2)."""
+    import torch
+    types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if out is None:
+        out = x
+    if x.dtype not in types:
+        raise TypeError(f"x: expected bf16, fp16 or fp32 data, got {x.dtype}")
+    if out.dtype != x.dtype:
+        raise TypeError(f"out: expected {x.dtype} data, got {out.dtype}")
+    if x.dim() not in (2, 3) or out.shape != x.shape:
+        raise ValueError(f"x, out: expected [tokens, heads, width] of one shape, got {tuple(x.shape)} and "
+                         f"{tuple(out.shape)}")
+    if cos_sin_cache.dim() != 2:
+        raise ValueError("cos_sin_cache: expected [max_position, d]")
+    max_position, dim = cos_sin_cache.shape
+    T, H, D = x.shape[0], (x.shape[1] if x.dim() == 3 else 1), x.shape[-1]
+    _check("positions", positions, "i64", T)
+    _check("cos_sin_cache", cos_sin_cache, "f32")
+    _check("device_error", device_error, "i32")
+    _on_cuda(x=x, positions=positions, cos_sin_cache=cos_sin_cache, out=out, device_error=device_error)
+    offset = D - dim if offset is None else offset
+    x_strides, out_strides = _row_strides("x", x), _row_strides("out", out)
+    _launch("dsv4_rope_rows", x.device, stream, lambda handle: lib().dsv4_rope_rows(
+        types[x.dtype], x.data_ptr(), *x_strides, out.data_ptr(), *out_strides, T, H, D, _int32(offset), dim,
+        layout, 1 if inverse else 0, _ptr(positions), _ptr(cos_sin_cache), max_position, _ptr(device_error),
+        handle))

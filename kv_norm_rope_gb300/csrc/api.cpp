@@ -475,7 +475,9 @@ int dsv4_debug_bounds_flags(int reset)
                                    dsv4::bounds_flag_indexer, dsv4::bounds_flag_mxfp8,
                                    dsv4::bounds_flag_fp4_gather, dsv4::bounds_flag_fp4_attention,
                                    dsv4::bounds_flag_fp4_weights,
-                                   dsv4::bounds_flag_fp4_evict};
+                                   dsv4::bounds_flag_fp4_evict, dsv4::bounds_flag_latent_attention,
+                                   dsv4::bounds_flag_tree_keep, dsv4::bounds_flag_rope_table,
+                                   dsv4::bounds_flag_rope_rows};
     int flags = 0;
     for (auto read : readers) {
         const int v = read(reset);

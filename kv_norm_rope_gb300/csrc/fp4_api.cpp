@@ -15,8 +15,17 @@
 namespace {
 
 using dsv4::aligned;
-using dsv4::Fp4Batch;
+using dsv4::check_sizes;
+using dsv4::PagedBatch;
 using dsv4::too_many_slots;
+
+// tiles of 128 keys
+int check_attention(int32_t q_len, int32_t num_heads, int32_t batch, float scale, int32_t window,
+                    int64_t most_keys)
+{
+    return dsv4::check_attention(q_len, num_heads, batch, scale, window, most_keys, 128,
+                                 dsv4::kFp4StartCost);
+}
 
 // SM count times CTAs per SM of the reader, per device (bit-identical values
 // from any thread, so a race only repeats the queries)
@@ -38,44 +47,6 @@ int resident_readers(int64_t *resident)
     *resident = int64_t(sms) * per;
     if (cached)
         g_resident[dev].store(*resident, std::memory_order_relaxed);
-    return DSV4_OK;
-}
-
-// keys of a request that a table can name: key indices, less a window and a
-// number of tokens, then stay in 32 bits
-constexpr int64_t kMaxKeys = int64_t(1) << 30;
-
-// sizes of what every operator over requests takes; pointers come after the
-// early return for an empty batch
-int check_sizes(int64_t num_blocks, int32_t block_size, int64_t table_stride, int32_t table_width,
-                int32_t batch)
-{
-    if (num_blocks < 1 || block_size < 1 || table_width < 1 || batch < 0 ||
-        table_stride < table_width)
-        return DSV4_ERR_SHAPE;
-    if (too_many_slots(num_blocks, block_size) || num_blocks > INT32_MAX ||
-        int64_t(table_width) * block_size > kMaxKeys || table_stride > INT64_MAX / 4096 / 65536 ||
-        batch > 65535)
-        return DSV4_ERR_SHAPE;
-    return DSV4_OK;
-}
-
-int check_attention(int32_t q_len, int32_t num_heads, int32_t batch, float scale, int32_t window,
-                    int64_t most_keys)
-{
-    if (q_len < 1 || q_len > (1 << 24) || num_heads < 1 || window < 0)
-        return DSV4_ERR_SHAPE;
-    if (int64_t(q_len) * num_heads > INT32_MAX ||
-        int64_t(q_len) * num_heads * batch > INT64_MAX / 4096 ||
-        (batch > 0 && int64_t(q_len) * num_heads > INT32_MAX / batch))
-        return DSV4_ERR_SHAPE;
-    // The line of tiles of 64 rows and 128 keys with what is added to it is counted in 32
-    // bits, up to a multiple of the CTAs (fewer than 1024).
-    if (((int64_t(q_len) * num_heads + 63) / 64) * batch >
-        (INT32_MAX - 1024) / ((most_keys + 127) / 128 + dsv4::kFp4StartCost))
-        return DSV4_ERR_SHAPE;
-    if (!(scale > 0.0f && scale <= 4294967296.0f))  // it is multiplied by 2^82 in fp32
-        return DSV4_ERR_VALUE;
     return DSV4_OK;
 }
 
@@ -141,8 +112,8 @@ int dsv4_fp4_attention(const void *q, const uint8_t *kv_cache, int64_t num_block
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(sinks, 4) ||
         !aligned(lse, 4) || !aligned(device_error, 4))
         return DSV4_ERR_ALIGN;
-    dsv4::Fp4AttentionArgs a = {};
-    a.b = Fp4Batch{kv_cache, num_blocks, block_size, block_table, table_stride,
+    dsv4::AttentionArgs a = {};
+    a.b = PagedBatch{kv_cache, num_blocks, block_size, block_table, table_stride,
                    table_width, seq_lens, batch, device_error};
     a.q = static_cast<const uint16_t *>(q);
     a.q_len = q_len;
@@ -180,8 +151,8 @@ int dsv4_fp4_attention_weights(const void *q, const uint8_t *kv_cache, int64_t n
         !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(weights, 4) ||
         !aligned(device_error, 4))
         return DSV4_ERR_ALIGN;
-    dsv4::Fp4AttentionArgs a = {};
-    a.b = Fp4Batch{kv_cache, num_blocks, block_size, block_table, table_stride,
+    dsv4::AttentionArgs a = {};
+    a.b = PagedBatch{kv_cache, num_blocks, block_size, block_table, table_stride,
                    table_width, seq_lens, batch, device_error};
     a.q = static_cast<const uint16_t *>(q);
     a.q_len = q_len;
@@ -223,7 +194,7 @@ int dsv4_fp4_evict(uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
         !aligned(new_seq_lens, 4) || !aligned(new_weights, 4) || !aligned(device_error, 4))
         return DSV4_ERR_ALIGN;
     dsv4::Fp4EvictArgs a = {};
-    a.b = Fp4Batch{kv_cache, num_blocks, block_size, block_table, table_stride,
+    a.b = PagedBatch{kv_cache, num_blocks, block_size, block_table, table_stride,
                    table_width, seq_lens, batch, device_error};
     a.weights = weights;
     a.weights_stride = weights_stride;

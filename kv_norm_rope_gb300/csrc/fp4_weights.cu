@@ -306,7 +306,7 @@ __device__ __forceinline__ void multiply_role(const WParams &w, Shared &s, uint3
 __device__ __forceinline__ void sum_role(const WParams &w, Shared &s, Sweep sw)
 {
     const AParams &p = w.p;
-    const Fp4AttentionArgs &a = p.a;
+    const AttentionArgs &a = p.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
     const int key = warp * 32 + lane, col0 = group * kCols, tid = threadIdx.x;
     const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_weights_kernel(const __grid_c
     const int warp = threadIdx.x >> 5;
     Sweep sw;
     wait_for_kernel_before();
-    deal(w.p, blockIdx.x, gridDim.x, s.scratch, sw.c);
+    Tiles::deal(w.p, blockIdx.x, gridDim.x, s.scratch, sw.c);
     if (sw.c.left == 0)
         return;
     if ((smem_addr(smem) & 1023u) != 0u) {  // never: there is no static shared memory
@@ -465,7 +465,7 @@ int configure(int *sms)
 
 }  // namespace
 
-int launch_fp4_weights(const Fp4AttentionArgs &a, cudaStream_t stream)
+int launch_fp4_weights(const AttentionArgs &a, cudaStream_t stream)
 {
     int sms = 0;
     if (configure(&sms) != DSV4_OK)

@@ -47,9 +47,9 @@ int launch_indexer_gather(const uint8_t *cache, int64_t num_blocks, int32_t bloc
 // cycles (clamped to the kernels' own limit), then flags DSV4_DEVERR_TIMEOUT.
 int launch_wait_check(int64_t max_cycles, int32_t *err, cudaStream_t stream);
 
-// The 4-bit cache (fp4.cuh: its rows).  What the operators over it have in common:
-// B requests, their pages by a block table, and Q new tokens each.
-struct Fp4Batch {
+// What the operators over the paged caches have in common: B requests, their pages by a
+// block table, and Q new tokens each.
+struct PagedBatch {
     const uint8_t *cache;
     int64_t num_blocks;
     int32_t block_size;
@@ -65,13 +65,14 @@ struct Fp4Batch {
 // beside one for each of its tiles of keys (fp4_tiles.cuh).
 constexpr int kFp4StartCost = 2;
 
-struct Fp4AttentionArgs {
-    Fp4Batch b;
+struct AttentionArgs {
+    PagedBatch b;
     const uint16_t *q;      // [batch, q_len, heads, 512]
     int32_t q_len;
     int32_t heads;
     float scale;
     int32_t window;         // 0: none
+    const uint64_t *tree;   // [batch, q_len] or null: the drafted keys that each drafted token sees
     const float *sinks;     // [heads] or null
     uint16_t *out;
     float *lse;             // [batch, q_len, heads]: written by the attention, read by the weights
@@ -83,7 +84,7 @@ struct Fp4AttentionArgs {
 constexpr int kFp4MoveRows = 64;  // kept rows that a CTA of the eviction moves
 
 struct Fp4EvictArgs {
-    Fp4Batch b;             // b.cache is written too
+    PagedBatch b;             // b.cache is written too
     const float *weights;
     int64_t weights_stride;
     int32_t weights_width;
@@ -97,6 +98,64 @@ struct Fp4EvictArgs {
     float *new_weights;     // [batch, budget]
 };
 
+// Keys in a tile of the attention over the FP8 and bf16 caches, and the positions that
+// beginning a row tile takes on its line.
+constexpr int kLatentTileKeys = 64;
+constexpr int kLatentStartCost = 4;
+
+// latent_attention.cu; the workspace holds latent_attention_workspace() bytes
+size_t latent_attention_workspace();
+int launch_latent_attention(int store_mode, const AttentionArgs &a, void *workspace, cudaStream_t stream);
+
+// Drafted tokens of a request: a token's ancestors are bits of one word.
+constexpr int kMaxDrafted = 64;
+
+struct TreeKeepArgs {
+    PagedBatch b;              // b.cache is written too
+    int32_t q_len;
+    const int32_t *path;       // [batch, q_len]
+    const int32_t *path_lens;  // [batch]
+    int32_t *new_lens;         // [batch]
+};
+
+// tree_keep.cu
+int launch_tree_keep(int store_mode, const TreeKeepArgs &a, cudaStream_t stream);
+
+constexpr int kMaxRopeDim = 256;
+
+struct RopeTableArgs {
+    const double *frequencies;  // host, [rope_dim / 2]
+    int32_t rope_dim;
+    double magnitude;
+    const int64_t *positions;   // [count] or null: first, first + 1, ...
+    int64_t first, count;
+    float *out;                 // [count, rope_dim]
+    int32_t sms;
+    int32_t *err;
+};
+
+// rope_table.cu
+int launch_rope_table(const RopeTableArgs &a, cudaStream_t stream);
+
+struct RopeRowsArgs {
+    const uint8_t *x;
+    uint8_t *out;               // x itself, with the same strides, or apart from it
+    int32_t type;
+    int64_t tokens;
+    int32_t heads, width;
+    int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;  // elements
+    int32_t offset, rope_dim, layout;
+    bool inverse;
+    const int64_t *positions;   // [tokens]
+    const float *cos_sin;       // [max_position, rope_dim]
+    int64_t max_position;
+    int32_t sms;
+    int32_t *err;
+};
+
+// rope_rows.cu
+int launch_rope_rows(const RopeRowsArgs &a, cudaStream_t stream);
+
 // fp4_gather.cu; the grid is capped at max_ctas
 int fp4_gather_ctas_per_sm(int *ctas_per_sm);
 int launch_fp4_gather(const uint8_t *cache, int64_t num_blocks, int32_t block_size,
@@ -104,9 +163,9 @@ int launch_fp4_gather(const uint8_t *cache, int64_t num_blocks, int32_t block_si
                       int64_t max_ctas, cudaStream_t stream);
 // fp4_attention.cu; the workspace holds fp4_attention_workspace() bytes
 size_t fp4_attention_workspace();
-int launch_fp4_attention(const Fp4AttentionArgs &a, void *workspace, cudaStream_t stream);
+int launch_fp4_attention(const AttentionArgs &a, void *workspace, cudaStream_t stream);
 // fp4_weights.cu
-int launch_fp4_weights(const Fp4AttentionArgs &a, cudaStream_t stream);
+int launch_fp4_weights(const AttentionArgs &a, cudaStream_t stream);
 // fp4_evict.cu
 int launch_fp4_evict(const Fp4EvictArgs &a, cudaStream_t stream);
 
@@ -122,5 +181,9 @@ int bounds_flag_fp4_gather(int reset);
 int bounds_flag_fp4_attention(int reset);
 int bounds_flag_fp4_weights(int reset);
 int bounds_flag_fp4_evict(int reset);
+int bounds_flag_latent_attention(int reset);
+int bounds_flag_tree_keep(int reset);
+int bounds_flag_rope_table(int reset);
+int bounds_flag_rope_rows(int reset);
 
 }  // namespace dsv4

@@ -65,12 +65,18 @@ __device__ __forceinline__ Operand operator+(Operand o, uint32_t bytes)
     return Operand{o.low + (bytes >> 4), o.high};
 }
 
-// Instruction descriptor: bf16 operands, fp32 accumulator, M = 128, N = n;
-// `across` marks MN-major operands (both).
+// Instruction descriptor: bf16 operands, fp32 accumulator, M = m (64 or 128), N = n;
+// a_across, b_across mark MN-major operands.
+__device__ __forceinline__ uint32_t instruction_of(uint32_t m, uint32_t n, bool a_across, bool b_across)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_across ? 1u << 15 : 0u) | (b_across ? 1u << 16 : 0u) |
+           ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// M = 128, both operands alike
 __device__ __forceinline__ uint32_t instruction(uint32_t n, bool across)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (across ? 3u << 15 : 0u) | ((n >> 3) << 17) |
-           ((128u >> 4) << 24);
+    return instruction_of(128u, n, across, across);
 }
 
 // The matrix instructions take their operands from uniform registers, so a whole
@@ -127,6 +133,21 @@ __device__ __forceinline__ void tmem_load16(uint32_t address, float *v)
     uint32_t *u = reinterpret_cast<uint32_t *>(v);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15])
+        : "r"(address));
+}
+
+// 32 columns from `address` on of 16 lanes (the first of the warp's quarter, where the rows of a
+// product with M = 64 are): v[4j], v[4j + 1] are row lane / 4, columns 8j + 2 (lane % 4) and the
+// next, v[4j + 2], v[4j + 3] the same of row lane / 4 + 8; finished after tmem_wait_load
+__device__ __forceinline__ void tmem_load16_rows16(uint32_t address, float *v)
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
           "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
