@@ -32,7 +32,7 @@ _HEADERS = [os.path.join(_INCLUDE, "dsv4kv.h")] + [
     os.path.join(_CSRC, h)
     for h in ("launch.h", "ops.h", "fastdiv.h", "convert.cuh", "launch_status.h", "rowmath.cuh",
               "halfrow.cuh", "bulkcopy.cuh", "bounds.cuh", "bounds_range.h", "fp4.cuh",
-              "fp4_tiles.cuh", "fp8_rows.cuh", "key_tiles.cuh", "run_join.cuh", "tcgen05.cuh", "hostcheck.h")]
+              "fp4_tiles.cuh", "fp8_rows.cuh", "key_tiles.cuh", "run_join.cuh", "tcgen05.cuh", "tensor_copy.cuh", "hostcheck.h")]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # status codes and constants (mirrors include/dsv4kv.h)

@@ -609,8 +609,9 @@ int launch_fp4_attention(const AttentionArgs &a, void *workspace, cudaStream_t s
     int sms = 0;
     if (configure_runs(fp4_attention_kernel, kSmemBytes, sm_count, &sms) != DSV4_OK)
         return DSV4_ERR_CUDA;
-    return launch_runs<Tiles>(fp4_attention_kernel, kThreads, kSmemBytes, sms, a, kOperandUnit, workspace,
-                              stream);
+    const WParams w = plan_runs<Tiles>(a, kOperandUnit, sms, workspace);
+    const int st = launch_after(fp4_attention_kernel, dim3(unsigned(w.runs)), dim3(kThreads), stream, w, kSmemBytes);
+    return st != DSV4_OK ? st : launch_join<Tiles>(w, stream);
 }
 
 }  // namespace dsv4

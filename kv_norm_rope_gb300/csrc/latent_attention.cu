@@ -40,14 +40,17 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "bounds.cuh"
+#include "convert.cuh"
 #include "fp8_rows.cuh"
 #include "key_tiles.cuh"
 #include "launch_status.h"
 #include "ops.h"
 #include "run_join.cuh"
 #include "tcgen05.cuh"
+#include "tensor_copy.cuh"
 
 namespace dsv4 {
 namespace {
@@ -56,31 +59,58 @@ constexpr int kTileKeys = kLatentTileKeys;
 using Tiles = KeyTiles<kTileKeys, kLatentStartCost, true>;
 using Cursor = Tiles::Cursor;
 
-constexpr int kChunks = 8;  // a row in chunks of 64 dims
-constexpr uint32_t kChunkBytes = kTileKeys * 128;
-constexpr int kSoftmaxWarps = 8, kLoadWarp = kSoftmaxWarps, kLoadWarps = 16;
-constexpr int kMultiplyWarp = kLoadWarp + kLoadWarps;
-constexpr int kThreads = (kMultiplyWarp + 4) * 32;  // whole warpgroups: the last two warps idle
-constexpr int kWarpKeys = kTileKeys / kLoadWarps;   // 4
-// registers a thread: 72 at launch (896 * 72 = 64512), then
-constexpr int kSoftmaxRegs = 88, kLoadRegs = 72, kMultiplyRegs = 40;
-static_assert(128 * (2 * kSoftmaxRegs + 4 * kLoadRegs + kMultiplyRegs) <= kThreads * 72,
-              "the shares exceed what the CTA was launched with");
-static_assert(kRows == 64 && kTileKeys == 64 && kWarpKeys == 4, "the lanes are dealt for these");
+// A tile lies in groups of 8 keys, a group in 8 chunks of 64 dims, each an atom of the swizzle
+// (tcgen05.cuh): a copy can bring whole groups, and both products read them as they are.
+constexpr int kChunks = 8;
+constexpr uint32_t kGroupBytes = kChunks * 1024;
+constexpr uint32_t kTileBytes = kTileKeys / 8 * kGroupBytes;
+constexpr uint32_t kQueryBytes = kChunks * kRows * 128;
+constexpr uint32_t kProbBytes = kRows * 128;  // 64 rows of 64 keys
+constexpr int kSoftmaxWarps = 8, kRowWarp = kSoftmaxWarps;  // warps from kRowWarp on see to the rows
 constexpr float kSlack = 16.0f;
+static_assert(kRows == 64 && kTileKeys == 64, "the lanes are dealt for these");
+
+// What differs with the store.
+template <bool kFp8>
+struct Kind;
+template <>
+struct Kind<true> {
+    static constexpr int row_warps = 16;
+    static constexpr int prob_slots = 1;  // the second one's place is the ring's
+    static constexpr uint32_t ring_bytes = row_warps * 1536;
+    // registers a thread: 72 at launch (896 * 72 = 64512), then
+    static constexpr int softmax_regs = 88, row_regs = 72, other_regs = 40;
+};
+template <>
+struct Kind<false> {
+    static constexpr int row_warps = 8;
+    static constexpr int prob_slots = 2;
+    static constexpr uint32_t ring_bytes = 0;
+};
+constexpr int kCopyWarps = 4;  // bf16
+template <bool kFp8>
+constexpr int kMultiplyWarp = kRowWarp + Kind<kFp8>::row_warps;  // then the run's ends, the queries, none
+template <bool kFp8>
+constexpr int kThreads = (kMultiplyWarp<kFp8> + 4 + (kFp8 ? 0 : kCopyWarps)) * 32;
+static_assert(128 * (2 * Kind<true>::softmax_regs + 4 * Kind<true>::row_regs + Kind<true>::other_regs) <=
+                  kThreads<true> * 72,
+              "the shares exceed what the CTA was launched with");
 
 // Shared memory (from a 1024-byte boundary).
-constexpr uint32_t kTileBytes = kChunks * kChunkBytes;
-constexpr uint32_t kKeys = 0;                              // two tiles
-constexpr uint32_t kQuery = kKeys + 2 * kTileBytes;        // 8 chunks of 64 rows
-constexpr uint32_t kProbs = kQuery + kChunks * kRows * 128;  // two P: 64 rows of 64 keys
-constexpr uint32_t kShared = kProbs + 2 * kRows * 128;
+constexpr uint32_t kKeys = 0;                        // two tiles
+constexpr uint32_t kQuery = kKeys + 2 * kTileBytes;  // 8 chunks of 64 rows
+constexpr uint32_t kProbs = kQuery + kQueryBytes;    // P
+template <bool kFp8>
+constexpr uint32_t kRing = kProbs + Kind<kFp8>::prob_slots * kProbBytes;
+template <bool kFp8>
+constexpr uint32_t kShared = kRing<kFp8> + Kind<kFp8>::ring_bytes;
 
 // Tensor memory: O^T in 4 blocks of 128 dims by 64 rows, then two S of 64 keys.
 constexpr uint32_t kScoresAt = 4 * kRows;
 
 struct Shared {
-    uint64_t full[2], free[2], scores[2], probs[2];  // of the two tiles in flight
+    uint64_t landed[2];                              // bf16: of the copies of the two tiles in flight
+    uint64_t full[2], free[2], scores[2], probs[2];  // of the two tiles
     uint64_t query, query_free, output;
     uint32_t tmem;
     int scratch[kDealWords];
@@ -88,10 +118,20 @@ struct Shared {
     alignas(16) float factor[kRows];
     float half_rows[2][kRows];  // maxima or sums over the keys of either half
     alignas(4) uint8_t state[2][kTileKeys];
+    alignas(16) uint32_t dirty[2][kCopyWarps];  // bf16: the tile has to be looked through before the products
+    Cursor place[kSoftmaxWarps];
 };
-constexpr size_t kSmemBytes = kShared + sizeof(Shared);
+template <bool kFp8>
+constexpr size_t kSmemBytes = kShared<kFp8> + sizeof(Shared);
 enum : uint8_t { kMissing = 0, kTaken = 1, kNotFinite = 2 };  // of a key
-static_assert(kSmemBytes <= 227 * 1024, "too much shared memory");
+static_assert(kSmemBytes<true> <= 227 * 1024 && kSmemBytes<false> <= 227 * 1024, "too much shared memory");
+
+struct LParams {
+    WParams w;
+    CUtensorMap q;     // boxes of 64 rows
+    CUtensorMap rows;  // bf16: the cache, in boxes of `box` rows, or by single rows
+    int box;           // 64, 32, 16, 8, or 1: single rows, gathered by fours
+};
 
 __device__ __forceinline__ void store_shared16(uint32_t at, uint4 v)
 {
@@ -105,26 +145,95 @@ __device__ __forceinline__ void store_shared4(uint32_t at, uint32_t v)
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-// ---- Warps 8..23: cache rows and queries into operands
-
-template <bool kFp8>
-__device__ __forceinline__ Span cache_span(const PagedBatch &b)
+__device__ __forceinline__ uint4 load_shared16(uint32_t at)
 {
-    return Span{b.cache, uint64_t(b.num_blocks) * uint32_t(b.block_size) *
-                             (kFp8 ? DSV4_FP8_SLOT_BYTES : DSV4_BF16_SLOT_BYTES)};
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
 }
 
-// Where key `kWarpKeys * warp + lane % kWarpKeys` of a tile is: its block (on its way when this
-// returns) and the offset in it, UINT32_MAX for a key that no row of the unit may see.
+// where 16 bytes of a key are in a tile: piece 0..7 of a chunk
+__device__ __forceinline__ uint32_t piece_of(int key, int chunk, int piece)
+{
+    return (key >> 3) * kGroupBytes + chunk * 1024 + swizzled(key & 7, piece);
+}
+
+// a wait by the whole warp
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(kFull, mbar_wait(bar, parity));
+}
+
+// ---- Queries, by the copying warp
+
+// (Copies are issued by one elected lane of code that the whole warp runs with the same values:
+// from lanes of their own each took about 80 cycles.)
+__device__ __forceinline__ void copy_query(const LParams &l, Shared &s, uint32_t smem, int request, int row0,
+                                           uint32_t elected)
+{
+    if (elected != 0u)
+        mbar_arrive_expect_tx(&s.query, kQueryBytes);
+    __syncwarp();
+    // rows past the unit's last are another request's, or zeros past the batch's: their scores
+    // go nowhere
+    copy_rows3(smem + kQuery, &l.q, request * l.w.p.all_rows + row0, &s.query, elected);
+}
+
+__device__ __forceinline__ void query_role(const LParams &l, Shared &s, uint32_t smem, Cursor c)
+{
+    const uint32_t elected = elect_one();
+    int segment = 0;
+    bool alive = c.left > 0;
+    while (alive && c.left > 0) {
+        alive = segment == 0 || warp_wait(&s.query_free, (segment - 1) & 1);
+        if (!alive)
+            break;
+        copy_query(l, s, smem, c.request, c.row0, elected);
+        ++segment;
+        // to the next unit
+        const int rest = c.range.stop() - c.tile;
+        if (c.left <= rest)
+            break;
+        c.left -= rest - 1;
+        c.tile = c.range.stop() - 1;
+        c.advance(l.w.p);
+    }
+    // nothing of this CTA's is on its way when it ends
+    if (segment > 0 && !warp_wait(&s.query, (segment - 1) & 1))
+        alive = false;
+    if (!alive && segment > 0)
+        flag(l.w.p.a.b.err, DSV4_DEVERR_TIMEOUT);
+}
+
+// ---- FP8 rows into operands: warps 8..23, a warp 4 keys of each tile
+//
+// Of a row lanes 0..27 have 16 codes and lanes 28..31 eight rope dims; the other 32 rope dims of
+// the four rows are with lanes 0..15.  The first three rows come through the warp's part of a ring in
+// shared memory (asynchronous copies into each lane's own bytes), the fourth, the rest of the
+// rope dims and the exponents in registers: what is on its way to registers takes lines of the
+// L1 that shared memory leaves, about 28 KB, and a load that finds none waits.
+
+constexpr int kWarpKeys = 4, kRingRows = 3;
+
+__device__ __forceinline__ Span fp8_span(const PagedBatch &b)
+{
+    return Span{b.cache, uint64_t(b.num_blocks) * uint32_t(b.block_size) * DSV4_FP8_SLOT_BYTES};
+}
+
+// Where a key is: its block (on its way when this returns) and the offset in it, UINT32_MAX
+// for a key outside [lo, hi).
 struct KeyPlace {
     uint32_t block, off;
 };
 
-__device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c, int key)
+__device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c, int key, int lo, int hi)
 {
     KeyPlace k{0u, UINT32_MAX};
     const int i = c.tile * kTileKeys + key;
-    if (c.left > 0 && i >= c.range.lo && i < c.range.hi) {
+    if (c.left > 0 && i >= lo && i < hi) {
         const uint32_t at = fastdiv(uint32_t(i), p.block_div);
         k.off = uint32_t(i) - at * uint32_t(p.a.b.block_size);
         k.block = ldg4_now_in(p.a.b.table + c.request * p.a.b.table_stride + at, table_span(p.a.b),
@@ -142,277 +251,432 @@ __device__ __forceinline__ void check_place(const AParams &p, KeyPlace &k)
     }
 }
 
-// What a lane holds of its warp's keys of a tile.
-//  FP8: of each row lanes 0..27 have 16 codes (and their block's exponent) and lanes 28..31
-//  eight rope dims; the other 32 rope dims of all four rows are with lanes 0..15.
-//  bf16: 16 bytes of either half of each row.
-template <bool kFp8>
-struct Raw;
-template <>
-struct Raw<true> {
-    uint4 a[kWarpKeys], tail;
-    uint32_t e[kWarpKeys];
-};
-template <>
-struct Raw<false> {
-    uint4 a[kWarpKeys], b[kWarpKeys];
+// The place as addresses, found once by the lanes that have the key: null for none.  A row's
+// exponents stand `scale` bytes after its data.
+struct Fp8Row {
+    const uint8_t *data;
+    uint32_t scale;
 };
 
-// 16 bytes of an FP8 row, which is 16-byte aligned in caches with an even block size (wide)
+__device__ __forceinline__ Fp8Row fp8_row(const AParams &p, const KeyPlace &k)
+{
+    if (k.off == UINT32_MAX)
+        return Fp8Row{nullptr, 0u};
+    const uint32_t bs = uint32_t(p.a.b.block_size);
+    return Fp8Row{p.a.b.cache + uint64_t(k.block) * bs * DSV4_FP8_SLOT_BYTES + uint64_t(k.off) * DSV4_FP8_DATA_BYTES,
+                  (bs - k.off) * DSV4_FP8_DATA_BYTES + k.off * DSV4_FP8_SCALE_BYTES};
+}
+
+__device__ __forceinline__ Fp8Row row_of_lane(const Fp8Row &mine, int lane)
+{
+    const uint64_t at = reinterpret_cast<uint64_t>(mine.data);
+    const uint32_t low = __shfl_sync(kFull, uint32_t(at), lane), high = __shfl_sync(kFull, uint32_t(at >> 32), lane);
+    return Fp8Row{reinterpret_cast<const uint8_t *>(uint64_t(high) << 32 | low), __shfl_sync(kFull, mine.scale, lane)};
+}
+
+// Rows are 16-byte aligned in caches with an even block size (wide), else 8-byte.
 __device__ __forceinline__ uint4 load_fp8_16(const AParams &p, const uint8_t *at, bool wide)
 {
-    const Span cs = cache_span<true>(p.a.b);
+    const Span cs = fp8_span(p.a.b);
     if (wide)
         return ldg16_now_in(at, cs, p.a.b.err);
     const uint2 lo = ldg8_now_in(at, cs, p.a.b.err), hi = ldg8_now_in(at + 8, cs, p.a.b.err);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-// the warp's row i on its way (zeros for a key that is not there)
-__device__ __forceinline__ void load_row(const AParams &p, const KeyPlace &k, int i, bool wide, Raw<true> &raw)
+// 16 bytes to shared memory, zeros for none
+__device__ __forceinline__ void copy_fp8_16(const AParams &p, uint32_t to, const uint8_t *from, bool ok, bool wide)
 {
-    const int lane = threadIdx.x & 31;
-    const uint32_t block = __shfl_sync(kFull, k.block, i), off = __shfl_sync(kFull, k.off, i);
-    raw.a[i] = make_uint4(0u, 0u, 0u, 0u);
-    raw.e[i] = 0u;
-    if (off == UINT32_MAX)
-        return;
-    const uint32_t bs = uint32_t(p.a.b.block_size);
-    const uint8_t *page = p.a.b.cache + uint64_t(block) * bs * DSV4_FP8_SLOT_BYTES;
-    raw.a[i] = load_fp8_16(p, page + uint64_t(off) * DSV4_FP8_DATA_BYTES + 16 * lane, wide);
-    if (lane < 28)
-        raw.e[i] = ldg_byte_now_in(page + uint64_t(bs) * DSV4_FP8_DATA_BYTES + uint64_t(off) * DSV4_FP8_SCALE_BYTES + (lane >> 2),
-                                   cache_span<true>(p.a.b), p.a.b.err);
-}
-
-__device__ __forceinline__ void load_tail(const AParams &p, const KeyPlace &k, bool wide, Raw<true> &raw)
-{
-    const int lane = threadIdx.x & 31;
-    const uint32_t block = __shfl_sync(kFull, k.block, (lane >> 2) & 3), off = __shfl_sync(kFull, k.off, (lane >> 2) & 3);
-    raw.tail = make_uint4(0u, 0u, 0u, 0u);
-    if (lane < 16 && off != UINT32_MAX) {
-        const uint32_t bs = uint32_t(p.a.b.block_size);
-        const uint8_t *page = p.a.b.cache + uint64_t(block) * bs * DSV4_FP8_SLOT_BYTES;
-        raw.tail = load_fp8_16(p, page + uint64_t(off) * DSV4_FP8_DATA_BYTES + DSV4_NOPE_DIM + 64 + 16 * (lane & 3), wide);
+    ok = ok && in_span(from, 16, fp8_span(p.a.b), p.a.b.err);
+    const uint8_t *at = ok ? from : p.a.b.cache;
+    if (wide) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(at), "r"(ok ? 16 : 0) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(at), "r"(ok ? 8 : 0) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 8), "l"(at + 8), "r"(ok ? 8 : 0)
+                     : "memory");
     }
 }
 
-__device__ __forceinline__ void load_row(const AParams &p, const KeyPlace &k, int i, bool, Raw<false> &raw)
+// what a lane holds of its warp's keys of a tile, beside the ring
+struct Raw {
+    uint4 last, tail;
+    uint32_t e[kWarpKeys];
+};
+
+// the warp's rows on their way (zeros for keys that are not there); ring: the lane's first bytes
+__device__ __forceinline__ void load_rows(const AParams &p, const Fp8Row &mine, uint32_t ring, bool wide, Raw &raw)
 {
     const int lane = threadIdx.x & 31;
-    const uint32_t block = __shfl_sync(kFull, k.block, i), off = __shfl_sync(kFull, k.off, i);
-    raw.a[i] = raw.b[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (off == UINT32_MAX)
-        return;
-    const uint8_t *row = p.a.b.cache + (uint64_t(block) * uint32_t(p.a.b.block_size) + off) * DSV4_BF16_SLOT_BYTES + 16 * lane;
-    raw.a[i] = ldg16_now_in(row, cache_span<false>(p.a.b), p.a.b.err);
-    raw.b[i] = ldg16_now_in(row + 512, cache_span<false>(p.a.b), p.a.b.err);
+#pragma unroll
+    for (int i = 0; i < kWarpKeys; ++i) {
+        const Fp8Row row = row_of_lane(mine, i);
+        const bool ok = row.data != nullptr;
+        if (i < kRingRows)
+            copy_fp8_16(p, ring + 512 * i, row.data + 16 * lane, ok, wide);
+        else
+            raw.last = ok ? load_fp8_16(p, row.data + 16 * lane, wide) : make_uint4(0u, 0u, 0u, 0u);
+        raw.e[i] = ok && lane < 28
+                       ? ldg_byte_now_in(row.data + row.scale + (lane >> 2), fp8_span(p.a.b), p.a.b.err)
+                       : 0u;
+    }
+    const Fp8Row row = row_of_lane(mine, (lane >> 2) & 3);
+    raw.tail = lane < 16 && row.data != nullptr
+                   ? load_fp8_16(p, row.data + DSV4_NOPE_DIM + 64 + 16 * (lane & 3), wide)
+                   : make_uint4(0u, 0u, 0u, 0u);
 }
 
-__device__ __forceinline__ void load_tail(const AParams &, const KeyPlace &, bool, Raw<false> &) {}
+// the same on their way to L2: 8 lanes a row, five of them for its data and one for its exponents
+__device__ __forceinline__ void prefetch_rows(const AParams &p, const Fp8Row &mine)
+{
+    const int lane = threadIdx.x & 31, part = lane & 7;
+    const Fp8Row row = row_of_lane(mine, lane >> 3);
+    const uint8_t *at = row.data + (part < 5 ? 128u * part : row.scale);
+    if (row.data != nullptr && part < 6 && in_span(at, 1, fp8_span(p.a.b), p.a.b.err))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
 
-// Row i of the warp's four into the operand at `tile` (key: its place there); true where it is not
-// finite: it is then zeros.  kTail: the marks of the rows' other rope dims, by lane.
-__device__ __forceinline__ bool store_row(const Raw<true> &raw, int i, uint32_t tile, int key, uint32_t tail_marks)
+// Row i of the warp's four, whose bytes are `bits`, into the operand at `tile` (key: its place there);
+// true where it is not finite: it is then zeros.  tail_marks: of the rows' other rope dims, by lane.
+__device__ __forceinline__ bool store_row(uint4 bits, uint32_t e, int i, uint32_t tile, int key, uint32_t tail_marks)
 {
     const int lane = threadIdx.x & 31, chunk = lane >> 2, quarter = lane & 3;
     uint4 first, second;
     uint32_t bad;
     if (lane < 28) {
-        const uint32_t e = raw.e[i];
-        bad = e4m3x16_nan(raw.a[i]) | (e > kFp8OperandTop ? 1u : 0u);
+        bad = e4m3x16_nan(bits) | (e > kFp8OperandTop ? 1u : 0u);
         const uint32_t scale2 = fp8_operand_scale(e);
-        const uint4 lo = e4m3x8_scaled(raw.a[i].x, raw.a[i].y, scale2);
-        const uint4 hi = e4m3x8_scaled(raw.a[i].z, raw.a[i].w, scale2);
+        const uint4 lo = e4m3x8_scaled(bits.x, bits.y, scale2);
+        const uint4 hi = e4m3x8_scaled(bits.z, bits.w, scale2);
         // odd chunks store their pieces the other way round: no two of 8 lanes meet in a bank
         first = (chunk & 1) ? hi : lo;
         second = (chunk & 1) ? lo : hi;
     } else {
-        bad = bf16x8_not_finite(raw.a[i]);
-        first = second = fp8_rope_operand(raw.a[i]);
+        bad = bf16x8_not_finite(bits);
+        first = second = fp8_rope_operand(bits);
     }
     const bool not_finite = __any_sync(kFull, bad != 0u) || ((tail_marks >> (4 * i)) & 15u) != 0u;
     if (not_finite)
         first = second = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t row = tile + chunk * kChunkBytes;
-    const int piece = lane < 28 ? 2 * quarter + (chunk & 1) : quarter;
-    store_shared16(row + swizzled(key, piece), first);
+    const uint32_t at = tile + piece_of(key, chunk, lane < 28 ? 2 * quarter + (chunk & 1) : quarter);
+    store_shared16(at, first);
     if (lane < 28)
-        store_shared16(row + swizzled(key, piece ^ 1), second);
+        store_shared16(at ^ 16u, second);
     return not_finite;
 }
 
-__device__ __forceinline__ uint32_t tail_marks(const Raw<true> &raw)
+__device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
-    return __ballot_sync(kFull, bf16x8_not_finite(raw.tail) != 0u);
-}
-
-// the rope dims 32..63 of the warp's rows; `bad`: which of them are zeros instead
-__device__ __forceinline__ void store_tail(const Raw<true> &raw, uint32_t tile, int key0, uint32_t bad)
-{
-    const int lane = threadIdx.x & 31;
-    if (lane < 16)
-        store_shared16(tile + 7 * kChunkBytes + swizzled(key0 + (lane >> 2), 4 + (lane & 3)),
-                       ((bad >> (lane >> 2)) & 1u) ? make_uint4(0u, 0u, 0u, 0u) : fp8_rope_operand(raw.tail));
-}
-
-__device__ __forceinline__ bool store_row(const Raw<false> &raw, int i, uint32_t tile, int key, uint32_t)
-{
-    const int lane = threadIdx.x & 31;
-    const bool not_finite =
-        __any_sync(kFull, (bf16x8_not_finite(raw.a[i]) | bf16x8_not_finite(raw.b[i])) != 0u);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t at = tile + (lane >> 3) * kChunkBytes + swizzled(key, lane & 7);
-    store_shared16(at, not_finite ? zero : raw.a[i]);
-    store_shared16(at + 4 * kChunkBytes, not_finite ? zero : raw.b[i]);
-    return not_finite;
-}
-
-__device__ __forceinline__ uint32_t tail_marks(const Raw<false> &) { return 0u; }
-__device__ __forceinline__ void store_tail(const Raw<false> &, uint32_t, int, uint32_t) {}
-
-template <bool kFp8>
-__device__ __forceinline__ void load_role(const AParams &p, Shared &s, uint8_t *smem, Cursor c)
-{
-    const int lane = threadIdx.x & 31, tid = threadIdx.x - kLoadWarp * 32;
-    const int key0 = (tid >> 5) * kWarpKeys, key = key0 + (lane & (kWarpKeys - 1));
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kRowWarp;
+    const int key0 = warp * kWarpKeys, key = key0 + (lane & (kWarpKeys - 1));
     const bool wide = ((reinterpret_cast<uintptr_t>(p.a.b.cache) | (8u * uint32_t(p.a.b.block_size))) & 15u) == 0u;
-    const uint32_t base = smem_addr(smem);
+    const uint32_t ring = smem + kRing<true> + warp * (kRingRows * 512) + 16 * lane;
     const int count = c.left;
-    KeyPlace now = key_place(p, c, key);
-    check_place(p, now);
-    Raw<kFp8> raw;
-#pragma unroll
-    for (int i = 0; i < kWarpKeys; ++i)
-        load_row(p, now, i, wide, raw);
-    load_tail(p, now, wide, raw);
-    const auto fill_query = [&](int request, int row0) {
-        load_query(p, request, row0, smem + kQuery, kRows, tid, kLoadWarps * 32);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&s.query);
+    // A key's block number is loaded three tiles ahead of its conversion, its row put on its way to
+    // L2 two and to the SM one tile ahead.
+    const auto place_and_advance = [&] {
+        const KeyPlace k = key_place(p, c, key, c.range.lo, c.range.hi);
+        if (c.left > 0)
+            c.advance(p);
+        return k;
     };
-    fill_query(c.request, c.row0);
-    // the cursor runs a tile ahead of the rows and two ahead of what is stored
-    bool next_begins = c.advance(p);
-    int next_request = c.request, next_row0 = c.row0;
-    KeyPlace next = key_place(p, c, key);
-    bool begins = false;  // this tile begins another unit than the first
-    int request = 0, row0 = 0, segment = 1;
+    const auto row_at = [&](KeyPlace k) {
+        check_place(p, k);
+        return fp8_row(p, k);
+    };
+    KeyPlace third = place_and_advance();
+    Fp8Row next = row_at(third);
+    Raw raw;
+    load_rows(p, next, ring, wide, raw);
+    bool now = next.data != nullptr;  // the tile's key is there
+    third = place_and_advance();
+    next = row_at(third);
+    prefetch_rows(p, next);
+    third = place_and_advance();
+    bool alive = true;
     for (int t = 0; t < count; ++t) {
-        bool after_begins = false;
-        KeyPlace after{0u, UINT32_MAX};
-        if (c.left > 0) {
-            after_begins = c.advance(p);
-            after = key_place(p, c, key);
-        }
-        bool alive = true;
-        if (begins) {
-            alive = __all_sync(kFull, mbar_wait(&s.query_free, (segment - 1) & 1));
-            ++segment;
-            if (alive)
-                fill_query(request, row0);
-        }
-        if (alive && t >= 2)
-            alive = __all_sync(kFull, mbar_wait(&s.free[t & 1], ((t >> 1) - 1) & 1));
-        if (!alive) {
-            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1)) {
+            alive = false;
             break;
         }
-        const uint32_t tile = base + kKeys + uint32_t(t & 1) * kTileBytes;
-        const uint32_t marks = tail_marks(raw);
-        const bool mine = now.off != UINT32_MAX;
-        check_place(p, next);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        const uint32_t tile = smem + kKeys + uint32_t(t & 1) * kTileBytes;
+        const uint32_t marks = __ballot_sync(kFull, bf16x8_not_finite(raw.tail) != 0u);
         uint32_t bad = 0u;
 #pragma unroll
         for (int i = 0; i < kWarpKeys; ++i) {
-            bad |= store_row(raw, i, tile, key0 + i, marks) ? 1u << i : 0u;
-            load_row(p, next, i, wide, raw);
+            const uint4 bits = i < kRingRows ? load_shared16(ring + 512 * i) : raw.last;
+            bad |= store_row(bits, raw.e[i], i, tile, key0 + i, marks) ? 1u << i : 0u;
         }
-        store_tail(raw, tile, key0, bad);
-        load_tail(p, next, wide, raw);
+        if (lane < 16)
+            store_shared16(tile + piece_of(key0 + (lane >> 2), 7, 4 + (lane & 3)),
+                           ((bad >> (lane >> 2)) & 1u) ? make_uint4(0u, 0u, 0u, 0u) : fp8_rope_operand(raw.tail));
         if (lane < kWarpKeys)
-            s.state[t & 1][key] = !mine ? kMissing : ((bad >> lane) & 1u) ? kNotFinite : kTaken;
+            s.state[t & 1][key] = !now ? kMissing : ((bad >> lane) & 1u) ? kNotFinite : kTaken;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&s.full[t & 1]);
+        // Every load stands behind the fence, which waits for those before it (128 heads, 262147
+        // bf16 keys, when those rows came this way too: 243 us with the next rows' loads before it, 188 so).
+        load_rows(p, next, ring, wide, raw);
+        now = next.data != nullptr;
+        next = row_at(third);
+        prefetch_rows(p, next);
+        third = place_and_advance();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!alive)
+        flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+}
+
+// ---- bf16 rows: copied as they are, and, where a tile is not seen whole by all rows of the unit
+// or lacks keys, looked through by warps 8..15
+//
+// In a tile that every row sees whole, a row that is not finite makes scores that are not finite
+// in every row of S, and the softmax makes NaN of those.
+
+// the keys that all rows of the unit see, but those of tokens that see nothing
+__device__ __forceinline__ Tiles::Range whole_range(const AParams &p, const Cursor &c)
+{
+    const AttentionArgs &a = p.a;
+    const int context = c.n - a.q_len;
+    if (a.tree != nullptr)
+        return Tiles::Range{a.window > 0 ? context + a.q_len - a.window : INT32_MIN, context};
+    const int first = int(fastdiv(uint32_t(c.row0), p.head_div)), last = int(fastdiv(uint32_t(c.row1 - 1), p.head_div));
+    return Tiles::Range{a.window > 0 ? context + 1 + last - a.window : INT32_MIN, context + 1 + first};
+}
+
+// Copy warp j has keys 16j.. of each tile, one a lane of its first half.  In boxes of more keys
+// the warp of the first one copies; a box is copied if a row of the unit may see a key of it.
+constexpr int kCopyKeys = kTileKeys / kCopyWarps;
+
+__device__ __forceinline__ void copy_role(const LParams &l, Shared &s, uint32_t smem, Cursor c)
+{
+    const AParams &p = l.w.p;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - (kMultiplyWarp<false> + 4);
+    const int count = c.left, box = l.box, key0 = kCopyKeys * warp, key = key0 + (lane & (kCopyKeys - 1));
+    const uint32_t elected = elect_one();
+    // what the warp copies of a tile
+    const int boxes = box > kCopyKeys ? (key0 % box == 0 ? 1 : 0) : box >= 8 ? kCopyKeys / box : 0;
+    const uint32_t bytes = (box >= 8 ? boxes * box : kCopyKeys) * DSV4_BF16_SLOT_BYTES;
+    struct Place {
+        KeyPlace k;
+        bool seen, dirty;
+    };
+    const auto place_and_advance = [&] {
+        const int lo = c.range.lo & ~(box - 1), hi = (c.range.hi + box - 1) & ~(box - 1), i = c.tile * kTileKeys;
+        const Tiles::Range whole = whole_range(p, c);
+        Place a;
+        a.k = key_place(p, c, key, lo, hi);
+        a.seen = i + key >= c.range.lo && i + key < c.range.hi;
+        a.dirty = i < whole.lo || i + kTileKeys > whole.hi;
+        if (c.left > 0)
+            c.advance(p);
+        return a;
+    };
+    // the key's row of the cache; row 0 for none, whose bytes the tile then has instead
+    const auto resolve = [&](Place &a) {
+        check_place(p, a.k);
+        const bool there = a.k.off != UINT32_MAX;
+        a.seen = a.seen && there;
+        a.dirty = a.dirty || __any_sync(kFull, !a.seen);
+        return there ? int(a.k.block * uint32_t(p.a.b.block_size) + a.k.off) : 0;
+    };
+    Place now = place_and_advance(), next = place_and_advance();
+    int row = resolve(now), t = 0;
+    for (; t < count; ++t) {
+        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1))
+            break;
+        if (lane < kCopyKeys)
+            s.state[t & 1][key] = now.seen ? kTaken : kMissing;
+        if (lane == 0)
+            s.dirty[t & 1][warp] = now.dirty;
+        __syncwarp();
+        if (elected != 0u)
+            mbar_arrive_expect_tx(&s.landed[t & 1], bytes);
+        __syncwarp();
+        const uint32_t to = smem + kKeys + uint32_t(t & 1) * kTileBytes + (key0 >> 3) * kGroupBytes;
+        if (box >= 8) {
+            for (int b = 0; b < boxes; ++b)
+                copy_groups(to + b * (box >> 3) * kGroupBytes, &l.rows, __shfl_sync(kFull, row, b * box) >> 3,
+                            &s.landed[t & 1], elected);
+        } else {
+            for (int g = 0; g < kCopyKeys; g += 4) {
+                int at[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    at[i] = __shfl_sync(kFull, row, g + i);
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i)
+                    copy_four(to + (g >> 3) * kGroupBytes + i * 1024 + (g & 4) * 128, &l.rows, 64 * i, at,
+                              &s.landed[t & 1], elected);
+            }
+        }
         now = next;
-        next = after;
-        begins = next_begins;
-        request = next_request;
-        row0 = next_row0;
-        next_begins = after_begins;
-        next_request = c.request;
-        next_row0 = c.row0;
+        row = resolve(now);
+        if (box >= 8 && t + 1 < count)
+            for (int b = 0; b < boxes; ++b)
+                prefetch_groups(&l.rows, __shfl_sync(kFull, row, b * box) >> 3, elected);
+        next = place_and_advance();
+    }
+    // nothing of this CTA's is on its way when it ends
+    bool alive = t == count;
+    for (int u = t >= 2 ? t - 2 : 0; u < t; ++u)
+        alive = warp_wait(&s.landed[u & 1], (u >> 1) & 1) && alive;
+    if (!alive)
+        flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+}
+
+// whether one of the copy warps found its keys of the tile in need of it
+__device__ __forceinline__ bool is_dirty(const Shared &s, int slot)
+{
+    uint32_t any = 0u;
+#pragma unroll
+    for (int j = 0; j < kCopyWarps; ++j)
+        any |= s.dirty[slot][j];
+    return any != 0u;
+}
+
+__device__ __forceinline__ void clean_role(const AParams &p, Shared &s, uint32_t smem, int count)
+{
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kRowWarp;
+    for (int t = 0; t < count; ++t) {
+        if (!warp_wait(&s.landed[t & 1], (t >> 1) & 1)) {
+            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+            return;
+        }
+        if (is_dirty(s, t & 1)) {
+            constexpr int kOwn = kTileKeys / Kind<false>::row_warps;
+#pragma unroll 2
+            for (int i = 0; i < kOwn; ++i) {
+                const int key = warp * kOwn + i;
+                const uint32_t at = smem + kKeys + uint32_t(t & 1) * kTileBytes + piece_of(key, lane >> 3, lane & 7);
+                const uint32_t bad =
+                    bf16x8_not_finite(load_shared16(at)) | bf16x8_not_finite(load_shared16(at + 4 * 1024));
+                if (!__any_sync(kFull, bad != 0u))
+                    continue;
+                store_shared16(at, make_uint4(0u, 0u, 0u, 0u));
+                store_shared16(at + 4 * 1024, make_uint4(0u, 0u, 0u, 0u));
+                if (lane == 0 && s.state[t & 1][key] == kTaken)
+                    s.state[t & 1][key] = kNotFinite;
+            }
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&s.full[t & 1]);
     }
 }
 
-// ---- Warp 24: the products
+// ---- The products, by one warp
 
+// What they take their operands from.  Slots of the two tiles are template arguments, so that
+// every descriptor is a constant away from these, in uniform registers.
+struct Operands {
+    Operand keys, query, values, probs;
+    uint32_t tmem, scores_inst, elected;
+};
+
+// the first product of the tile in slot kSlot
+template <int kSlot>
+__device__ __forceinline__ void multiply_scores(const Operands &o)
+{
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mma_bf16(o.tmem + kScoresAt + kSlot * kTileKeys, o.query + (i * kRows * 128 + 32 * k),
+                     o.keys + (kSlot * kTileBytes + i * 1024 + 32 * k), o.scores_inst, i > 0 || k > 0,
+                     o.elected);
+}
+
+// the second
+template <int kSlot, int kProbSlot>
+__device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst, bool first)
+{
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mma_bf16(o.tmem + i * kRows, o.values + (kSlot * kTileBytes + 2 * i * 1024 + 2 * kGroupBytes * k),
+                     o.probs + (kProbSlot * kProbBytes + 32 * k), inst, !first || k > 0, o.elected);
+}
+
+// Tile t's first product may run as soon as its rows are there and the second product of tile t - 2
+// has been issued, the second one as soon as its P is there: whichever is ready is issued.  (With
+// a fixed order each waited for the other's operands.)
+template <bool kFp8>
 __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
-    const uint32_t elected = elect_one();
-    const Operand keys = operand(smem + kKeys, 16, 1024), query = operand(smem + kQuery, 16, 1024);
-    const Operand values = operand(smem + kKeys, kChunkBytes, 1024);
-    const Operand probs = operand(smem + kProbs, 16, 1024);
-    const uint32_t scores_inst = instruction_of(kRows, kTileKeys, false, false);
-    // the second product of tile u
-    const auto output = [&](uint32_t u, uint32_t inst, bool first, bool last) {
-        if (!__all_sync(kFull, mbar_wait(&s.probs[u & 1], (u >> 1) & 1)))
-            return false;
+    Operands o;
+    o.keys = operand(smem + kKeys, 16, kGroupBytes);
+    o.query = operand(smem + kQuery, 16, 1024);
+    o.values = operand(smem + kKeys, 1024, kGroupBytes);
+    o.probs = operand(smem + kProbs, 16, 1024);
+    o.tmem = s.tmem;
+    o.scores_inst = instruction_of(kRows, kTileKeys, false, false);
+    o.elected = elect_one();
+    const int count = c.left;
+    int scores = 0, values = 0, segment = 0;  // the next tile of either product, and its segment
+    bool first = true;                        // of its segment, the next tile of the first product
+    uint32_t inst[2] = {0u, 0u};              // of the second products to come, by slot
+    bool begins[2] = {false, false}, ends[2] = {false, false};
+    const auto multiply_next_scores = [&](auto slot) {
+        constexpr int kSlot = decltype(slot)::value;
         tmem_fence_after();
-        const uint32_t tile = (u & 1) * kTileBytes, p_at = (u & 1) * (kRows * 128);
-#pragma unroll
-        for (int i = 0; i < kChunks / 2; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_bf16(s.tmem + i * kRows, values + (tile + 2 * i * kChunkBytes + 2048 * k),
-                         probs + (p_at + 32 * k), inst, !first || k > 0, elected);
-        mma_commit(&s.free[u & 1], elected);
-        if (last)
-            mma_commit(&s.output, elected);
-        return true;
-    };
-    int segment = 0;
-    bool first = true;  // of its segment
-    uint32_t t = 0, before_inst = 0;
-    bool before_first = false, before_last = false, alive = true;
-    for (; c.left > 0; ++t) {
-        if (first) {
-            alive = __all_sync(kFull, mbar_wait(&s.query, segment & 1));
-            ++segment;
-        }
-        alive = alive && __all_sync(kFull, mbar_wait(&s.full[t & 1], (t >> 1) & 1));
-        if (!alive)
-            break;
-        tmem_fence_after();
-        const uint32_t tile = (t & 1) * kTileBytes, d = s.tmem + kScoresAt + (t & 1) * kTileKeys;
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_bf16(d, query + (i * kRows * 128 + 32 * k), keys + (tile + i * kChunkBytes + 32 * k),
-                         scores_inst, i > 0 || k > 0, elected);
+        multiply_scores<kSlot>(o);
+        mma_commit(&s.scores[kSlot], o.elected);
         const bool last = c.ends_segment();
-        mma_commit(&s.scores[t & 1], elected);
         if (last)
-            mma_commit(&s.query_free, elected);
-        if (t > 0 && !output(t - 1, before_inst, before_first, before_last)) {
-            alive = false;
-            break;
-        }
-        before_inst = instruction_of(128, uint32_t((c.row1 - c.row0 + 15) & ~15), true, false);
-        before_first = first;
-        before_last = last;
+            mma_commit(&s.query_free, o.elected);
+        inst[kSlot] = instruction_of(128, uint32_t((c.row1 - c.row0 + 15) & ~15), true, false);
+        begins[kSlot] = first;
+        ends[kSlot] = last;
+        segment += first ? 1 : 0;
         first = last;
         c.advance(p);
+        ++scores;
+    };
+    const auto multiply_next_values = [&](auto slot) {
+        constexpr int kSlot = decltype(slot)::value;
+        tmem_fence_after();
+        multiply_values<kSlot, kFp8 ? 0 : kSlot>(o, inst[kSlot], begins[kSlot]);
+        mma_commit(&s.free[kSlot], o.elected);
+        if (ends[kSlot])
+            mma_commit(&s.output, o.elected);
+        ++values;
+    };
+    const auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, mbar_test(bar, parity)); };
+    const auto rows_ready = [&](int t) {
+        const int slot = t & 1;
+        const uint32_t parity = (t >> 1) & 1;
+        if constexpr (kFp8)
+            return ready(&s.full[slot], parity);
+        else
+            return ready(&s.landed[slot], parity) && (!is_dirty(s, slot) || ready(&s.full[slot], parity));
+    };
+    long long since = clock64();
+    while (values < count) {
+        if (scores < count && scores - values < 2 && rows_ready(scores) && (!first || ready(&s.query, segment & 1))) {
+            if (scores & 1)
+                multiply_next_scores(std::integral_constant<int, 1>());
+            else
+                multiply_next_scores(std::integral_constant<int, 0>());
+            since = clock64();
+        }
+        if (values < scores && ready(&s.probs[values & 1], (values >> 1) & 1)) {
+            if (values & 1)
+                multiply_next_values(std::integral_constant<int, 1>());
+            else
+                multiply_next_values(std::integral_constant<int, 0>());
+            since = clock64();
+        }
+        if (__any_sync(kFull, clock64() - since > kWaitCycles)) {
+            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+            return;
+        }
     }
-    if (alive && t > 0)
-        alive = output(t - 1, before_inst, before_first, before_last);
-    if (!alive)
-        flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
 
 // ---- Warps 0..7: softmax and results
@@ -431,7 +695,7 @@ struct RowView {
 __device__ __forceinline__ RowView view_of(const AParams &p, const Cursor &c, int r)
 {
     const AttentionArgs &a = p.a;
-    // a row past the unit's last has zeros for a query, and its results go nowhere
+    // the results of a row past the unit's last go nowhere
     RowView v{INT32_MAX, INT32_MIN, 0u};
     if (c.row0 + r >= c.row1)
         return v;
@@ -455,26 +719,34 @@ __device__ __forceinline__ RowView view_of(const AParams &p, const Cursor &c, in
     return v;
 }
 
-__device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor c)
+template <bool kFp8>
+__device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const Cursor &start)
 {
     const AParams &p = w.p;
     const AttentionArgs &a = p.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
     // rows r and r + 8; of each 8 keys of the half, the two from `pair` on
     const int r = 16 * warp + (lane >> 2), pair = 2 * (lane & 3), key0 = 32 * half;
+    // the warp's place lives in shared memory: the rest fills the registers
+    Cursor &c = s.place[threadIdx.x >> 5];
+    if (lane == 0)
+        c = start;
+    __syncwarp();
     const uint32_t tmem = s.tmem + (uint32_t(warp * 32) << 16);
     const float scale = a.scale * (kLog2e * w.unit);
-    const uint32_t probs = smem_addr(smem) + kProbs + 2 * pair;
+    const uint32_t probs = smem + kProbs + 2 * pair;
     RowView lo{0, 0, 0u}, hi{0, 0, 0u};
     int whole_to = 0, whole_from = 0;  // keys that all of the warp's rows see
     float m0 = 0.0f, m1 = 0.0f, sum0 = 0.0f, sum1 = 0.0f;
-    bool first = true;
+    bool first = true, valid_lo = true, valid_hi = true;  // of rows r and r + 8: of the unit
     int segment = 0, from_tile = 0;
     for (uint32_t t = 0; c.left > 0; ++t) {
         if (first) {
             from_tile = c.tile;
             lo = view_of(p, c, r);
             hi = view_of(p, c, r + 8);
+            valid_lo = c.row0 + r < c.row1;
+            valid_hi = c.row0 + r + 8 < c.row1;
             whole_to = __reduce_min_sync(kFull, min(lo.to, hi.to));
             whole_from = __reduce_max_sync(kFull, max(lo.from, hi.from));
             m0 = m1 = kUnset;
@@ -500,6 +772,16 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
                 v[j + 2] = __fmaf_rn(v[j + 2], scale, -ref1);
                 v[j + 3] = __fmaf_rn(v[j + 3], scale, -ref1);
             }
+            // an infinite score is one of a row that is not finite, or of a sum outside fp32
+            float least = v[0];
+#pragma unroll
+            for (int j = 1; j < 16; ++j)
+                least = fminf(least, v[j]);
+            if (least == -INFINITY) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] = v[j] == -INFINITY ? __int_as_float(0x7FFFFFFF) : v[j];
+            }
             if (__any_sync(kFull, (missing | marked) != 0u) || !whole) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -514,10 +796,12 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
         };
         __syncwarp();
         load_scores(m0, m1);
-        float over = v[0];
+        // (rows past the unit's last move nothing)
+        float over = -INFINITY;
 #pragma unroll
-        for (int j = 1; j < 16; ++j)
-            over = fmaxf(over, v[j]);
+        for (int j = 0; j < 16; ++j)
+            if (((j & 2) ? valid_hi : valid_lo))
+                over = fmaxf(over, v[j]);
         if (named_barrier_any(1, 256, failed || over > kSlack)) {
             if (!first)  // the second product of the tile before is done with O
                 failed = !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1) || failed;
@@ -569,15 +853,25 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             }
             load_scores(m0, m1);
         }
-        const uint32_t p_at = probs + (t & 1) * (kRows * 128);
+        uint32_t packed[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a0 = exp2_approx(v[4 * j]), a1 = exp2_approx(v[4 * j + 1]);
-            const float b0 = exp2_approx(v[4 * j + 2]), b1 = exp2_approx(v[4 * j + 3]);
+        for (int j = 0; j < 8; j += 2) {
+            const float a0 = exp2_approx(v[2 * j]), a1 = exp2_approx(v[2 * j + 1]);
+            const float b0 = exp2_approx(v[2 * j + 2]), b1 = exp2_approx(v[2 * j + 3]);
             sum0 += a0 + a1;
             sum1 += b0 + b1;
-            store_shared4(p_at + swizzled(r, 4 * half + j), bf16x2_rn(a0, a1));
-            store_shared4(p_at + swizzled(r + 8, 4 * half + j), bf16x2_rn(b0, b1));
+            packed[j] = bf16x2_rn(a0, a1);
+            packed[j + 1] = bf16x2_rn(b0, b1);
+        }
+        if (Kind<kFp8>::prob_slots == 1 && t > 0 && !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1)) {
+            // (P of the tile before was not taken; the others of the CTA run out of time as well)
+            flag(a.b.err, DSV4_DEVERR_TIMEOUT);
+        }
+        const uint32_t p_at = probs + (Kind<kFp8>::prob_slots == 1 ? 0u : (t & 1) * kProbBytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            store_shared4(p_at + swizzled(r, 4 * half + j), packed[2 * j]);
+            store_shared4(p_at + swizzled(r + 8, 4 * half + j), packed[2 * j + 1]);
         }
         fence_proxy_async_smem();
         tmem_fence_before();
@@ -665,32 +959,37 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint8_t *smem, Cursor 
             named_barrier(1, 256);  // m, factor and the halves' rows are free for the next segment
         }
         first = last;
-        c.advance(p);
+        __syncwarp();
+        if (lane == 0)
+            c.advance(p);
+        __syncwarp();
     }
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __grid_constant__ WParams w)
+__global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(const __grid_constant__ LParams l)
 {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    Shared &s = *reinterpret_cast<Shared *>(smem + kShared);
-    const AParams &p = w.p;
+    extern __shared__ __align__(1024) uint8_t smem_bytes[];
+    Shared &s = *reinterpret_cast<Shared *>(smem_bytes + kShared<kFp8>);
+    const uint32_t smem = smem_addr(smem_bytes);
+    const AParams &p = l.w.p;
     const int warp = threadIdx.x >> 5;
     wait_for_kernel_before();
-    if ((smem_addr(smem) & 1023u) != 0u) {  // never: there is no static shared memory
+    if ((smem & 1023u) != 0u) {  // never: there is no static shared memory
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
         return;
     }
-    if (warp == kMultiplyWarp) {
+    if (warp == kMultiplyWarp<kFp8>) {
         tmem_alloc512(&s.tmem);
         if ((threadIdx.x & 31) == 0) {
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&s.full[i], kLoadWarps);
+                mbar_init(&s.landed[i], kCopyWarps);
+                mbar_init(&s.full[i], Kind<kFp8>::row_warps);
                 mbar_init(&s.free[i], 1);
                 mbar_init(&s.scores[i], 1);
                 mbar_init(&s.probs[i], kSoftmaxWarps);
             }
-            mbar_init(&s.query, kLoadWarps);
+            mbar_init(&s.query, 1);
             mbar_init(&s.query_free, 1);
             mbar_init(&s.output, 1);
             mbar_init_fence();
@@ -700,26 +999,62 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
     Cursor c;
     Tiles::deal(p, blockIdx.x, gridDim.x, s.scratch, c);  // with barriers for the CTA
     tmem_fence_after();
-    if (warp >= kMultiplyWarp) {
-        registers_down<kMultiplyRegs>();
-        if (warp == kMultiplyWarp)
-            multiply_role(p, s, smem_addr(smem), c);
-        else if (warp == kMultiplyWarp + 1)
-            note_ends(w, c);
+    if (warp >= kMultiplyWarp<kFp8>) {
+        if constexpr (kFp8)
+            registers_down<Kind<true>::other_regs>();
+        if (warp == kMultiplyWarp<kFp8>)
+            multiply_role<kFp8>(p, s, smem, c);
+        else if (warp == kMultiplyWarp<kFp8> + 1)
+            note_ends(l.w, c);
+        else if (warp == kMultiplyWarp<kFp8> + 2)
+            query_role(l, s, smem, c);
+        else if (warp >= kMultiplyWarp<kFp8> + 4)
+            copy_role(l, s, smem, c);
     } else if (c.left == 0) {
         // more CTAs than tiles
     } else if (warp < kSoftmaxWarps) {
-        registers_up<kSoftmaxRegs>();
-        softmax_role(w, s, smem, c);
+        if constexpr (kFp8)
+            registers_up<Kind<true>::softmax_regs>();
+        softmax_role<kFp8>(l.w, s, smem, c);
     } else {
-        load_role<kFp8>(p, s, smem, c);
+        if constexpr (kFp8)
+            convert_role(p, s, smem, c);
+        else
+            clean_role(p, s, smem, c.left);
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == kMultiplyWarp) {
+    if (warp == kMultiplyWarp<kFp8>) {
         tmem_fence_after();
         tmem_free512(s.tmem);
     }
+}
+
+template <bool kFp8>
+int launch(const AttentionArgs &a, void *workspace, cudaStream_t stream)
+{
+    static std::atomic<int> sm_count[64];
+    int sms = 0;
+    if (configure_runs(latent_attention_kernel<kFp8>, kSmemBytes<kFp8>, sm_count, &sms) != DSV4_OK)
+        return DSV4_ERR_CUDA;
+    LParams l;
+    l.w = plan_runs<Tiles>(a, kFp8 ? kFp8OperandUnit : 1.0f, sms, workspace);
+    // the largest boxes of rows that never cross a block's end
+    l.box = kTileKeys;
+    while (a.b.block_size % l.box != 0)
+        l.box /= 2;
+    if (l.box < 8)
+        l.box = 1;
+    const uint64_t rows = uint64_t(a.b.num_blocks) * uint32_t(a.b.block_size);
+    int st = encode_rows(&l.q, a.q, uint64_t(a.b.batch) * uint32_t(l.w.p.all_rows), kRows);
+    if (st == DSV4_OK && !kFp8)
+        st = l.box >= 8 ? encode_groups(&l.rows, a.b.cache, rows / 8, uint32_t(l.box / 8))
+                        : encode_single_rows(&l.rows, a.b.cache, rows);
+    if (st != DSV4_OK)
+        return st;
+    st = launch_after(latent_attention_kernel<kFp8>, dim3(unsigned(l.w.runs)), dim3(kThreads<kFp8>), stream, l,
+                                kSmemBytes<kFp8>);
+    return st != DSV4_OK ? st : launch_join<Tiles>(l.w, stream);
 }
 
 }  // namespace
@@ -731,13 +1066,7 @@ size_t latent_attention_workspace()
 
 int launch_latent_attention(int store_mode, const AttentionArgs &a, void *workspace, cudaStream_t stream)
 {
-    static std::atomic<int> sm_count[2][64];
-    const bool fp8 = store_mode == DSV4_STORE_FP8;
-    const auto kernel = fp8 ? latent_attention_kernel<true> : latent_attention_kernel<false>;
-    int sms = 0;
-    if (configure_runs(kernel, kSmemBytes, sm_count[fp8], &sms) != DSV4_OK)
-        return DSV4_ERR_CUDA;
-    return launch_runs<Tiles>(kernel, kThreads, kSmemBytes, sms, a, fp8 ? kFp8OperandUnit : 1.0f, workspace, stream);
+    return store_mode == DSV4_STORE_FP8 ? launch<true>(a, workspace, stream) : launch<false>(a, workspace, stream);
 }
 
 }  // namespace dsv4

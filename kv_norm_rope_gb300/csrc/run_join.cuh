@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 
 // The current device's SMs, and the kernel's shared memory allowed on it; `sm_count` is the
 // kernel's own.
-inline int configure_runs(void (*kernel)(WParams), size_t smem, std::atomic<int> (&sm_count)[64], int *sms)
+template <typename P>
+inline int configure_runs(void (*kernel)(P), size_t smem, std::atomic<int> (&sm_count)[64], int *sms)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
@@ -329,10 +330,9 @@ inline size_t run_workspace()
     return size_t(kMaxCtas) * (2 * kPartialFloats * sizeof(float) + sizeof(RunEnds));
 }
 
-// The kernel, a CTA a run, then the join.
+// What an attention kernel of w.runs CTAs is launched with.
 template <typename Tiles>
-inline int launch_runs(void (*kernel)(WParams), int threads, size_t smem, int sms, const AttentionArgs &a,
-                       float unit, void *workspace, cudaStream_t stream)
+inline WParams plan_runs(const AttentionArgs &a, float unit, int sms, void *workspace)
 {
     WParams w;
     w.p = tile_params(a, kRows);
@@ -346,14 +346,18 @@ inline int launch_runs(void (*kernel)(WParams), int threads, size_t smem, int sm
     w.runs = runs;
     // each is begun by a run that is not the last
     w.splits = w.p.units < runs - 1 ? w.p.units : runs - 1;
-    const int st = launch_after(kernel, dim3(unsigned(runs)), dim3(unsigned(threads)), stream, w, smem);
-    if (st != DSV4_OK)
-        return st;
+    return w;
+}
+
+// The join, after that kernel.
+template <typename Tiles>
+inline int launch_join(const WParams &w, cudaStream_t stream)
+{
     const int idle = w.p.units < kIdleColumns ? w.p.units : kIdleColumns;
     const unsigned columns = unsigned(w.splits + idle);
     const unsigned rows = unsigned(w.p.all_rows < kRows ? w.p.all_rows : kRows);
     // a unit spans runs / units of them and at most two more
-    if (runs / w.p.units >= kJoinWarps)
+    if (w.runs / w.p.units >= kJoinWarps)
         return launch_after(join_kernel<true, Tiles>, dim3(columns, rows), dim3(kJoinWarps * 32), stream, w);
     return launch_after(join_kernel<false, Tiles>, dim3(columns, (rows + kJoinWarps - 1) / kJoinWarps),
                         dim3(kJoinWarps * 32), stream, w);
