@@ -59,11 +59,13 @@ constexpr int kTileKeys = kLatentTileKeys;
 using Tiles = KeyTiles<kTileKeys, kLatentStartCost, true>;
 using Cursor = Tiles::Cursor;
 
-// A tile lies in groups of 8 keys, a group in 8 chunks of 64 dims, each an atom of the swizzle
-// (tcgen05.cuh): a copy can bring whole groups, and both products read them as they are.
-constexpr int kChunks = 8;
-constexpr uint32_t kGroupBytes = kChunks * 1024;
-constexpr uint32_t kTileBytes = kTileKeys / 8 * kGroupBytes;
+// A tile lies in 4 parts of 128 dims, a part in groups of 8 keys, a group in 2 chunks of 64
+// dims, each an atom of the swizzle (tcgen05.cuh): a copy can bring a part of many groups, and both
+// products read it as it is.  The second product frees the parts one by one.
+constexpr int kChunks = 8, kParts = kChunks / 2;
+constexpr uint32_t kGroupBytes = 2 * 1024;
+constexpr uint32_t kPartBytes = kTileKeys / 8 * kGroupBytes;
+constexpr uint32_t kTileBytes = kParts * kPartBytes;
 constexpr uint32_t kQueryBytes = kChunks * kRows * 128;
 constexpr uint32_t kProbBytes = kRows * 128;  // 64 rows of 64 keys
 constexpr int kSoftmaxWarps = 8, kRowWarp = kSoftmaxWarps;  // warps from kRowWarp on see to the rows
@@ -77,7 +79,7 @@ template <>
 struct Kind<true> {
     static constexpr int row_warps = 16;
     static constexpr int prob_slots = 1;  // the second one's place is the ring's
-    static constexpr uint32_t ring_bytes = row_warps * 1536;
+    static constexpr uint32_t ring_bytes = row_warps * 3 * DSV4_NOPE_DIM;  // three rows of codes a warp
     // registers a thread: 72 at launch (896 * 72 = 64512), then
     static constexpr int softmax_regs = 88, row_regs = 72, other_regs = 40;
 };
@@ -87,9 +89,10 @@ struct Kind<false> {
     static constexpr int prob_slots = 2;
     static constexpr uint32_t ring_bytes = 0;
 };
-constexpr int kCopyWarps = 4;  // bf16
+constexpr int kCopyWarps = 4;   // bf16
+constexpr int kPlaceSlots = 3;  // FP8
 template <bool kFp8>
-constexpr int kMultiplyWarp = kRowWarp + Kind<kFp8>::row_warps;  // then the run's ends, the queries, none
+constexpr int kMultiplyWarp = kRowWarp + Kind<kFp8>::row_warps;  // then the run's ends, the queries, FP8: places
 template <bool kFp8>
 constexpr int kThreads = (kMultiplyWarp<kFp8> + 4 + (kFp8 ? 0 : kCopyWarps)) * 32;
 static_assert(128 * (2 * Kind<true>::softmax_regs + 4 * Kind<true>::row_regs + Kind<true>::other_regs) <=
@@ -109,8 +112,10 @@ constexpr uint32_t kShared = kRing<kFp8> + Kind<kFp8>::ring_bytes;
 constexpr uint32_t kScoresAt = 4 * kRows;
 
 struct Shared {
-    uint64_t landed[2];                              // bf16: of the copies of the two tiles in flight
-    uint64_t full[2], free[2], scores[2], probs[2];  // of the two tiles
+    // of the two tiles
+    uint64_t landed[2][kParts];  // bf16: of its copies
+    uint64_t full[2], scores[2], probs[2];
+    uint64_t free[2][kParts];    // (FP8: the last alone)
     uint64_t query, query_free, output;
     uint32_t tmem;
     int scratch[kDealWords];
@@ -118,11 +123,25 @@ struct Shared {
     alignas(16) float factor[kRows];
     float half_rows[2][kRows];  // maxima or sums over the keys of either half
     alignas(4) uint8_t state[2][kTileKeys];
-    alignas(16) uint32_t dirty[2][kCopyWarps];  // bf16: the tile has to be looked through before the products
     Cursor place[kSoftmaxWarps];
 };
 template <bool kFp8>
-constexpr size_t kSmemBytes = kShared<kFp8> + sizeof(Shared);
+struct KindShared;
+template <>
+struct KindShared<true> {
+    // where a tile's keys are (null: not there), and their exponents
+    uint64_t placed[kPlaceSlots], taken[kPlaceSlots];
+    const uint8_t *row[kPlaceSlots][kTileKeys];
+    uint2 exponents[kPlaceSlots][kTileKeys];
+};
+template <>
+struct KindShared<false> {
+    uint32_t dirty[2][kCopyWarps];  // the tile has to be looked through before the products
+};
+template <bool kFp8>
+constexpr uint32_t kKindShared = kShared<kFp8> + (sizeof(Shared) + 15) / 16 * 16;
+template <bool kFp8>
+constexpr size_t kSmemBytes = kKindShared<kFp8> + sizeof(KindShared<kFp8>);
 enum : uint8_t { kMissing = 0, kTaken = 1, kNotFinite = 2 };  // of a key
 static_assert(kSmemBytes<true> <= 227 * 1024 && kSmemBytes<false> <= 227 * 1024, "too much shared memory");
 
@@ -158,7 +177,7 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t at)
 // where 16 bytes of a key are in a tile: piece 0..7 of a chunk
 __device__ __forceinline__ uint32_t piece_of(int key, int chunk, int piece)
 {
-    return (key >> 3) * kGroupBytes + chunk * 1024 + swizzled(key & 7, piece);
+    return (chunk >> 1) * kPartBytes + (key >> 3) * kGroupBytes + (chunk & 1) * 1024 + swizzled(key & 7, piece);
 }
 
 // a wait by the whole warp
@@ -208,13 +227,19 @@ __device__ __forceinline__ void query_role(const LParams &l, Shared &s, uint32_t
         flag(l.w.p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
 
+// keeps values from being computed later than here
+__device__ __forceinline__ void computed(uint4 &v)
+{
+    asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
+}
+
 // ---- FP8 rows into operands: warps 8..23, a warp 4 keys of each tile
 //
-// Of a row lanes 0..27 have 16 codes and lanes 28..31 eight rope dims; the other 32 rope dims of
-// the four rows are with lanes 0..15.  The first three rows come through the warp's part of a ring in
-// shared memory (asynchronous copies into each lane's own bytes), the fourth, the rest of the
-// rope dims and the exponents in registers: what is on its way to registers takes lines of the
-// L1 that shared memory leaves, about 28 KB, and a load that finds none waits.
+// Of a row lanes 0..27 have 16 codes; of the rope dims of all four rows each lane has 8.  The codes of
+// the first three rows come through the warp's part of a ring in shared memory (asynchronous copies
+// into each lane's own bytes), those of the fourth and the rope dims in registers: what is on its way
+// to registers takes lines of the L1 that shared memory leaves, about 28 KB, and a load that
+// finds none waits.  Where the rows are, one warp finds for all, and puts them on their way to L2.
 
 constexpr int kWarpKeys = 4, kRingRows = 3;
 
@@ -251,29 +276,6 @@ __device__ __forceinline__ void check_place(const AParams &p, KeyPlace &k)
     }
 }
 
-// The place as addresses, found once by the lanes that have the key: null for none.  A row's
-// exponents stand `scale` bytes after its data.
-struct Fp8Row {
-    const uint8_t *data;
-    uint32_t scale;
-};
-
-__device__ __forceinline__ Fp8Row fp8_row(const AParams &p, const KeyPlace &k)
-{
-    if (k.off == UINT32_MAX)
-        return Fp8Row{nullptr, 0u};
-    const uint32_t bs = uint32_t(p.a.b.block_size);
-    return Fp8Row{p.a.b.cache + uint64_t(k.block) * bs * DSV4_FP8_SLOT_BYTES + uint64_t(k.off) * DSV4_FP8_DATA_BYTES,
-                  (bs - k.off) * DSV4_FP8_DATA_BYTES + k.off * DSV4_FP8_SCALE_BYTES};
-}
-
-__device__ __forceinline__ Fp8Row row_of_lane(const Fp8Row &mine, int lane)
-{
-    const uint64_t at = reinterpret_cast<uint64_t>(mine.data);
-    const uint32_t low = __shfl_sync(kFull, uint32_t(at), lane), high = __shfl_sync(kFull, uint32_t(at >> 32), lane);
-    return Fp8Row{reinterpret_cast<const uint8_t *>(uint64_t(high) << 32 | low), __shfl_sync(kFull, mine.scale, lane)};
-}
-
 // Rows are 16-byte aligned in caches with an even block size (wide), else 8-byte.
 __device__ __forceinline__ uint4 load_fp8_16(const AParams &p, const uint8_t *at, bool wide)
 {
@@ -298,132 +300,194 @@ __device__ __forceinline__ void copy_fp8_16(const AParams &p, uint32_t to, const
     }
 }
 
+// A lane has keys `lane` and `lane + 32` of a tile: their addresses and exponents, kPlaceSlots tiles
+// ahead of the converting warps at most, found two tiles and loaded one tile ahead of that.
+__device__ __forceinline__ void place_role(const AParams &p, Shared &s, KindShared<true> &ks, Cursor c)
+{
+    const int lane = threadIdx.x & 31, count = c.left;
+    struct Two {
+        KeyPlace k[2];
+    };
+    struct Rows {
+        const uint8_t *data[2];
+        uint2 exponents[2];
+    };
+    const auto place_and_advance = [&] {
+        Two a;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            a.k[h] = key_place(p, c, lane + 32 * h, c.range.lo, c.range.hi);
+        if (c.left > 0)
+            c.advance(p);
+        return a;
+    };
+    const auto load = [&](Two a) {
+        const Span cs = fp8_span(p.a.b);
+        const uint32_t bs = uint32_t(p.a.b.block_size);
+        Rows r;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            check_place(p, a.k[h]);
+            r.data[h] = nullptr;
+            r.exponents[h] = make_uint2(0u, 0u);
+            if (a.k[h].off == UINT32_MAX)
+                continue;
+            const uint8_t *page = p.a.b.cache + uint64_t(a.k[h].block) * bs * DSV4_FP8_SLOT_BYTES;
+            r.data[h] = page + uint64_t(a.k[h].off) * DSV4_FP8_DATA_BYTES;
+            r.exponents[h] = ldg8_now_in(page + uint64_t(bs) * DSV4_FP8_DATA_BYTES +
+                                             uint64_t(a.k[h].off) * DSV4_FP8_SCALE_BYTES, cs, p.a.b.err);
+            if (in_span(r.data[h], DSV4_FP8_DATA_BYTES, cs, p.a.b.err))
+#pragma unroll
+                for (int i = 0; i < DSV4_FP8_DATA_BYTES; i += 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(r.data[h] + i));
+        }
+        return r;
+    };
+    Rows now = load(place_and_advance());
+    Two next = place_and_advance();
+    for (int t = 0, slot = 0, round = 0; t < count; ++t) {
+        if (round > 0 && !warp_wait(&ks.taken[slot], (round - 1) & 1)) {
+            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+            return;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            ks.row[slot][lane + 32 * h] = now.data[h];
+            ks.exponents[slot][lane + 32 * h] = now.exponents[h];
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&ks.placed[slot]);
+        now = load(next);
+        next = place_and_advance();
+        if (++slot == kPlaceSlots) {
+            slot = 0;
+            ++round;
+        }
+    }
+}
+
 // what a lane holds of its warp's keys of a tile, beside the ring
 struct Raw {
-    uint4 last, tail;
-    uint32_t e[kWarpKeys];
+    uint4 last, rope;
 };
 
 // the warp's rows on their way (zeros for keys that are not there); ring: the lane's first bytes
-__device__ __forceinline__ void load_rows(const AParams &p, const Fp8Row &mine, uint32_t ring, bool wide, Raw &raw)
+__device__ __forceinline__ void load_rows(const AParams &p, const uint8_t *const *rows, uint32_t ring, bool wide,
+                                          Raw &raw)
 {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < kWarpKeys; ++i) {
-        const Fp8Row row = row_of_lane(mine, i);
-        const bool ok = row.data != nullptr;
-        if (i < kRingRows)
-            copy_fp8_16(p, ring + 512 * i, row.data + 16 * lane, ok, wide);
-        else
-            raw.last = ok ? load_fp8_16(p, row.data + 16 * lane, wide) : make_uint4(0u, 0u, 0u, 0u);
-        raw.e[i] = ok && lane < 28
-                       ? ldg_byte_now_in(row.data + row.scale + (lane >> 2), fp8_span(p.a.b), p.a.b.err)
-                       : 0u;
-    }
-    const Fp8Row row = row_of_lane(mine, (lane >> 2) & 3);
-    raw.tail = lane < 16 && row.data != nullptr
-                   ? load_fp8_16(p, row.data + DSV4_NOPE_DIM + 64 + 16 * (lane & 3), wide)
-                   : make_uint4(0u, 0u, 0u, 0u);
-}
-
-// the same on their way to L2: 8 lanes a row, five of them for its data and one for its exponents
-__device__ __forceinline__ void prefetch_rows(const AParams &p, const Fp8Row &mine)
-{
-    const int lane = threadIdx.x & 31, part = lane & 7;
-    const Fp8Row row = row_of_lane(mine, lane >> 3);
-    const uint8_t *at = row.data + (part < 5 ? 128u * part : row.scale);
-    if (row.data != nullptr && part < 6 && in_span(at, 1, fp8_span(p.a.b), p.a.b.err))
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-}
-
-// Row i of the warp's four, whose bytes are `bits`, into the operand at `tile` (key: its place there);
-// true where it is not finite: it is then zeros.  tail_marks: of the rows' other rope dims, by lane.
-__device__ __forceinline__ bool store_row(uint4 bits, uint32_t e, int i, uint32_t tile, int key, uint32_t tail_marks)
-{
-    const int lane = threadIdx.x & 31, chunk = lane >> 2, quarter = lane & 3;
-    uint4 first, second;
-    uint32_t bad;
+    const uint8_t *own = rows[lane >> 3];
+    raw.rope = own != nullptr ? load_fp8_16(p, own + DSV4_NOPE_DIM + 16 * (lane & 7), wide) : make_uint4(0u, 0u, 0u, 0u);
+    raw.last = make_uint4(0u, 0u, 0u, 0u);
     if (lane < 28) {
-        bad = e4m3x16_nan(bits) | (e > kFp8OperandTop ? 1u : 0u);
-        const uint32_t scale2 = fp8_operand_scale(e);
-        const uint4 lo = e4m3x8_scaled(bits.x, bits.y, scale2);
-        const uint4 hi = e4m3x8_scaled(bits.z, bits.w, scale2);
-        // odd chunks store their pieces the other way round: no two of 8 lanes meet in a bank
-        first = (chunk & 1) ? hi : lo;
-        second = (chunk & 1) ? lo : hi;
-    } else {
-        bad = bf16x8_not_finite(bits);
-        first = second = fp8_rope_operand(bits);
+        const uint8_t *row[kWarpKeys];
+#pragma unroll
+        for (int i = 0; i < kWarpKeys; ++i)
+            row[i] = rows[i];
+        if (row[kRingRows] != nullptr)
+            raw.last = load_fp8_16(p, row[kRingRows] + 16 * lane, wide);
+#pragma unroll
+        for (int i = 0; i < kRingRows; ++i)
+            copy_fp8_16(p, ring + DSV4_NOPE_DIM * i, row[i] + 16 * lane, row[i] != nullptr, wide);
     }
-    const bool not_finite = __any_sync(kFull, bad != 0u) || ((tail_marks >> (4 * i)) & 15u) != 0u;
-    if (not_finite)
-        first = second = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t at = tile + piece_of(key, chunk, lane < 28 ? 2 * quarter + (chunk & 1) : quarter);
-    store_shared16(at, first);
-    if (lane < 28)
-        store_shared16(at ^ 16u, second);
-    return not_finite;
 }
 
-__device__ __forceinline__ void convert_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
+// 16 codes times their block's scale as two pieces of an operand, the second first where `swap`;
+// nonzero if one of them is not finite.
+__device__ __forceinline__ uint32_t convert_codes(uint4 c, uint32_t e, bool swap, uint4 &first, uint4 &second)
 {
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kRowWarp;
-    const int key0 = warp * kWarpKeys, key = key0 + (lane & (kWarpKeys - 1));
+    const uint32_t scale2 = fp8_operand_scale(e);
+    first = e4m3x8_scaled(swap ? c.z : c.x, swap ? c.w : c.y, scale2);
+    second = e4m3x8_scaled(swap ? c.x : c.z, swap ? c.y : c.w, scale2);
+    return e4m3x16_nan(c) | (e > kFp8OperandTop ? 1u : 0u);
+}
+
+__device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindShared<true> &ks, uint32_t smem, int count)
+{
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kRowWarp, key0 = warp * kWarpKeys;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.a.b.cache) | (8u * uint32_t(p.a.b.block_size))) & 15u) == 0u;
-    const uint32_t ring = smem + kRing<true> + warp * (kRingRows * 512) + 16 * lane;
-    const int count = c.left;
-    // A key's block number is loaded three tiles ahead of its conversion, its row put on its way to
-    // L2 two and to the SM one tile ahead.
-    const auto place_and_advance = [&] {
-        const KeyPlace k = key_place(p, c, key, c.range.lo, c.range.hi);
-        if (c.left > 0)
-            c.advance(p);
-        return k;
-    };
-    const auto row_at = [&](KeyPlace k) {
-        check_place(p, k);
-        return fp8_row(p, k);
-    };
-    KeyPlace third = place_and_advance();
-    Fp8Row next = row_at(third);
+    const uint32_t ring = smem + kRing<true> + warp * (kRingRows * DSV4_NOPE_DIM) + 16 * lane;
+    // lanes 0..27: chunk lane / 4 of a row's codes, a quarter of it.  Odd chunks store their two pieces
+    // the other way round: no two of 8 lanes meet in a bank.
+    const bool odd = ((lane >> 2) & 1) != 0;
+    uint32_t place[kWarpKeys];
+#pragma unroll
+    for (int i = 0; i < kWarpKeys; ++i)
+        place[i] = smem + kKeys + piece_of(key0 + i, lane >> 2, 2 * (lane & 3) + (odd ? 1 : 0));
+    const uint32_t rope_place = smem + kKeys + piece_of(key0 + (lane >> 3), kChunks - 1, lane & 7);
     Raw raw;
-    load_rows(p, next, ring, wide, raw);
-    bool now = next.data != nullptr;  // the tile's key is there
-    third = place_and_advance();
-    next = row_at(third);
-    prefetch_rows(p, next);
-    third = place_and_advance();
-    bool alive = true;
-    for (int t = 0; t < count; ++t) {
-        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1)) {
+    bool alive = warp_wait(&ks.placed[0], 0);
+    if (alive)
+        load_rows(p, ks.row[0] + key0, ring, wide, raw);
+    int slot = 0, round = 0;  // of the tile's place
+    for (int t = 0; alive && t < count; ++t) {
+        // Converted before the wait for its place: that way only the stores stand between the product
+        // that frees it and the one that reads it.
+        uint32_t e[kWarpKeys];
+#pragma unroll
+        for (int i = 0; i < kWarpKeys; ++i)
+            e[i] = reinterpret_cast<const uint8_t *>(&ks.exponents[slot][key0 + i])[lane < 28 ? lane >> 2 : 7];
+        const bool there = ks.row[slot][key0 + (lane & (kWarpKeys - 1))] != nullptr;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        uint4 first[kWarpKeys], second[kWarpKeys];
+#pragma unroll
+        for (int i = 0; i < kRingRows; ++i)
+            first[i] = lane < 28 ? load_shared16(ring + DSV4_NOPE_DIM * i) : make_uint4(0u, 0u, 0u, 0u);
+        first[kRingRows] = raw.last;
+        uint32_t bad = bf16x8_not_finite(raw.rope) != 0u ? 1u << (lane >> 3) : 0u;
+        uint4 rope = fp8_rope_operand(raw.rope);
+#pragma unroll
+        for (int i = 0; i < kWarpKeys; ++i)
+            bad |= convert_codes(first[i], e[i], odd, first[i], second[i]) != 0u ? 1u << i : 0u;
+        bad = __reduce_or_sync(kFull, bad);
+        if (bad != 0u) {
+            // rows that are not finite enter as zeros
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < kWarpKeys; ++i)
+                if (((bad >> i) & 1u) != 0u)
+                    first[i] = second[i] = zero;
+            if (((bad >> (lane >> 3)) & 1u) != 0u)
+                rope = zero;
+        }
+#pragma unroll
+        for (int i = 0; i < kWarpKeys; ++i) {
+            computed(first[i]);
+            computed(second[i]);
+        }
+        if (t >= 2 && !warp_wait(&s.free[t & 1][kParts - 1], ((t >> 1) - 1) & 1)) {
             alive = false;
             break;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        const uint32_t tile = smem + kKeys + uint32_t(t & 1) * kTileBytes;
-        const uint32_t marks = __ballot_sync(kFull, bf16x8_not_finite(raw.tail) != 0u);
-        uint32_t bad = 0u;
+        const uint32_t tile = uint32_t(t & 1) * kTileBytes;
+        if (lane < 28) {
 #pragma unroll
-        for (int i = 0; i < kWarpKeys; ++i) {
-            const uint4 bits = i < kRingRows ? load_shared16(ring + 512 * i) : raw.last;
-            bad |= store_row(bits, raw.e[i], i, tile, key0 + i, marks) ? 1u << i : 0u;
+            for (int i = 0; i < kWarpKeys; ++i) {
+                store_shared16(place[i] + tile, first[i]);
+                store_shared16((place[i] + tile) ^ 16u, second[i]);
+            }
         }
-        if (lane < 16)
-            store_shared16(tile + piece_of(key0 + (lane >> 2), 7, 4 + (lane & 3)),
-                           ((bad >> (lane >> 2)) & 1u) ? make_uint4(0u, 0u, 0u, 0u) : fp8_rope_operand(raw.tail));
+        store_shared16(rope_place + tile, rope);
         if (lane < kWarpKeys)
-            s.state[t & 1][key] = !now ? kMissing : ((bad >> lane) & 1u) ? kNotFinite : kTaken;
+            s.state[t & 1][key0 + lane] = !there ? kMissing : ((bad >> lane) & 1u) ? kNotFinite : kTaken;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
+        if (lane == 0) {
             mbar_arrive(&s.full[t & 1]);
+            mbar_arrive(&ks.taken[slot]);
+        }
+        if (++slot == kPlaceSlots) {
+            slot = 0;
+            ++round;
+        }
         // Every load stands behind the fence, which waits for those before it (128 heads, 262147
         // bf16 keys, when those rows came this way too: 243 us with the next rows' loads before it, 188 so).
-        load_rows(p, next, ring, wide, raw);
-        now = next.data != nullptr;
-        next = row_at(third);
-        prefetch_rows(p, next);
-        third = place_and_advance();
+        if (t + 1 < count) {
+            alive = warp_wait(&ks.placed[slot], round & 1);
+            if (alive)
+                load_rows(p, ks.row[slot] + key0, ring, wide, raw);
+        }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!alive)
@@ -451,7 +515,7 @@ __device__ __forceinline__ Tiles::Range whole_range(const AParams &p, const Curs
 // the warp of the first one copies; a box is copied if a row of the unit may see a key of it.
 constexpr int kCopyKeys = kTileKeys / kCopyWarps;
 
-__device__ __forceinline__ void copy_role(const LParams &l, Shared &s, uint32_t smem, Cursor c)
+__device__ __forceinline__ void copy_role(const LParams &l, Shared &s, KindShared<false> &ks, uint32_t smem, Cursor c)
 {
     const AParams &p = l.w.p;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - (kMultiplyWarp<false> + 4);
@@ -459,7 +523,7 @@ __device__ __forceinline__ void copy_role(const LParams &l, Shared &s, uint32_t 
     const uint32_t elected = elect_one();
     // what the warp copies of a tile
     const int boxes = box > kCopyKeys ? (key0 % box == 0 ? 1 : 0) : box >= 8 ? kCopyKeys / box : 0;
-    const uint32_t bytes = (box >= 8 ? boxes * box : kCopyKeys) * DSV4_BF16_SLOT_BYTES;
+    const uint32_t bytes = (box >= 8 ? boxes * box : kCopyKeys) * (DSV4_BF16_SLOT_BYTES / kParts);
     struct Place {
         KeyPlace k;
         bool seen, dirty;
@@ -486,78 +550,95 @@ __device__ __forceinline__ void copy_role(const LParams &l, Shared &s, uint32_t 
     Place now = place_and_advance(), next = place_and_advance();
     int row = resolve(now), t = 0;
     for (; t < count; ++t) {
-        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1))
-            break;
-        if (lane < kCopyKeys)
-            s.state[t & 1][key] = now.seen ? kTaken : kMissing;
-        if (lane == 0)
-            s.dirty[t & 1][warp] = now.dirty;
-        __syncwarp();
-        if (elected != 0u)
-            mbar_arrive_expect_tx(&s.landed[t & 1], bytes);
-        __syncwarp();
         const uint32_t to = smem + kKeys + uint32_t(t & 1) * kTileBytes + (key0 >> 3) * kGroupBytes;
-        if (box >= 8) {
-            for (int b = 0; b < boxes; ++b)
-                copy_groups(to + b * (box >> 3) * kGroupBytes, &l.rows, __shfl_sync(kFull, row, b * box) >> 3,
-                            &s.landed[t & 1], elected);
-        } else {
-            for (int g = 0; g < kCopyKeys; g += 4) {
-                int at[4];
+        bool alive = true;
+        for (int i = 0; i < kParts && alive; ++i) {
+            if (t >= 2)
+                alive = warp_wait(&s.free[t & 1][i], ((t >> 1) - 1) & 1);
+            if (!alive)
+                break;
+            if (i == 0) {
+                // (the warps that look tiles through have seen the slot's last one)
+                if (t >= 2 && !warp_wait(&s.full[t & 1], ((t >> 1) - 1) & 1)) {
+                    alive = false;
+                    break;
+                }
+                if (lane < kCopyKeys)
+                    s.state[t & 1][key] = now.seen ? kTaken : kMissing;
+                if (lane == 0)
+                    ks.dirty[t & 1][warp] = now.dirty;
+                __syncwarp();
+            }
+            uint64_t *landed = &s.landed[t & 1][i];
+            if (elected != 0u)
+                mbar_arrive_expect_tx(landed, bytes);
+            __syncwarp();
+            if (box >= 8) {
+                for (int b = 0; b < boxes; ++b)
+                    copy_groups(to + i * kPartBytes + b * (box >> 3) * kGroupBytes, &l.rows, 2 * i,
+                                __shfl_sync(kFull, row, b * box) >> 3, landed, elected);
+            } else {
+                for (int g = 0; g < kCopyKeys; g += 4) {
+                    int at[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    at[i] = __shfl_sync(kFull, row, g + i);
+                    for (int j = 0; j < 4; ++j)
+                        at[j] = __shfl_sync(kFull, row, g + j);
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i)
-                    copy_four(to + (g >> 3) * kGroupBytes + i * 1024 + (g & 4) * 128, &l.rows, 64 * i, at,
-                              &s.landed[t & 1], elected);
+                    for (int j = 0; j < 2; ++j)
+                        copy_four(to + i * kPartBytes + (g >> 3) * kGroupBytes + j * 1024 + (g & 4) * 128, &l.rows,
+                                  128 * i + 64 * j, at, landed, elected);
+                }
             }
         }
+        if (!alive)
+            break;
         now = next;
         row = resolve(now);
-        if (box >= 8 && t + 1 < count)
-            for (int b = 0; b < boxes; ++b)
-                prefetch_groups(&l.rows, __shfl_sync(kFull, row, b * box) >> 3, elected);
         next = place_and_advance();
     }
-    // nothing of this CTA's is on its way when it ends
+    // nothing of this CTA's is on its way when it ends (a tile that was broken off at a part leaves
+    // the wait for the next to run out)
     bool alive = t == count;
-    for (int u = t >= 2 ? t - 2 : 0; u < t; ++u)
-        alive = warp_wait(&s.landed[u & 1], (u >> 1) & 1) && alive;
+    for (int u = t >= 2 ? t - 2 : 0; u < t + (alive ? 0 : 1); ++u)
+        for (int i = 0; i < kParts; ++i)
+            alive = warp_wait(&s.landed[u & 1][i], (u >> 1) & 1) && alive;
     if (!alive)
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
 
 // whether one of the copy warps found its keys of the tile in need of it
-__device__ __forceinline__ bool is_dirty(const Shared &s, int slot)
+__device__ __forceinline__ bool is_dirty(const KindShared<false> &ks, int slot)
 {
     uint32_t any = 0u;
 #pragma unroll
     for (int j = 0; j < kCopyWarps; ++j)
-        any |= s.dirty[slot][j];
+        any |= ks.dirty[slot][j];
     return any != 0u;
 }
 
-__device__ __forceinline__ void clean_role(const AParams &p, Shared &s, uint32_t smem, int count)
+__device__ __forceinline__ void clean_role(const AParams &p, Shared &s, const KindShared<false> &ks, uint32_t smem, int count)
 {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kRowWarp;
     for (int t = 0; t < count; ++t) {
-        if (!warp_wait(&s.landed[t & 1], (t >> 1) & 1)) {
+        bool alive = true;
+        for (int i = 0; i < kParts; ++i)
+            alive = alive && warp_wait(&s.landed[t & 1][i], (t >> 1) & 1);
+        if (!alive) {
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
             return;
         }
-        if (is_dirty(s, t & 1)) {
+        if (is_dirty(ks, t & 1)) {
             constexpr int kOwn = kTileKeys / Kind<false>::row_warps;
 #pragma unroll 2
             for (int i = 0; i < kOwn; ++i) {
                 const int key = warp * kOwn + i;
                 const uint32_t at = smem + kKeys + uint32_t(t & 1) * kTileBytes + piece_of(key, lane >> 3, lane & 7);
                 const uint32_t bad =
-                    bf16x8_not_finite(load_shared16(at)) | bf16x8_not_finite(load_shared16(at + 4 * 1024));
+                    bf16x8_not_finite(load_shared16(at)) | bf16x8_not_finite(load_shared16(at + 2 * kPartBytes));
                 if (!__any_sync(kFull, bad != 0u))
                     continue;
                 store_shared16(at, make_uint4(0u, 0u, 0u, 0u));
-                store_shared16(at + 4 * 1024, make_uint4(0u, 0u, 0u, 0u));
+                store_shared16(at + 2 * kPartBytes, make_uint4(0u, 0u, 0u, 0u));
                 if (lane == 0 && s.state[t & 1][key] == kTaken)
                     s.state[t & 1][key] = kNotFinite;
             }
@@ -578,36 +659,34 @@ struct Operands {
     uint32_t tmem, scores_inst, elected;
 };
 
-// the first product of the tile in slot kSlot
+// part `i` of the first product of the tile in slot kSlot
 template <int kSlot>
-__device__ __forceinline__ void multiply_scores(const Operands &o)
+__device__ __forceinline__ void multiply_scores(const Operands &o, int i)
 {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            mma_bf16(o.tmem + kScoresAt + kSlot * kTileKeys, o.query + (i * kRows * 128 + 32 * k),
-                     o.keys + (kSlot * kTileBytes + i * 1024 + 32 * k), o.scores_inst, i > 0 || k > 0,
-                     o.elected);
+            mma_bf16(o.tmem + kScoresAt + kSlot * kTileKeys, o.query + ((2 * i + j) * kRows * 128 + 32 * k),
+                     o.keys + (kSlot * kTileBytes + i * kPartBytes + j * 1024 + 32 * k), o.scores_inst,
+                     i > 0 || j > 0 || k > 0, o.elected);
 }
 
-// the second
+// of the second
 template <int kSlot, int kProbSlot>
-__device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst, bool first)
+__device__ __forceinline__ void multiply_values(const Operands &o, int i, uint32_t inst, bool first)
 {
 #pragma unroll
-    for (int i = 0; i < kChunks / 2; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            mma_bf16(o.tmem + i * kRows, o.values + (kSlot * kTileBytes + 2 * i * 1024 + 2 * kGroupBytes * k),
-                     o.probs + (kProbSlot * kProbBytes + 32 * k), inst, !first || k > 0, o.elected);
+    for (int k = 0; k < 4; ++k)
+        mma_bf16(o.tmem + i * kRows, o.values + (kSlot * kTileBytes + i * kPartBytes + 2 * kGroupBytes * k),
+                 o.probs + (kProbSlot * kProbBytes + 32 * k), inst, !first || k > 0, o.elected);
 }
 
-// Tile t's first product may run as soon as its rows are there and the second product of tile t - 2
-// has been issued, the second one as soon as its P is there: whichever is ready is issued.  (With
-// a fixed order each waited for the other's operands.)
+// A part of tile t's first product runs as soon as its rows are there, the second one of tile t - 1
+// as soon as its P is there, whichever is first.  (With a fixed order each waited for the other's
+// operands.)
 template <bool kFp8>
-__device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
+__device__ void multiply_role(const AParams &p, Shared &s, const KindShared<kFp8> &ks, uint32_t smem, Cursor c)
 {
     Operands o;
     o.keys = operand(smem + kKeys, 16, kGroupBytes);
@@ -618,65 +697,87 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
     o.scores_inst = instruction_of(kRows, kTileKeys, false, false);
     o.elected = elect_one();
     const int count = c.left;
-    int scores = 0, values = 0, segment = 0;  // the next tile of either product, and its segment
-    bool first = true;                        // of its segment, the next tile of the first product
-    uint32_t inst[2] = {0u, 0u};              // of the second products to come, by slot
-    bool begins[2] = {false, false}, ends[2] = {false, false};
-    const auto multiply_next_scores = [&](auto slot) {
+    int t = 0, segment = 0;  // the tile of the first product, and its segment
+    bool pending = false;    // the second product of tile t - 1 has not been issued
+    bool first = true;       // t begins its segment
+    uint32_t inst = 0u;      // of the pending product
+    bool begins = false, ends = false;
+    long long since = 0;
+    const auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, mbar_test(bar, parity)); };
+    const auto late = [&] { return __any_sync(kFull, clock64() - since > kWaitCycles) != 0; };
+    const auto multiply_pending = [&](auto slot) {
         constexpr int kSlot = decltype(slot)::value;
         tmem_fence_after();
-        multiply_scores<kSlot>(o);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            multiply_values<kSlot, kFp8 ? 0 : kSlot>(o, i, inst, begins);
+            if (!kFp8 || i == kParts - 1)
+                mma_commit(&s.free[kSlot][i], o.elected);
+        }
+        if (ends)
+            mma_commit(&s.output, o.elected);
+        pending = false;
+    };
+    // tile t, in slot kSlot; the pending one is in the other
+    const auto step = [&](auto slot) {
+        constexpr int kSlot = decltype(slot)::value;
+        constexpr std::integral_constant<int, 1 - kSlot> other;
+        const uint32_t parity = (t >> 1) & 1;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const auto there = [&] {
+                if constexpr (kFp8)
+                    return i > 0 || (ready(&s.full[kSlot], parity) && (!first || ready(&s.query, segment & 1)));
+                else
+                    return ready(&s.landed[kSlot][i], parity) &&
+                           (i > 0 || ((!is_dirty(ks, kSlot) || ready(&s.full[kSlot], parity)) &&
+                                      (!first || ready(&s.query, segment & 1))));
+            };
+            since = clock64();
+            while (!there()) {
+                if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
+                    multiply_pending(other);
+                else if (late())
+                    return false;
+            }
+            tmem_fence_after();
+            multiply_scores<kSlot>(o, i);
+        }
         mma_commit(&s.scores[kSlot], o.elected);
         const bool last = c.ends_segment();
         if (last)
             mma_commit(&s.query_free, o.elected);
-        inst[kSlot] = instruction_of(128, uint32_t((c.row1 - c.row0 + 15) & ~15), true, false);
-        begins[kSlot] = first;
-        ends[kSlot] = last;
+        if (pending) {
+            if (!warp_wait(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
+                return false;
+            multiply_pending(other);
+        }
+        inst = instruction_of(128, uint32_t((c.row1 - c.row0 + 15) & ~15), true, false);
+        begins = first;
+        ends = last;
+        pending = true;
         segment += first ? 1 : 0;
         first = last;
         c.advance(p);
-        ++scores;
+        ++t;
+        return true;
     };
-    const auto multiply_next_values = [&](auto slot) {
-        constexpr int kSlot = decltype(slot)::value;
-        tmem_fence_after();
-        multiply_values<kSlot, kFp8 ? 0 : kSlot>(o, inst[kSlot], begins[kSlot]);
-        mma_commit(&s.free[kSlot], o.elected);
-        if (ends[kSlot])
-            mma_commit(&s.output, o.elected);
-        ++values;
-    };
-    const auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, mbar_test(bar, parity)); };
-    const auto rows_ready = [&](int t) {
-        const int slot = t & 1;
-        const uint32_t parity = (t >> 1) & 1;
-        if constexpr (kFp8)
-            return ready(&s.full[slot], parity);
-        else
-            return ready(&s.landed[slot], parity) && (!is_dirty(s, slot) || ready(&s.full[slot], parity));
-    };
-    long long since = clock64();
-    while (values < count) {
-        if (scores < count && scores - values < 2 && rows_ready(scores) && (!first || ready(&s.query, segment & 1))) {
-            if (scores & 1)
-                multiply_next_scores(std::integral_constant<int, 1>());
-            else
-                multiply_next_scores(std::integral_constant<int, 0>());
-            since = clock64();
-        }
-        if (values < scores && ready(&s.probs[values & 1], (values >> 1) & 1)) {
-            if (values & 1)
-                multiply_next_values(std::integral_constant<int, 1>());
-            else
-                multiply_next_values(std::integral_constant<int, 0>());
-            since = clock64();
-        }
-        if (__any_sync(kFull, clock64() - since > kWaitCycles)) {
-            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
-            return;
-        }
+    bool alive = true;
+    while (alive && t < count) {
+        alive = step(std::integral_constant<int, 0>());
+        if (alive && t < count)
+            alive = step(std::integral_constant<int, 1>());
     }
+    if (alive && pending) {
+        const int slot = (t - 1) & 1;
+        alive = warp_wait(&s.probs[slot], ((t - 1) >> 1) & 1);
+        if (alive && slot == 0)
+            multiply_pending(std::integral_constant<int, 0>());
+        else if (alive)
+            multiply_pending(std::integral_constant<int, 1>());
+    }
+    if (!alive)
+        flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
 
 // ---- Warps 0..7: softmax and results
@@ -772,15 +873,17 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
                 v[j + 2] = __fmaf_rn(v[j + 2], scale, -ref1);
                 v[j + 3] = __fmaf_rn(v[j + 3], scale, -ref1);
             }
-            // an infinite score is one of a row that is not finite, or of a sum outside fp32
-            float least = v[0];
+if constexpr (!kFp8) {
+                // an infinite score is one of a row that is not finite, or of a sum outside fp32
+                float least = v[0];
 #pragma unroll
-            for (int j = 1; j < 16; ++j)
-                least = fminf(least, v[j]);
-            if (least == -INFINITY) {
+                for (int j = 1; j < 16; ++j)
+                    least = fminf(least, v[j]);
+                if (least == -INFINITY) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    v[j] = v[j] == -INFINITY ? __int_as_float(0x7FFFFFFF) : v[j];
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = v[j] == -INFINITY ? __int_as_float(0x7FFFFFFF) : v[j];
+                }
             }
             if (__any_sync(kFull, (missing | marked) != 0u) || !whole) {
 #pragma unroll
@@ -804,7 +907,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
                 over = fmaxf(over, v[j]);
         if (named_barrier_any(1, 256, failed || over > kSlack)) {
             if (!first)  // the second product of the tile before is done with O
-                failed = !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1) || failed;
+                failed = !mbar_wait(&s.free[(t - 1) & 1][kParts - 1], ((t - 1) >> 1) & 1) || failed;
             if (named_barrier_any(1, 256, failed)) {
                 flag(a.b.err, DSV4_DEVERR_TIMEOUT);
                 return;
@@ -863,7 +966,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
             packed[j] = bf16x2_rn(a0, a1);
             packed[j + 1] = bf16x2_rn(b0, b1);
         }
-        if (Kind<kFp8>::prob_slots == 1 && t > 0 && !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1)) {
+        if (Kind<kFp8>::prob_slots == 1 && t > 0 && !mbar_wait(&s.free[(t - 1) & 1][kParts - 1], ((t - 1) >> 1) & 1)) {
             // (P of the tile before was not taken; the others of the CTA run out of time as well)
             flag(a.b.err, DSV4_DEVERR_TIMEOUT);
         }
@@ -971,6 +1074,7 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
 {
     extern __shared__ __align__(1024) uint8_t smem_bytes[];
     Shared &s = *reinterpret_cast<Shared *>(smem_bytes + kShared<kFp8>);
+    KindShared<kFp8> &ks = *reinterpret_cast<KindShared<kFp8> *>(smem_bytes + kKindShared<kFp8>);
     const uint32_t smem = smem_addr(smem_bytes);
     const AParams &p = l.w.p;
     const int warp = threadIdx.x >> 5;
@@ -983,15 +1087,23 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         tmem_alloc512(&s.tmem);
         if ((threadIdx.x & 31) == 0) {
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&s.landed[i], kCopyWarps);
+                for (int j = 0; j < kParts; ++j) {
+                    mbar_init(&s.landed[i][j], kCopyWarps);
+                    mbar_init(&s.free[i][j], 1);
+                }
                 mbar_init(&s.full[i], Kind<kFp8>::row_warps);
-                mbar_init(&s.free[i], 1);
                 mbar_init(&s.scores[i], 1);
                 mbar_init(&s.probs[i], kSoftmaxWarps);
             }
             mbar_init(&s.query, 1);
             mbar_init(&s.query_free, 1);
             mbar_init(&s.output, 1);
+            if constexpr (kFp8) {
+                for (int i = 0; i < kPlaceSlots; ++i) {
+                    mbar_init(&ks.placed[i], 1);
+                    mbar_init(&ks.taken[i], Kind<true>::row_warps);
+                }
+            }
             mbar_init_fence();
         }
         tmem_fence_before();
@@ -1003,13 +1115,15 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         if constexpr (kFp8)
             registers_down<Kind<true>::other_regs>();
         if (warp == kMultiplyWarp<kFp8>)
-            multiply_role<kFp8>(p, s, smem, c);
+            multiply_role<kFp8>(p, s, ks, smem, c);
         else if (warp == kMultiplyWarp<kFp8> + 1)
             note_ends(l.w, c);
         else if (warp == kMultiplyWarp<kFp8> + 2)
             query_role(l, s, smem, c);
+        else if constexpr (kFp8)
+            place_role(p, s, ks, c);
         else if (warp >= kMultiplyWarp<kFp8> + 4)
-            copy_role(l, s, smem, c);
+            copy_role(l, s, ks, smem, c);
     } else if (c.left == 0) {
         // more CTAs than tiles
     } else if (warp < kSoftmaxWarps) {
@@ -1018,9 +1132,9 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         softmax_role<kFp8>(l.w, s, smem, c);
     } else {
         if constexpr (kFp8)
-            convert_role(p, s, smem, c);
+            convert_role(p, s, ks, smem, c.left);
         else
-            clean_role(p, s, smem, c.left);
+            clean_role(p, s, ks, smem, c.left);
     }
     tmem_fence_before();
     __syncthreads();

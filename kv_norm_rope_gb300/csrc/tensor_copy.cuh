@@ -31,25 +31,17 @@ __device__ __forceinline__ void copy_rows3(uint32_t to, const CUtensorMap *map, 
         : "memory");
 }
 
-// groups of 8 rows from `group` on, each as 8 chunks of its 8 rows (encode_groups)
-__device__ __forceinline__ void copy_groups(uint32_t to, const CUtensorMap *map, int group, uint64_t *bar,
+// chunks `chunk` and the next of groups of 8 rows from `group` on, each as 2 chunks of its 8 rows
+// (encode_groups)
+__device__ __forceinline__ void copy_groups(uint32_t to, const CUtensorMap *map, int chunk, int group, uint64_t *bar,
                                             uint32_t elected)
 {
     asm volatile(
-        "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %4, 0;\n\t"
+        "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %5, 0;\n\t"
         "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%5, %5, %5, %2}], [%3];\n\t}" ::"r"(to),
-        "l"(map), "r"(group), "r"(smem_addr(bar)), "r"(elected), "r"(0)
+        "[%0], [%1, {%6, %6, %2, %3}], [%4];\n\t}" ::"r"(to),
+        "l"(map), "r"(chunk), "r"(group), "r"(smem_addr(bar)), "r"(elected), "r"(0)
         : "memory");
-}
-
-// the same on their way to L2 only
-__device__ __forceinline__ void prefetch_groups(const CUtensorMap *map, int group, uint32_t elected)
-{
-    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %2, 0;\n\t"
-                 "@e cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%3, %3, %3, %1}];\n\t}" ::"l"(map),
-                 "r"(group), "r"(elected), "r"(0)
-                 : "memory");
 }
 
 // dims [dim, dim + 64) of four rows anywhere (encode_single_rows)
@@ -108,11 +100,12 @@ inline int encode_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32
     return encode_map(map, base, 3, sizes, strides, boxes);
 }
 
-// `groups` groups of 8 rows, in boxes of `box` groups: (dim in chunk, row in group, chunk, group)
+// `groups` groups of 8 rows, in boxes of 2 chunks of `box` groups: (dim in chunk, row in group,
+// chunk, group)
 inline int encode_groups(CUtensorMap *map, const void *base, uint64_t groups, uint32_t box)
 {
     const cuuint64_t sizes[4] = {64, 8, 8, groups}, strides[3] = {kRowBytes, 128, 8 * kRowBytes};
-    const cuuint32_t boxes[4] = {64, 8, 8, box};
+    const cuuint32_t boxes[4] = {64, 8, 2, box};
     return encode_map(map, base, 4, sizes, strides, boxes);
 }
 
