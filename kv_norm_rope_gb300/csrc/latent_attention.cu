@@ -59,13 +59,9 @@ constexpr int kTileKeys = kLatentTileKeys;
 using Tiles = KeyTiles<kTileKeys, kLatentStartCost, true>;
 using Cursor = Tiles::Cursor;
 
-// A tile lies in 4 parts of 128 dims, a part in groups of 8 keys, a group in 2 chunks of 64
-// dims, each an atom of the swizzle (tcgen05.cuh): a copy can bring a part of many groups, and both
-// products read it as it is.  The second product frees the parts one by one.
-constexpr int kChunks = 8, kParts = kChunks / 2;
-constexpr uint32_t kGroupBytes = 2 * 1024;
-constexpr uint32_t kPartBytes = kTileKeys / 8 * kGroupBytes;
-constexpr uint32_t kTileBytes = kParts * kPartBytes;
+constexpr int kChunks = 8;  // a row in chunks of 64 dims: a tile is 8 chunks of 64 keys
+constexpr uint32_t kChunkBytes = kTileKeys * 128;
+constexpr uint32_t kTileBytes = kChunks * kChunkBytes;
 constexpr uint32_t kQueryBytes = kChunks * kRows * 128;
 constexpr uint32_t kProbBytes = kRows * 128;  // 64 rows of 64 keys
 constexpr int kSoftmaxWarps = 8, kRowWarp = kSoftmaxWarps;  // warps from kRowWarp on see to the rows
@@ -89,12 +85,11 @@ struct Kind<false> {
     static constexpr int prob_slots = 2;
     static constexpr uint32_t ring_bytes = 0;
 };
-constexpr int kCopyWarps = 4;   // bf16
 constexpr int kPlaceSlots = 3;  // FP8
 template <bool kFp8>
 constexpr int kMultiplyWarp = kRowWarp + Kind<kFp8>::row_warps;  // then the run's ends, the queries, FP8: places
 template <bool kFp8>
-constexpr int kThreads = (kMultiplyWarp<kFp8> + 4 + (kFp8 ? 0 : kCopyWarps)) * 32;
+constexpr int kThreads = (kMultiplyWarp<kFp8> + 4) * 32;
 static_assert(128 * (2 * Kind<true>::softmax_regs + 4 * Kind<true>::row_regs + Kind<true>::other_regs) <=
                   kThreads<true> * 72,
               "the shares exceed what the CTA was launched with");
@@ -112,10 +107,7 @@ constexpr uint32_t kShared = kRing<kFp8> + Kind<kFp8>::ring_bytes;
 constexpr uint32_t kScoresAt = 4 * kRows;
 
 struct Shared {
-    // of the two tiles
-    uint64_t landed[2][kParts];  // bf16: of its copies
-    uint64_t full[2], scores[2], probs[2];
-    uint64_t free[2][kParts];    // (FP8: the last alone)
+    uint64_t full[2], free[2], scores[2], probs[2];  // of the two tiles
     uint64_t query, query_free, output;
     uint32_t tmem;
     int scratch[kDealWords];
@@ -135,9 +127,7 @@ struct KindShared<true> {
     uint2 exponents[kPlaceSlots][kTileKeys];
 };
 template <>
-struct KindShared<false> {
-    uint32_t dirty[2][kCopyWarps];  // the tile has to be looked through before the products
-};
+struct KindShared<false> {};
 template <bool kFp8>
 constexpr uint32_t kKindShared = kShared<kFp8> + (sizeof(Shared) + 15) / 16 * 16;
 template <bool kFp8>
@@ -147,9 +137,7 @@ static_assert(kSmemBytes<true> <= 227 * 1024 && kSmemBytes<false> <= 227 * 1024,
 
 struct LParams {
     WParams w;
-    CUtensorMap q;     // boxes of 64 rows
-    CUtensorMap rows;  // bf16: the cache, in boxes of `box` rows, or by single rows
-    int box;           // 64, 32, 16, 8, or 1: single rows, gathered by fours
+    CUtensorMap q;  // boxes of 64 rows
 };
 
 __device__ __forceinline__ void store_shared16(uint32_t at, uint4 v)
@@ -177,7 +165,7 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t at)
 // where 16 bytes of a key are in a tile: piece 0..7 of a chunk
 __device__ __forceinline__ uint32_t piece_of(int key, int chunk, int piece)
 {
-    return (chunk >> 1) * kPartBytes + (key >> 3) * kGroupBytes + (chunk & 1) * 1024 + swizzled(key & 7, piece);
+    return chunk * kChunkBytes + swizzled(key, piece);
 }
 
 // a wait by the whole warp
@@ -188,8 +176,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 
 // ---- Queries, by the copying warp
 
-// (Copies are issued by one elected lane of code that the whole warp runs with the same values:
-// from lanes of their own each took about 80 cycles.)
 __device__ __forceinline__ void copy_query(const LParams &l, Shared &s, uint32_t smem, int request, int row0,
                                            uint32_t elected)
 {
@@ -198,7 +184,7 @@ __device__ __forceinline__ void copy_query(const LParams &l, Shared &s, uint32_t
     __syncwarp();
     // rows past the unit's last are another request's, or zeros past the batch's: their scores
     // go nowhere
-    copy_rows3(smem + kQuery, &l.q, request * l.w.p.all_rows + row0, &s.query, elected);
+    copy_rows(smem + kQuery, &l.q, request * l.w.p.all_rows + row0, &s.query, elected);
 }
 
 __device__ __forceinline__ void query_role(const LParams &l, Shared &s, uint32_t smem, Cursor c)
@@ -248,17 +234,17 @@ __device__ __forceinline__ Span fp8_span(const PagedBatch &b)
     return Span{b.cache, uint64_t(b.num_blocks) * uint32_t(b.block_size) * DSV4_FP8_SLOT_BYTES};
 }
 
-// Where a key is: its block (on its way when this returns) and the offset in it, UINT32_MAX
-// for a key outside [lo, hi).
+// Where a key of a tile is: its block (on its way when this returns) and the offset in it,
+// UINT32_MAX for a key that no row of the unit may see.
 struct KeyPlace {
     uint32_t block, off;
 };
 
-__device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c, int key, int lo, int hi)
+__device__ __forceinline__ KeyPlace key_place(const AParams &p, const Cursor &c, int key)
 {
     KeyPlace k{0u, UINT32_MAX};
     const int i = c.tile * kTileKeys + key;
-    if (c.left > 0 && i >= lo && i < hi) {
+    if (c.left > 0 && i >= c.range.lo && i < c.range.hi) {
         const uint32_t at = fastdiv(uint32_t(i), p.block_div);
         k.off = uint32_t(i) - at * uint32_t(p.a.b.block_size);
         k.block = ldg4_now_in(p.a.b.table + c.request * p.a.b.table_stride + at, table_span(p.a.b),
@@ -316,7 +302,7 @@ __device__ __forceinline__ void place_role(const AParams &p, Shared &s, KindShar
         Two a;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            a.k[h] = key_place(p, c, lane + 32 * h, c.range.lo, c.range.hi);
+            a.k[h] = key_place(p, c, lane + 32 * h);
         if (c.left > 0)
             c.advance(p);
         return a;
@@ -456,7 +442,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
             computed(first[i]);
             computed(second[i]);
         }
-        if (t >= 2 && !warp_wait(&s.free[t & 1][kParts - 1], ((t >> 1) - 1) & 1)) {
+        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1)) {
             alive = false;
             break;
         }
@@ -494,11 +480,14 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
 
-// ---- bf16 rows: copied as they are, and, where a tile is not seen whole by all rows of the unit
-// or lacks keys, looked through by warps 8..15
+// ---- bf16 rows into operands: warps 8..15, a warp 8 keys of each tile
 //
-// In a tile that every row sees whole, a row that is not finite makes scores that are not finite
-// in every row of S, and the softmax makes NaN of those.
+// Copied as they are, asynchronously, half a row an instruction.  (By the copy unit, in boxes of up to 64
+// rows, a tile took no less: its copies wait for the products' use of shared memory as these
+// do.  Gathering single rows it took 3400 cycles a tile.)  A tile that is not seen whole by all rows
+// of the unit, or lacks keys, is looked through for rows that are not finite; in a tile that every
+// row sees whole, such a row makes scores that are not finite in every row of S, and the softmax
+// makes NaN of those.
 
 // the keys that all rows of the unit see, but those of tokens that see nothing
 __device__ __forceinline__ Tiles::Range whole_range(const AParams &p, const Cursor &c)
@@ -511,139 +500,99 @@ __device__ __forceinline__ Tiles::Range whole_range(const AParams &p, const Curs
     return Tiles::Range{a.window > 0 ? context + 1 + last - a.window : INT32_MIN, context + 1 + first};
 }
 
-// Copy warp j has keys 16j.. of each tile, one a lane of its first half.  In boxes of more keys
-// the warp of the first one copies; a box is copied if a row of the unit may see a key of it.
-constexpr int kCopyKeys = kTileKeys / kCopyWarps;
+// a lane's key of a tile, and whether some row of the unit does not see all of the tile
+struct Bf16Place {
+    KeyPlace k;
+    bool partly;
+};
 
-__device__ __forceinline__ void copy_role(const LParams &l, Shared &s, KindShared<false> &ks, uint32_t smem, Cursor c)
+__device__ __forceinline__ Bf16Place bf16_place(const AParams &p, const Cursor &c, int key)
 {
-    const AParams &p = l.w.p;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - (kMultiplyWarp<false> + 4);
-    const int count = c.left, box = l.box, key0 = kCopyKeys * warp, key = key0 + (lane & (kCopyKeys - 1));
-    const uint32_t elected = elect_one();
-    // what the warp copies of a tile
-    const int boxes = box > kCopyKeys ? (key0 % box == 0 ? 1 : 0) : box >= 8 ? kCopyKeys / box : 0;
-    const uint32_t bytes = (box >= 8 ? boxes * box : kCopyKeys) * (DSV4_BF16_SLOT_BYTES / kParts);
-    struct Place {
-        KeyPlace k;
-        bool seen, dirty;
-    };
+    const int i = c.tile * kTileKeys;
+    const Tiles::Range whole = whole_range(p, c);
+    return Bf16Place{key_place(p, c, key), i < whole.lo || i + kTileKeys > whole.hi};
+}
+
+// the key's row of the cache; row 0 for none, whose bytes the tile then has instead
+__device__ __forceinline__ uint32_t resolve(const AParams &p, Bf16Place &a)
+{
+    check_place(p, a.k);
+    return a.k.off != UINT32_MAX ? a.k.block * uint32_t(p.a.b.block_size) + a.k.off : 0u;
+}
+
+// Zeros for a key of the tile whose row is not finite: `at` is the first of the lane's two pieces, half a
+// row apart.  True if it is none.
+__device__ __forceinline__ bool clean_key(uint32_t at)
+{
+    const uint32_t bad = bf16x8_not_finite(load_shared16(at)) | bf16x8_not_finite(load_shared16(at + 4 * kChunkBytes));
+    if (!__any_sync(kFull, bad != 0u))
+        return true;
+    store_shared16(at, make_uint4(0u, 0u, 0u, 0u));
+    store_shared16(at + 4 * kChunkBytes, make_uint4(0u, 0u, 0u, 0u));
+    return false;
+}
+
+constexpr int kCopyKeys = kTileKeys / Kind<false>::row_warps;
+static_assert(kCopyKeys == 8, "a key and half a lane for its place");
+
+// 16 bytes to shared memory
+__device__ __forceinline__ void copy16(const AParams &p, uint32_t to, const uint8_t *from)
+{
+    const bool ok = in_span(from, 16, Span{p.a.b.cache, uint64_t(p.a.b.num_blocks) * uint32_t(p.a.b.block_size) *
+                                                            DSV4_BF16_SLOT_BYTES}, p.a.b.err);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(ok ? from : p.a.b.cache),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
+{
+    const int lane = threadIdx.x & 31, key0 = ((threadIdx.x >> 5) - kRowWarp) * kCopyKeys, key = key0 + (lane & 7);
+    const int count = c.left;
     const auto place_and_advance = [&] {
-        const int lo = c.range.lo & ~(box - 1), hi = (c.range.hi + box - 1) & ~(box - 1), i = c.tile * kTileKeys;
-        const Tiles::Range whole = whole_range(p, c);
-        Place a;
-        a.k = key_place(p, c, key, lo, hi);
-        a.seen = i + key >= c.range.lo && i + key < c.range.hi;
-        a.dirty = i < whole.lo || i + kTileKeys > whole.hi;
+        const Bf16Place a = bf16_place(p, c, key);
         if (c.left > 0)
             c.advance(p);
         return a;
     };
-    // the key's row of the cache; row 0 for none, whose bytes the tile then has instead
-    const auto resolve = [&](Place &a) {
-        check_place(p, a.k);
-        const bool there = a.k.off != UINT32_MAX;
-        a.seen = a.seen && there;
-        a.dirty = a.dirty || __any_sync(kFull, !a.seen);
-        return there ? int(a.k.block * uint32_t(p.a.b.block_size) + a.k.off) : 0;
-    };
-    Place now = place_and_advance(), next = place_and_advance();
-    int row = resolve(now), t = 0;
-    for (; t < count; ++t) {
-        const uint32_t to = smem + kKeys + uint32_t(t & 1) * kTileBytes + (key0 >> 3) * kGroupBytes;
-        bool alive = true;
-        for (int i = 0; i < kParts && alive; ++i) {
-            if (t >= 2)
-                alive = warp_wait(&s.free[t & 1][i], ((t >> 1) - 1) & 1);
-            if (!alive)
-                break;
-            if (i == 0) {
-                // (the warps that look tiles through have seen the slot's last one)
-                if (t >= 2 && !warp_wait(&s.full[t & 1], ((t >> 1) - 1) & 1)) {
-                    alive = false;
-                    break;
-                }
-                if (lane < kCopyKeys)
-                    s.state[t & 1][key] = now.seen ? kTaken : kMissing;
-                if (lane == 0)
-                    ks.dirty[t & 1][warp] = now.dirty;
-                __syncwarp();
-            }
-            uint64_t *landed = &s.landed[t & 1][i];
-            if (elected != 0u)
-                mbar_arrive_expect_tx(landed, bytes);
-            __syncwarp();
-            if (box >= 8) {
-                for (int b = 0; b < boxes; ++b)
-                    copy_groups(to + i * kPartBytes + b * (box >> 3) * kGroupBytes, &l.rows, 2 * i,
-                                __shfl_sync(kFull, row, b * box) >> 3, landed, elected);
-            } else {
-                for (int g = 0; g < kCopyKeys; g += 4) {
-                    int at[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        at[j] = __shfl_sync(kFull, row, g + j);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        copy_four(to + i * kPartBytes + (g >> 3) * kGroupBytes + j * 1024 + (g & 4) * 128, &l.rows,
-                                  128 * i + 64 * j, at, landed, elected);
-                }
-            }
-        }
-        if (!alive)
-            break;
-        now = next;
-        row = resolve(now);
-        next = place_and_advance();
-    }
-    // nothing of this CTA's is on its way when it ends (a tile that was broken off at a part leaves
-    // the wait for the next to run out)
-    bool alive = t == count;
-    for (int u = t >= 2 ? t - 2 : 0; u < t + (alive ? 0 : 1); ++u)
-        for (int i = 0; i < kParts; ++i)
-            alive = warp_wait(&s.landed[u & 1][i], (u >> 1) & 1) && alive;
-    if (!alive)
-        flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
-}
-
-// whether one of the copy warps found its keys of the tile in need of it
-__device__ __forceinline__ bool is_dirty(const KindShared<false> &ks, int slot)
-{
-    uint32_t any = 0u;
-#pragma unroll
-    for (int j = 0; j < kCopyWarps; ++j)
-        any |= ks.dirty[slot][j];
-    return any != 0u;
-}
-
-__device__ __forceinline__ void clean_role(const AParams &p, Shared &s, const KindShared<false> &ks, uint32_t smem, int count)
-{
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kRowWarp;
+    Bf16Place now = place_and_advance(), next = place_and_advance();
+    uint32_t row = resolve(p, now);
     for (int t = 0; t < count; ++t) {
-        bool alive = true;
-        for (int i = 0; i < kParts; ++i)
-            alive = alive && warp_wait(&s.landed[t & 1][i], (t >> 1) & 1);
-        if (!alive) {
+        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1)) {
             flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
             return;
         }
-        if (is_dirty(ks, t & 1)) {
-            constexpr int kOwn = kTileKeys / Kind<false>::row_warps;
-#pragma unroll 2
-            for (int i = 0; i < kOwn; ++i) {
-                const int key = warp * kOwn + i;
-                const uint32_t at = smem + kKeys + uint32_t(t & 1) * kTileBytes + piece_of(key, lane >> 3, lane & 7);
-                const uint32_t bad =
-                    bf16x8_not_finite(load_shared16(at)) | bf16x8_not_finite(load_shared16(at + 2 * kPartBytes));
-                if (!__any_sync(kFull, bad != 0u))
-                    continue;
-                store_shared16(at, make_uint4(0u, 0u, 0u, 0u));
-                store_shared16(at + 2 * kPartBytes, make_uint4(0u, 0u, 0u, 0u));
-                if (lane == 0 && s.state[t & 1][key] == kTaken)
-                    s.state[t & 1][key] = kNotFinite;
-            }
-            fence_proxy_async_smem();
+        const uint32_t group = smem + kKeys + uint32_t(t & 1) * kTileBytes + piece_of(key0, lane >> 3, 0);
+#pragma unroll
+        for (int i = 0; i < kCopyKeys; ++i) {
+            const uint8_t *from = p.a.b.cache + uint64_t(__shfl_sync(kFull, row, i)) * DSV4_BF16_SLOT_BYTES + 16 * lane;
+            const uint32_t to = group + swizzled(i, lane & 7);
+            copy16(p, to, from);
+            copy16(p, to + 4 * kChunkBytes, from + 512);
         }
+        const bool there = now.k.off != UINT32_MAX, look = now.partly || __any_sync(kFull, !there);
+        // the next tile's rows on their way to L2 meanwhile, 8 lanes a row
+        now = next;
+        row = resolve(p, now);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t *at = p.a.b.cache + 128 * (lane & 7) +
+                                uint64_t(__shfl_sync(kFull, row, 4 * i + (lane >> 3))) * DSV4_BF16_SLOT_BYTES;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
+        next = place_and_advance();
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        uint32_t finite = 0xffu;
+        if (look) {
+#pragma unroll 2
+            for (int i = 0; i < kCopyKeys; ++i)
+                if (!clean_key(group + swizzled(i, lane & 7)))
+                    finite &= ~(1u << i);
+        }
+        if (lane < kCopyKeys)
+            s.state[t & 1][key] = !there ? kMissing : ((finite >> lane) & 1u) ? kTaken : kNotFinite;
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&s.full[t & 1]);
@@ -659,39 +608,40 @@ struct Operands {
     uint32_t tmem, scores_inst, elected;
 };
 
-// part `i` of the first product of the tile in slot kSlot
+// the first product of the tile in slot kSlot
 template <int kSlot>
-__device__ __forceinline__ void multiply_scores(const Operands &o, int i)
+__device__ __forceinline__ void multiply_scores(const Operands &o)
 {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int i = 0; i < kChunks; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            mma_bf16(o.tmem + kScoresAt + kSlot * kTileKeys, o.query + ((2 * i + j) * kRows * 128 + 32 * k),
-                     o.keys + (kSlot * kTileBytes + i * kPartBytes + j * 1024 + 32 * k), o.scores_inst,
-                     i > 0 || j > 0 || k > 0, o.elected);
+            mma_bf16(o.tmem + kScoresAt + kSlot * kTileKeys, o.query + (i * kRows * 128 + 32 * k),
+                     o.keys + (kSlot * kTileBytes + i * kChunkBytes + 32 * k), o.scores_inst, i > 0 || k > 0,
+                     o.elected);
 }
 
-// of the second
+// the second
 template <int kSlot, int kProbSlot>
-__device__ __forceinline__ void multiply_values(const Operands &o, int i, uint32_t inst, bool first)
+__device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst, bool first)
 {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        mma_bf16(o.tmem + i * kRows, o.values + (kSlot * kTileBytes + i * kPartBytes + 2 * kGroupBytes * k),
-                 o.probs + (kProbSlot * kProbBytes + 32 * k), inst, !first || k > 0, o.elected);
+    for (int i = 0; i < kChunks / 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mma_bf16(o.tmem + i * kRows, o.values + (kSlot * kTileBytes + 2 * i * kChunkBytes + 2048 * k),
+                     o.probs + (kProbSlot * kProbBytes + 32 * k), inst, !first || k > 0, o.elected);
 }
 
-// A part of tile t's first product runs as soon as its rows are there, the second one of tile t - 1
-// as soon as its P is there, whichever is first.  (With a fixed order each waited for the other's
-// operands.)
+// Tile t's first product runs as soon as its rows are there, the second one of tile t - 1 as soon as
+// its P is there, whichever is first.  (In a fixed order each waited for the other's operands.)
 template <bool kFp8>
-__device__ void multiply_role(const AParams &p, Shared &s, const KindShared<kFp8> &ks, uint32_t smem, Cursor c)
+__device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
     Operands o;
-    o.keys = operand(smem + kKeys, 16, kGroupBytes);
+    o.keys = operand(smem + kKeys, 16, 1024);
     o.query = operand(smem + kQuery, 16, 1024);
-    o.values = operand(smem + kKeys, 1024, kGroupBytes);
+    o.values = operand(smem + kKeys, kChunkBytes, 1024);
     o.probs = operand(smem + kProbs, 16, 1024);
     o.tmem = s.tmem;
     o.scores_inst = instruction_of(kRows, kTileKeys, false, false);
@@ -702,18 +652,12 @@ __device__ void multiply_role(const AParams &p, Shared &s, const KindShared<kFp8
     bool first = true;       // t begins its segment
     uint32_t inst = 0u;      // of the pending product
     bool begins = false, ends = false;
-    long long since = 0;
     const auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, mbar_test(bar, parity)); };
-    const auto late = [&] { return __any_sync(kFull, clock64() - since > kWaitCycles) != 0; };
     const auto multiply_pending = [&](auto slot) {
         constexpr int kSlot = decltype(slot)::value;
         tmem_fence_after();
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-            multiply_values<kSlot, kFp8 ? 0 : kSlot>(o, i, inst, begins);
-            if (!kFp8 || i == kParts - 1)
-                mma_commit(&s.free[kSlot][i], o.elected);
-        }
+        multiply_values<kSlot, kFp8 ? 0 : kSlot>(o, inst, begins);
+        mma_commit(&s.free[kSlot], o.elected);
         if (ends)
             mma_commit(&s.output, o.elected);
         pending = false;
@@ -722,27 +666,15 @@ __device__ void multiply_role(const AParams &p, Shared &s, const KindShared<kFp8
     const auto step = [&](auto slot) {
         constexpr int kSlot = decltype(slot)::value;
         constexpr std::integral_constant<int, 1 - kSlot> other;
-        const uint32_t parity = (t >> 1) & 1;
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-            const auto there = [&] {
-                if constexpr (kFp8)
-                    return i > 0 || (ready(&s.full[kSlot], parity) && (!first || ready(&s.query, segment & 1)));
-                else
-                    return ready(&s.landed[kSlot][i], parity) &&
-                           (i > 0 || ((!is_dirty(ks, kSlot) || ready(&s.full[kSlot], parity)) &&
-                                      (!first || ready(&s.query, segment & 1))));
-            };
-            since = clock64();
-            while (!there()) {
-                if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
-                    multiply_pending(other);
-                else if (late())
-                    return false;
-            }
-            tmem_fence_after();
-            multiply_scores<kSlot>(o, i);
+        const long long since = clock64();
+        while (!ready(&s.full[kSlot], (t >> 1) & 1) || (first && !ready(&s.query, segment & 1))) {
+            if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
+                multiply_pending(other);
+            else if (__any_sync(kFull, clock64() - since > kWaitCycles))
+                return false;
         }
+        tmem_fence_after();
+        multiply_scores<kSlot>(o);
         mma_commit(&s.scores[kSlot], o.elected);
         const bool last = c.ends_segment();
         if (last)
@@ -818,6 +750,57 @@ __device__ __forceinline__ RowView view_of(const AParams &p, const Cursor &c, in
     else if (a.window > 0)
         v.from = v.to + __popcll(v.bits) - a.window;
     return v;
+}
+
+// 16 rows of 32 dims of the output from O^T: each lane brings the dim `dim` + lane of the rows, times
+// their factors, and stores 8 dims of two rows, after three exchanges with the lanes 1, 2 and 4
+// away.  (Stores of two dims took 7400 cycles a row tile, four times as many.)
+__device__ __forceinline__ void store_rows16(const float *o, const float *factor, bool some_idle,
+                                             const AttentionArgs &a, int64_t row0, int rows, int dim)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t x[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float4 f = *reinterpret_cast<const float4 *>(factor + 2 * i);
+        float v[4] = {o[2 * i] * f.x, o[2 * i + 1] * f.y, o[2 * i + 2] * f.z, o[2 * i + 3] * f.w};
+        if (some_idle) {
+            v[0] = f.x == 0.0f ? 0.0f : v[0];
+            v[1] = f.y == 0.0f ? 0.0f : v[1];
+            v[2] = f.z == 0.0f ? 0.0f : v[2];
+            v[3] = f.w == 0.0f ? 0.0f : v[3];
+        }
+        x[i] = bf16x2_rn(v[0], v[1]);
+        x[i + 1] = bf16x2_rn(v[2], v[3]);
+    }
+    // x[i]: rows 2i, 2i + 1 of one dim -> row 2i + lane % 2 of two dims
+    const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t other = __shfl_xor_sync(kFull, x[i], 1);
+        x[i] = __byte_perm(x[i], other, pick);
+    }
+    // -> rows 4q + lane % 4 of four dims
+    const bool second = (lane & 2) != 0, third = (lane & 4) != 0;
+    uint2 y[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t keep = second ? x[2 * q + 1] : x[2 * q];
+        const uint32_t got = __shfl_xor_sync(kFull, second ? x[2 * q] : x[2 * q + 1], 2);
+        y[q] = second ? make_uint2(got, keep) : make_uint2(keep, got);
+    }
+    // -> rows 8u + lane % 8 of eight dims
+    const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint2 keep = third ? y[2 * u + 1] : y[2 * u], give = third ? y[2 * u] : y[2 * u + 1];
+        const uint2 got = make_uint2(__shfl_xor_sync(kFull, give.x, 4), __shfl_xor_sync(kFull, give.y, 4));
+        const int row = 8 * u + (lane & 7);
+        if (row < rows)
+            st16_in(a.out + (row0 + row) * DSV4_HEAD_DIM + dim + (lane >> 3) * 8,
+                    third ? make_uint4(got.x, got.y, keep.x, keep.y) : make_uint4(keep.x, keep.y, got.x, got.y), os,
+                    a.b.err);
+    }
 }
 
 template <bool kFp8>
@@ -907,7 +890,7 @@ if constexpr (!kFp8) {
                 over = fmaxf(over, v[j]);
         if (named_barrier_any(1, 256, failed || over > kSlack)) {
             if (!first)  // the second product of the tile before is done with O
-                failed = !mbar_wait(&s.free[(t - 1) & 1][kParts - 1], ((t - 1) >> 1) & 1) || failed;
+                failed = !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1) || failed;
             if (named_barrier_any(1, 256, failed)) {
                 flag(a.b.err, DSV4_DEVERR_TIMEOUT);
                 return;
@@ -966,7 +949,7 @@ if constexpr (!kFp8) {
             packed[j] = bf16x2_rn(a0, a1);
             packed[j + 1] = bf16x2_rn(b0, b1);
         }
-        if (Kind<kFp8>::prob_slots == 1 && t > 0 && !mbar_wait(&s.free[(t - 1) & 1][kParts - 1], ((t - 1) >> 1) & 1)) {
+        if (Kind<kFp8>::prob_slots == 1 && t > 0 && !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1)) {
             // (P of the tile before was not taken; the others of the CTA run out of time as well)
             flag(a.b.err, DSV4_DEVERR_TIMEOUT);
         }
@@ -983,6 +966,7 @@ if constexpr (!kFp8) {
             mbar_arrive(&s.probs[t & 1]);
         if (last) {
             // the segment's result
+            const int row0 = c.row0, rows = c.row1 - c.row0;
 #pragma unroll
             for (int d = 1; d <= 2; d <<= 1) {
                 sum0 += __shfl_xor_sync(kFull, sum0, d);
@@ -996,6 +980,7 @@ if constexpr (!kFp8) {
                     s.m[r + 8] = m1;
                 }
             }
+            const float sink = threadIdx.x < rows ? sink_of(a, c.row0 + threadIdx.x) : 0.0f;
             failed = !mbar_wait(&s.output, segment & 1);
             ++segment;
             if (named_barrier_any(1, 256, failed)) {
@@ -1003,7 +988,6 @@ if constexpr (!kFp8) {
                 return;
             }
             tmem_fence_after();
-            const int row0 = c.row0, rows = c.row1 - c.row0;
             const bool whole_range = from_tile == c.range.first() && c.tile + 1 == c.range.stop();
             const int64_t out_row = int64_t(c.request) * p.all_rows + row0;
             // the run's first segment or its last
@@ -1014,8 +998,9 @@ if constexpr (!kFp8) {
                 const float total = s.half_rows[0][i] + s.half_rows[1][i];
                 if (whole_range) {
                     float lse = 0.0f;
+                    s.factor[i] = 1.0f;
                     if (i < rows)
-                        s.factor[i] = finish(s.m[i], total, sink_of(a, row0 + i), w.unit, &lse);
+                        s.factor[i] = finish(s.m[i], total, sink, w.unit, &lse);
                     if (i < rows && a.lse != nullptr)
                         st_f32_in(a.lse + out_row + i, lse, Span{a.lse, rows_of(a) * 4u}, a.b.err);
                 } else {
@@ -1024,38 +1009,33 @@ if constexpr (!kFp8) {
                 }
             }
             named_barrier(1, 256);
-            const Span os{a.out, rows_of(a) * (DSV4_HEAD_DIM * 2u)};
-            const int col0 = key0, mine = rows - col0 < 32 ? rows - col0 : 32;
-            if (mine > 0) {
+            const int mine = rows - key0;  // of the half's 32 rows, which are columns here
+            if (mine > 0 && whole_range) {
+                // (rows without keys have factor 0, and may have anything in O)
+                const bool some_idle = __any_sync(kFull, s.factor[key0 + lane] == 0.0f);
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
                     float o[32];
-                    tmem_load16(tmem + k * kRows + col0, o);
-                    tmem_load16(tmem + k * kRows + col0 + 16, o + 16);
+                    tmem_load16(tmem + k * kRows + key0, o);
+                    tmem_load16(tmem + k * kRows + key0 + 16, o + 16);
                     tmem_wait_load();
-                    const int dim = k * 128 + warp * 32 + lane;
-                    if (whole_range) {
-                        // neighbouring lanes swap, so that each stores two dims of one row
-                        const int odd = lane & 1;
-                        uint16_t *to = a.out + (out_row + col0 + odd) * DSV4_HEAD_DIM + (dim - odd);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            // (a row without keys has factor 0 and may have anything in O)
-                            const float f0 = s.factor[col0 + j], f1 = s.factor[col0 + j + 1];
-                            const float o0 = f0 == 0.0f ? 0.0f : o[j] * f0;
-                            const float o1 = f1 == 0.0f ? 0.0f : o[j + 1] * f1;
-                            const float other = __shfl_xor_sync(kFull, odd ? o0 : o1, 1);
-                            if (j + odd < mine)
-                                st4_in(to + j * DSV4_HEAD_DIM, odd ? bf16x2_rn(other, o1) : bf16x2_rn(o0, other),
-                                       os, a.b.err);
-                        }
-                    } else {
-                        float *to = part + col0 * DSV4_HEAD_DIM + dim;
+                    for (int i = 0; i < 32; i += 16)
+                        store_rows16(o + i, s.factor + key0 + i, some_idle, a, out_row + key0 + i, mine - i,
+                                     k * 128 + warp * 32);
+                }
+            } else if (mine > 0) {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    float o[32];
+                    tmem_load16(tmem + k * kRows + key0, o);
+                    tmem_load16(tmem + k * kRows + key0 + 16, o + 16);
+                    tmem_wait_load();
+                    float *to = part + key0 * DSV4_HEAD_DIM + k * 128 + warp * 32 + lane;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < mine)
-                                st_f32_in(to + j * DSV4_HEAD_DIM, o[j], ps, a.b.err);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (j < mine)
+                            st_f32_in(to + j * DSV4_HEAD_DIM, o[j], ps, a.b.err);
                 }
             }
             tmem_fence_before();
@@ -1087,10 +1067,7 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         tmem_alloc512(&s.tmem);
         if ((threadIdx.x & 31) == 0) {
             for (int i = 0; i < 2; ++i) {
-                for (int j = 0; j < kParts; ++j) {
-                    mbar_init(&s.landed[i][j], kCopyWarps);
-                    mbar_init(&s.free[i][j], 1);
-                }
+                mbar_init(&s.free[i], 1);
                 mbar_init(&s.full[i], Kind<kFp8>::row_warps);
                 mbar_init(&s.scores[i], 1);
                 mbar_init(&s.probs[i], kSoftmaxWarps);
@@ -1115,15 +1092,13 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         if constexpr (kFp8)
             registers_down<Kind<true>::other_regs>();
         if (warp == kMultiplyWarp<kFp8>)
-            multiply_role<kFp8>(p, s, ks, smem, c);
+            multiply_role<kFp8>(p, s, smem, c);
         else if (warp == kMultiplyWarp<kFp8> + 1)
             note_ends(l.w, c);
         else if (warp == kMultiplyWarp<kFp8> + 2)
             query_role(l, s, smem, c);
         else if constexpr (kFp8)
             place_role(p, s, ks, c);
-        else if (warp >= kMultiplyWarp<kFp8> + 4)
-            copy_role(l, s, ks, smem, c);
     } else if (c.left == 0) {
         // more CTAs than tiles
     } else if (warp < kSoftmaxWarps) {
@@ -1131,10 +1106,11 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
             registers_up<Kind<true>::softmax_regs>();
         softmax_role<kFp8>(l.w, s, smem, c);
     } else {
-        if constexpr (kFp8)
+        if constexpr (kFp8) {
             convert_role(p, s, ks, smem, c.left);
-        else
-            clean_role(p, s, ks, smem, c.left);
+        } else {
+            copy_role(p, s, smem, c);
+        }
     }
     tmem_fence_before();
     __syncthreads();
@@ -1153,17 +1129,7 @@ int launch(const AttentionArgs &a, void *workspace, cudaStream_t stream)
         return DSV4_ERR_CUDA;
     LParams l;
     l.w = plan_runs<Tiles>(a, kFp8 ? kFp8OperandUnit : 1.0f, sms, workspace);
-    // the largest boxes of rows that never cross a block's end
-    l.box = kTileKeys;
-    while (a.b.block_size % l.box != 0)
-        l.box /= 2;
-    if (l.box < 8)
-        l.box = 1;
-    const uint64_t rows = uint64_t(a.b.num_blocks) * uint32_t(a.b.block_size);
     int st = encode_rows(&l.q, a.q, uint64_t(a.b.batch) * uint32_t(l.w.p.all_rows), kRows);
-    if (st == DSV4_OK && !kFp8)
-        st = l.box >= 8 ? encode_groups(&l.rows, a.b.cache, rows / 8, uint32_t(l.box / 8))
-                        : encode_single_rows(&l.rows, a.b.cache, rows);
     if (st != DSV4_OK)
         return st;
     st = launch_after(latent_attention_kernel<kFp8>, dim3(unsigned(l.w.runs)), dim3(kThreads<kFp8>), stream, l,
