@@ -262,22 +262,24 @@ __device__ __forceinline__ void check_place(const AParams &p, KeyPlace &k)
     }
 }
 
-// Rows are 16-byte aligned in caches with an even block size (wide), else 8-byte.
-__device__ __forceinline__ uint4 load_fp8_16(const AParams &p, const uint8_t *at, bool wide)
+// Rows are 16-byte aligned in aligned caches with an even block size (kWide), else 8-byte.
+template <bool kWide>
+__device__ __forceinline__ uint4 load_fp8_16(const AParams &p, const uint8_t *at)
 {
     const Span cs = fp8_span(p.a.b);
-    if (wide)
+    if constexpr (kWide)
         return ldg16_now_in(at, cs, p.a.b.err);
     const uint2 lo = ldg8_now_in(at, cs, p.a.b.err), hi = ldg8_now_in(at + 8, cs, p.a.b.err);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
 // 16 bytes to shared memory, zeros for none
-__device__ __forceinline__ void copy_fp8_16(const AParams &p, uint32_t to, const uint8_t *from, bool ok, bool wide)
+template <bool kWide>
+__device__ __forceinline__ void copy_fp8_16(const AParams &p, uint32_t to, const uint8_t *from, bool ok)
 {
     ok = ok && in_span(from, 16, fp8_span(p.a.b), p.a.b.err);
     const uint8_t *at = ok ? from : p.a.b.cache;
-    if (wide) {
+    if constexpr (kWide) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(at), "r"(ok ? 16 : 0) : "memory");
     } else {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(at), "r"(ok ? 8 : 0) : "memory");
@@ -359,12 +361,12 @@ struct Raw {
 };
 
 // the warp's rows on their way (zeros for keys that are not there); ring: the lane's first bytes
-__device__ __forceinline__ void load_rows(const AParams &p, const uint8_t *const *rows, uint32_t ring, bool wide,
-                                          Raw &raw)
+template <bool kWide>
+__device__ __forceinline__ void load_rows(const AParams &p, const uint8_t *const *rows, uint32_t ring, Raw &raw)
 {
     const int lane = threadIdx.x & 31;
     const uint8_t *own = rows[lane >> 3];
-    raw.rope = own != nullptr ? load_fp8_16(p, own + DSV4_NOPE_DIM + 16 * (lane & 7), wide) : make_uint4(0u, 0u, 0u, 0u);
+    raw.rope = own != nullptr ? load_fp8_16<kWide>(p, own + DSV4_NOPE_DIM + 16 * (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
     raw.last = make_uint4(0u, 0u, 0u, 0u);
     if (lane < 28) {
         const uint8_t *row[kWarpKeys];
@@ -372,10 +374,10 @@ __device__ __forceinline__ void load_rows(const AParams &p, const uint8_t *const
         for (int i = 0; i < kWarpKeys; ++i)
             row[i] = rows[i];
         if (row[kRingRows] != nullptr)
-            raw.last = load_fp8_16(p, row[kRingRows] + 16 * lane, wide);
+            raw.last = load_fp8_16<kWide>(p, row[kRingRows] + 16 * lane);
 #pragma unroll
         for (int i = 0; i < kRingRows; ++i)
-            copy_fp8_16(p, ring + DSV4_NOPE_DIM * i, row[i] + 16 * lane, row[i] != nullptr, wide);
+            copy_fp8_16<kWide>(p, ring + DSV4_NOPE_DIM * i, row[i] + 16 * lane, row[i] != nullptr);
     }
 }
 
@@ -389,10 +391,10 @@ __device__ __forceinline__ uint32_t convert_codes(uint4 c, uint32_t e, bool swap
     return e4m3x16_nan(c) | (e > kFp8OperandTop ? 1u : 0u);
 }
 
+template <bool kWide>
 __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindShared<true> &ks, uint32_t smem, int count)
 {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kRowWarp, key0 = warp * kWarpKeys;
-    const bool wide = ((reinterpret_cast<uintptr_t>(p.a.b.cache) | (8u * uint32_t(p.a.b.block_size))) & 15u) == 0u;
     const uint32_t ring = smem + kRing<true> + warp * (kRingRows * DSV4_NOPE_DIM) + 16 * lane;
     // lanes 0..27: chunk lane / 4 of a row's codes, a quarter of it.  Odd chunks store their two pieces
     // the other way round: no two of 8 lanes meet in a bank.
@@ -405,7 +407,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
     Raw raw;
     bool alive = warp_wait(&ks.placed[0], 0);
     if (alive)
-        load_rows(p, ks.row[0] + key0, ring, wide, raw);
+        load_rows<kWide>(p, ks.row[0] + key0, ring, raw);
     int slot = 0, round = 0;  // of the tile's place
     for (int t = 0; alive && t < count; ++t) {
         // Converted before the wait for its place: that way only the stores stand between the product
@@ -472,7 +474,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
         if (t + 1 < count) {
             alive = warp_wait(&ks.placed[slot], round & 1);
             if (alive)
-                load_rows(p, ks.row[slot] + key0, ring, wide, raw);
+                load_rows<kWide>(p, ks.row[slot] + key0, ring, raw);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1049,7 +1051,7 @@ if constexpr (!kFp8) {
     }
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kWide>
 __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(const __grid_constant__ LParams l)
 {
     extern __shared__ __align__(1024) uint8_t smem_bytes[];
@@ -1107,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         softmax_role<kFp8>(l.w, s, smem, c);
     } else {
         if constexpr (kFp8) {
-            convert_role(p, s, ks, smem, c.left);
+            convert_role<kWide>(p, s, ks, smem, c.left);
         } else {
             copy_role(p, s, smem, c);
         }
@@ -1120,20 +1122,20 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
     }
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kWide>
 int launch(const AttentionArgs &a, void *workspace, cudaStream_t stream)
 {
     static std::atomic<int> sm_count[64];
     int sms = 0;
-    if (configure_runs(latent_attention_kernel<kFp8>, kSmemBytes<kFp8>, sm_count, &sms) != DSV4_OK)
+    if (configure_runs(latent_attention_kernel<kFp8, kWide>, kSmemBytes<kFp8>, sm_count, &sms) != DSV4_OK)
         return DSV4_ERR_CUDA;
     LParams l;
     l.w = plan_runs<Tiles>(a, kFp8 ? kFp8OperandUnit : 1.0f, sms, workspace);
     int st = encode_rows(&l.q, a.q, uint64_t(a.b.batch) * uint32_t(l.w.p.all_rows), kRows);
     if (st != DSV4_OK)
         return st;
-    st = launch_after(latent_attention_kernel<kFp8>, dim3(unsigned(l.w.runs)), dim3(kThreads<kFp8>), stream, l,
-                                kSmemBytes<kFp8>);
+    st = launch_after(latent_attention_kernel<kFp8, kWide>, dim3(unsigned(l.w.runs)), dim3(kThreads<kFp8>), stream, l,
+                      kSmemBytes<kFp8>);
     return st != DSV4_OK ? st : launch_join<Tiles>(l.w, stream);
 }
 
@@ -1146,7 +1148,10 @@ size_t latent_attention_workspace()
 
 int launch_latent_attention(int store_mode, const AttentionArgs &a, void *workspace, cudaStream_t stream)
 {
-    return store_mode == DSV4_STORE_FP8 ? launch<true>(a, workspace, stream) : launch<false>(a, workspace, stream);
+    if (store_mode != DSV4_STORE_FP8)
+        return launch<false, true>(a, workspace, stream);
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.b.cache) | (8u * uint32_t(a.b.block_size))) & 15u) == 0u;
+    return wide ? launch<true, true>(a, workspace, stream) : launch<true, false>(a, workspace, stream);
 }
 
 }  // namespace dsv4
