@@ -4,9 +4,14 @@
 // the others are copied.
 //
 // Bound by memory.  A thread has one column (a vector of 16 bytes; two of them in the half
-// layout, one from either half of the rotated dims) of one or four rows at once; the table's
-// rows come from L1 and L2, where the heads of a token share them.  Where a size, a stride or an
-// address is not a multiple of 16 bytes, a column is one pair or one copied element.
+// layout, one from either half of the rotated dims) of one or two rows at once.  Two rows of one
+// token share the table's values, which come from L1 and L2.  Where a size, a stride or an address is
+// not a multiple of 16 bytes, a column is one pair or one copied element.
+//
+// 16383 tokens of 32 heads of 128 fp16, 64 dims of them turned in halves out of place, take 51.5 us
+// (80% of a copy's rate).  What counts is how many loads an SM holds: with ten CTAs of 128 threads
+// (48 registers) 51.5 us, of 256 threads five 53 and as many as 60 registers let 56; four rows
+// at once 61, one 74.5; two rows of different tokens, each with its table's row, 58.
 
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
@@ -21,7 +26,7 @@
 namespace dsv4 {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
 struct RowParams {
     RopeRowsArgs a;
@@ -120,8 +125,8 @@ __device__ __forceinline__ void load_table(const float *p, Span s, int32_t *err,
     }
 }
 
-template <int kType, bool kVector, bool kHalf, int kRowsAtOnce>
-__global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_constant__ RowParams p)
+template <int kType, bool kVector, bool kHalf, int kRowsAtOnce, bool kOneToken>
+__global__ void __launch_bounds__(kRowThreads, 10) rope_rows_kernel(const __grid_constant__ RowParams p)
 {
     constexpr int kSize = kType == DSV4_TYPE_FP32 ? 4 : 2;
     constexpr int kElems = kVector ? 16 / kSize : 1;
@@ -135,7 +140,9 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
     const int half = a.rope_dim / 2;
     const Span xs{a.x, p.x_bytes}, os{a.out, p.out_bytes};
     const Span ts{a.cos_sin, uint64_t(a.max_position) * uint32_t(a.rope_dim) * 4u};
-    const int64_t row0 = int64_t(blockIdx.x) * (p.slots * kRowsAtOnce) + slot;
+    // a thread's rows: one after the other if they are one token's, else with the CTA's others between
+    const int64_t row0 = int64_t(blockIdx.x) * (p.slots * kRowsAtOnce) + slot * (kOneToken ? kRowsAtOnce : 1);
+    const uint32_t step = kOneToken ? 1u : p.slots;
     for (int column = threadIdx.x - slot * p.lanes; column < p.columns; column += p.lanes) {
         const bool turns = column < p.turned;
         // the column's first elements, and the pair that they begin with
@@ -153,18 +160,22 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
         uint4 first[kRowsAtOnce], second[kRowsAtOnce];
 #pragma unroll
         for (int u = 0; u < kRowsAtOnce; ++u) {
-            const int64_t row = row0 + int64_t(u) * p.slots;
+            const int64_t row = row0 + int64_t(u) * step;
             live[u] = row < p.rows;
             if (!live[u])
                 continue;
             const uint32_t token = fastdiv(uint32_t(row), p.head_div), head = uint32_t(row) - token * uint32_t(a.heads);
-            position[u] = ldg_i64_in(a.positions + token, Span{a.positions, uint64_t(a.tokens) * 8u}, a.err);
+            if (!kOneToken || u == 0)
+                position[u] = ldg_i64_in(a.positions + token, Span{a.positions, uint64_t(a.tokens) * 8u}, a.err);
+            else
+                position[u] = position[0];
             x_at[u] = (token * a.x_token_stride + head * a.x_head_stride + at) * kSize;
             out_at[u] = (token * a.out_token_stride + head * a.out_head_stride + at) * kSize;
             first[u] = load_some<kType, kVector>(a.x + x_at[u], xs, a.err);
             if (kTwo && turns)
                 second[u] = load_some<kType, kVector>(a.x + x_at[u] + other * kSize, xs, a.err);
         }
+        float c[kPairs], s[kPairs];
 #pragma unroll
         for (int u = 0; u < kRowsAtOnce; ++u) {
             if (!live[u])
@@ -175,10 +186,11 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
                 continue;
             }
             if (turns) {
-                float c[kPairs], s[kPairs];
-                const float *angles = a.cos_sin + position[u] * a.rope_dim + pair;
-                load_table<kPairs>(angles, ts, a.err, c);
-                load_table<kPairs>(angles + half, ts, a.err, s);
+                if (!kOneToken || u == 0) {
+                    const float *angles = a.cos_sin + position[u] * a.rope_dim + pair;
+                    load_table<kPairs>(angles, ts, a.err, c);
+                    load_table<kPairs>(angles + half, ts, a.err, s);
+                }
                 float f[2 * 8], g[8];
                 unpack<kType>(first[u], f);
                 if constexpr (kTwo)
@@ -202,17 +214,24 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
     }
 }
 
+template <int kType, bool kVector, bool kHalf, int kRowsAtOnce, bool kOneToken>
+int launch_rows(const RowParams &p, cudaStream_t stream)
+{
+    const int64_t per = int64_t(p.slots) * kRowsAtOnce;
+    return launch_after(rope_rows_kernel<kType, kVector, kHalf, kRowsAtOnce, kOneToken>,
+                        dim3(unsigned((p.rows + per - 1) / per)), dim3(kRowThreads), stream, p);
+}
+
 template <int kType, bool kVector, bool kHalf>
 int launch_kind(const RowParams &p, cudaStream_t stream)
 {
-    // four rows at once where that still gives each SM four CTAs, else one
-    const int64_t at_once = int64_t(p.slots) * 4;
-    const bool many = kVector && p.rows / at_once >= 4 * p.a.sms;
-    const int64_t per = many ? at_once : p.slots;
-    const dim3 grid(unsigned((p.rows + per - 1) / per));
-    if (many)
-        return launch_after(rope_rows_kernel<kType, kVector, kHalf, kVector ? 4 : 1>, grid, dim3(kRowThreads), stream, p);
-    return launch_after(rope_rows_kernel<kType, kVector, kHalf, 1>, grid, dim3(kRowThreads), stream, p);
+    // two rows at once where that still gives each SM four CTAs, else one
+    if constexpr (kVector) {
+        if (p.rows / (int64_t(p.slots) * 2) >= 4 * p.a.sms)
+            return p.a.heads % 2 == 0 ? launch_rows<kType, true, kHalf, 2, true>(p, stream)
+                                      : launch_rows<kType, true, kHalf, 2, false>(p, stream);
+    }
+    return launch_rows<kType, kVector, kHalf, 1, false>(p, stream);
 }
 
 template <int kType>
