@@ -257,11 +257,7 @@ def bf16_cache_bytes(num_blocks: int, block_size: int) -> int:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream_handle(stream) -> int | None:
@@ -295,7 +291,7 @@ def _check(name: str, t, kind: str, numel: int | None = None, min_bytes: int | N
     too few bytes.  Raw integer pointers pass unchecked; _on_cuda checks devices."""
     if t is None or isinstance(t, int):
         return
-    allowed = _kinds()[kind]
+    allowed = (_kinds_table or _kinds())[kind]
     if allowed is not None and t.dtype not in allowed:
         raise TypeError(f"{name}: expected {kind} data, got {t.dtype}")
     if not t.is_contiguous():
@@ -309,15 +305,18 @@ def _check(name: str, t, kind: str, numel: int | None = None, min_bytes: int | N
 
 def _on_cuda(**tensors):
     """Every tensor argument lives on one CUDA device: there is no CPU path."""
-    devices = set()
+    first, several = None, False
     for name, t in tensors.items():
         if t is None or isinstance(t, int):
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-        devices.add(t.device)
-    if len(devices) > 1:
-        raise ValueError(f"tensor arguments on several devices: {sorted(map(str, devices))}")
+        index = t.get_device()
+        several = several or first is not None and index != first
+        first = index
+    if several:
+        devices = {str(t.device) for t in tensors.values() if t is not None and not isinstance(t, int)}
+        raise ValueError(f"tensor arguments on several devices: {sorted(devices)}")
 
 
 def _check_step(store_mode, q, kv, w, positions, cos_sin_cache, slot_mapping, kv_cache,
@@ -580,9 +579,11 @@ def _check_rows(name: str, t, kind: str, batch: int) -> tuple:
     return (t.stride(0) if batch > 1 else t.shape[1]), t.shape[1]
 
 
+_CACHE_BYTES = {STORE_BF16: bf16_cache_bytes, STORE_FP4: fp4_cache_bytes, STORE_INDEXER: indexer_cache_bytes}
+
+
 def _cache_bytes(store_mode, num_blocks, block_size):
-    return {STORE_BF16: bf16_cache_bytes, STORE_FP4: fp4_cache_bytes, STORE_INDEXER: indexer_cache_bytes}.get(
-        store_mode, fp8_cache_bytes)(num_blocks, block_size)
+    return _CACHE_BYTES.get(store_mode, fp8_cache_bytes)(num_blocks, block_size)
 
 
 def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens, store_mode=STORE_FP4):
@@ -724,8 +725,10 @@ def _launch(what: str, device, stream, call) -> None:
     import torch
     if not isinstance(stream, int) and stream is not None and stream.device != device:
         raise ValueError(f"stream: on {stream.device}, the tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        st = call(_stream_handle(stream))
+    current = torch.cuda.current_device()
+    if device.index == current:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) if stream is None else None
+        st = call(raw(current) if raw is not None else _stream_handle(stream))
     else:
         with torch.cuda.device(device):
             st = call(_stream_handle(stream))
