@@ -98,6 +98,18 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// this thread's asynchronous copies of single pieces (cp.async): until they have landed
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// an arrival of this thread at *bar once they have, one of those the barrier counts on
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // order this thread's earlier generic-proxy accesses to shared memory before
 // later bulk copies (the async proxy) that overwrite it
 __device__ __forceinline__ void fence_proxy_async_smem()

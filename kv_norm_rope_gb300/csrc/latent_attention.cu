@@ -75,6 +75,7 @@ template <>
 struct Kind<true> {
     static constexpr int row_warps = 16;
     static constexpr int prob_slots = 1;  // the second one's place is the ring's
+    static constexpr int parts = 1;       // of the dims, that a tile is filled and freed in
     static constexpr uint32_t ring_bytes = row_warps * 3 * DSV4_NOPE_DIM;  // three rows of codes a warp
     // registers a thread: 72 at launch (896 * 72 = 64512), then
     static constexpr int softmax_regs = 88, row_regs = 72, other_regs = 40;
@@ -83,6 +84,7 @@ template <>
 struct Kind<false> {
     static constexpr int row_warps = 8;
     static constexpr int prob_slots = 2;
+    static constexpr int parts = 2;
     static constexpr uint32_t ring_bytes = 0;
 };
 constexpr int kPlaceSlots = 3;  // FP8
@@ -107,7 +109,8 @@ constexpr uint32_t kShared = kRing<kFp8> + Kind<kFp8>::ring_bytes;
 constexpr uint32_t kScoresAt = 4 * kRows;
 
 struct Shared {
-    uint64_t full[2], free[2], scores[2], probs[2];  // of the two tiles
+    uint64_t full[2][2], free[2][2];  // of the two tiles, and their parts
+    uint64_t scores[2], probs[2];     // of the two tiles
     uint64_t query, query_free, output;
     uint32_t tmem;
     int scratch[kDealWords];
@@ -417,7 +420,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
         for (int i = 0; i < kWarpKeys; ++i)
             e[i] = reinterpret_cast<const uint8_t *>(&ks.exponents[slot][key0 + i])[lane < 28 ? lane >> 2 : 7];
         const bool there = ks.row[slot][key0 + (lane & (kWarpKeys - 1))] != nullptr;
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        copies_wait();
         uint4 first[kWarpKeys], second[kWarpKeys];
 #pragma unroll
         for (int i = 0; i < kRingRows; ++i)
@@ -444,7 +447,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
             computed(first[i]);
             computed(second[i]);
         }
-        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1)) {
+        if (t >= 2 && !warp_wait(&s.free[t & 1][0], ((t >> 1) - 1) & 1)) {
             alive = false;
             break;
         }
@@ -462,7 +465,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(&s.full[t & 1]);
+            mbar_arrive(&s.full[t & 1][0]);
             mbar_arrive(&ks.taken[slot]);
         }
         if (++slot == kPlaceSlots) {
@@ -477,7 +480,7 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
                 load_rows<kWide>(p, ks.row[slot] + key0, ring, raw);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    copies_wait();
     if (!alive)
         flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
 }
@@ -560,19 +563,31 @@ __device__ __forceinline__ void copy_role(const AParams &p, Shared &s, uint32_t 
     Bf16Place now = place_and_advance(), next = place_and_advance();
     uint32_t row = resolve(p, now);
     for (int t = 0; t < count; ++t) {
-        if (t >= 2 && !warp_wait(&s.free[t & 1], ((t >> 1) - 1) & 1)) {
-            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
-            return;
-        }
-        const uint32_t group = smem + kKeys + uint32_t(t & 1) * kTileBytes + piece_of(key0, lane >> 3, 0);
-#pragma unroll
-        for (int i = 0; i < kCopyKeys; ++i) {
-            const uint8_t *from = p.a.b.cache + uint64_t(__shfl_sync(kFull, row, i)) * DSV4_BF16_SLOT_BYTES + 16 * lane;
-            const uint32_t to = group + swizzled(i, lane & 7);
-            copy16(p, to, from);
-            copy16(p, to + 4 * kChunkBytes, from + 512);
-        }
         const bool there = now.k.off != UINT32_MAX, look = now.partly || __any_sync(kFull, !there);
+        const uint32_t group = smem + kKeys + uint32_t(t & 1) * kTileBytes + piece_of(key0, lane >> 3, 0);
+        bool alive = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            alive = alive && (t < 2 || warp_wait(&s.free[t & 1][h], ((t >> 1) - 1) & 1));
+            if (!alive)
+                break;
+#pragma unroll
+            for (int i = 0; i < kCopyKeys; ++i)
+                copy16(p, group + swizzled(i, lane & 7) + h * 4 * kChunkBytes,
+                       p.a.b.cache + uint64_t(__shfl_sync(kFull, row, i)) * DSV4_BF16_SLOT_BYTES + 16 * lane + 512 * h);
+            if (!look) {
+                if (h == 1 && lane < kCopyKeys)
+                    s.state[t & 1][key] = kTaken;
+                copies_arrive(&s.full[t & 1][h]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&s.full[t & 1][h]);
+            }
+        }
+        if (!alive) {
+            flag(p.a.b.err, DSV4_DEVERR_TIMEOUT);
+            break;
+        }
         // the next tile's rows on their way to L2 meanwhile, 8 lanes a row
         now = next;
         row = resolve(p, now);
@@ -583,22 +598,26 @@ __device__ __forceinline__ void copy_role(const AParams &p, Shared &s, uint32_t 
             asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
         }
         next = place_and_advance();
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-        uint32_t finite = 0xffu;
         if (look) {
+            copies_wait();
+            __syncwarp();
+            uint32_t finite = 0xffu;
 #pragma unroll 2
             for (int i = 0; i < kCopyKeys; ++i)
                 if (!clean_key(group + swizzled(i, lane & 7)))
                     finite &= ~(1u << i);
+            if (lane < kCopyKeys)
+                s.state[t & 1][key] = !there ? kMissing : ((finite >> lane) & 1u) ? kTaken : kNotFinite;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                copies_arrive(&s.full[t & 1][h]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&s.full[t & 1][h]);
+            }
         }
-        if (lane < kCopyKeys)
-            s.state[t & 1][key] = !there ? kMissing : ((finite >> lane) & 1u) ? kTaken : kNotFinite;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&s.full[t & 1]);
     }
+    copies_wait();
 }
 
 // ---- The products, by one warp
@@ -610,12 +629,12 @@ struct Operands {
     uint32_t tmem, scores_inst, elected;
 };
 
-// the first product of the tile in slot kSlot
-template <int kSlot>
+// part kPart of kParts of the sum of the first product, of the tile in slot kSlot
+template <int kSlot, int kPart, int kParts>
 __device__ __forceinline__ void multiply_scores(const Operands &o)
 {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
+    for (int i = kPart * kChunks / kParts; i < (kPart + 1) * kChunks / kParts; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             mma_bf16(o.tmem + kScoresAt + kSlot * kTileKeys, o.query + (i * kRows * 128 + 32 * k),
@@ -623,12 +642,13 @@ __device__ __forceinline__ void multiply_scores(const Operands &o)
                      o.elected);
 }
 
-// the second
-template <int kSlot, int kProbSlot>
+// and of the dims of the second
+template <int kSlot, int kProbSlot, int kPart, int kParts>
 __device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst, bool first)
 {
+    constexpr int kBlocks = kChunks / 2;
 #pragma unroll
-    for (int i = 0; i < kChunks / 2; ++i)
+    for (int i = kPart * kBlocks / kParts; i < (kPart + 1) * kBlocks / kParts; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             mma_bf16(o.tmem + i * kRows, o.values + (kSlot * kTileBytes + 2 * i * kChunkBytes + 2048 * k),
@@ -640,6 +660,7 @@ __device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst
 template <bool kFp8>
 __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
+    constexpr int kParts = Kind<kFp8>::parts;
     Operands o;
     o.keys = operand(smem + kKeys, 16, 1024);
     o.query = operand(smem + kQuery, 16, 1024);
@@ -658,8 +679,13 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
     const auto multiply_pending = [&](auto slot) {
         constexpr int kSlot = decltype(slot)::value;
         tmem_fence_after();
-        multiply_values<kSlot, kFp8 ? 0 : kSlot>(o, inst, begins);
-        mma_commit(&s.free[kSlot], o.elected);
+        fence_proxy_async_smem();
+        multiply_values<kSlot, kFp8 ? 0 : kSlot, 0, kParts>(o, inst, begins);
+        mma_commit(&s.free[kSlot][0], o.elected);
+        if constexpr (kParts == 2) {
+            multiply_values<kSlot, kFp8 ? 0 : kSlot, 1, kParts>(o, inst, begins);
+            mma_commit(&s.free[kSlot][1], o.elected);
+        }
         if (ends)
             mma_commit(&s.output, o.elected);
         pending = false;
@@ -668,15 +694,27 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
     const auto step = [&](auto slot) {
         constexpr int kSlot = decltype(slot)::value;
         constexpr std::integral_constant<int, 1 - kSlot> other;
-        const long long since = clock64();
-        while (!ready(&s.full[kSlot], (t >> 1) & 1) || (first && !ready(&s.query, segment & 1))) {
-            if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
-                multiply_pending(other);
-            else if (__any_sync(kFull, clock64() - since > kWaitCycles))
+        const auto rows_ready = [&](int part) {
+            const long long since = clock64();
+            while (!ready(&s.full[kSlot][part], (t >> 1) & 1) || (part == 0 && first && !ready(&s.query, segment & 1))) {
+                if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
+                    multiply_pending(other);
+                else if (__any_sync(kFull, clock64() - since > kWaitCycles))
+                    return false;
+            }
+            tmem_fence_after();
+            if constexpr (!kFp8)
+                fence_proxy_async_smem();
+            return true;
+        };
+        if (!rows_ready(0))
+            return false;
+        multiply_scores<kSlot, 0, kParts>(o);
+        if constexpr (kParts == 2) {
+            if (!rows_ready(1))
                 return false;
+            multiply_scores<kSlot, 1, kParts>(o);
         }
-        tmem_fence_after();
-        multiply_scores<kSlot>(o);
         mma_commit(&s.scores[kSlot], o.elected);
         const bool last = c.ends_segment();
         if (last)
@@ -892,7 +930,7 @@ if constexpr (!kFp8) {
                 over = fmaxf(over, v[j]);
         if (named_barrier_any(1, 256, failed || over > kSlack)) {
             if (!first)  // the second product of the tile before is done with O
-                failed = !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1) || failed;
+                failed = !mbar_wait(&s.free[(t - 1) & 1][Kind<kFp8>::parts - 1], ((t - 1) >> 1) & 1) || failed;
             if (named_barrier_any(1, 256, failed)) {
                 flag(a.b.err, DSV4_DEVERR_TIMEOUT);
                 return;
@@ -951,7 +989,7 @@ if constexpr (!kFp8) {
             packed[j] = bf16x2_rn(a0, a1);
             packed[j + 1] = bf16x2_rn(b0, b1);
         }
-        if (Kind<kFp8>::prob_slots == 1 && t > 0 && !mbar_wait(&s.free[(t - 1) & 1], ((t - 1) >> 1) & 1)) {
+        if (Kind<kFp8>::prob_slots == 1 && t > 0 && !mbar_wait(&s.free[(t - 1) & 1][Kind<kFp8>::parts - 1], ((t - 1) >> 1) & 1)) {
             // (P of the tile before was not taken; the others of the CTA run out of time as well)
             flag(a.b.err, DSV4_DEVERR_TIMEOUT);
         }
@@ -961,7 +999,6 @@ if constexpr (!kFp8) {
             store_shared4(p_at + swizzled(r, 4 * half + j), packed[2 * j]);
             store_shared4(p_at + swizzled(r + 8, 4 * half + j), packed[2 * j + 1]);
         }
-        fence_proxy_async_smem();
         tmem_fence_before();
         __syncwarp();
         if (lane == 0)
@@ -1069,8 +1106,11 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         tmem_alloc512(&s.tmem);
         if ((threadIdx.x & 31) == 0) {
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&s.free[i], 1);
-                mbar_init(&s.full[i], Kind<kFp8>::row_warps);
+                for (int h = 0; h < Kind<kFp8>::parts; ++h) {
+                    mbar_init(&s.free[i][h], 1);
+                    // bf16: each thread when its copies have landed, too
+                    mbar_init(&s.full[i][h], Kind<kFp8>::row_warps * (kFp8 ? 1 : 33));
+                }
                 mbar_init(&s.scores[i], 1);
                 mbar_init(&s.probs[i], kSoftmaxWarps);
             }
