@@ -656,7 +656,7 @@ __device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst
 }
 
 // Tile t's first product runs as soon as its rows are there, the second one of tile t - 1 as soon as
-// its P is there, whichever is first.  (In a fixed order each waited for the other's operands.)
+// its P is there, whichever is first, and the second if both are.  (In a fixed order each waited for the other's operands.)
 template <bool kFp8>
 __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
@@ -696,9 +696,12 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
         constexpr std::integral_constant<int, 1 - kSlot> other;
         const auto rows_ready = [&](int part) {
             const long long since = clock64();
-            while (!ready(&s.full[kSlot][part], (t >> 1) & 1) || (part == 0 && first && !ready(&s.query, segment & 1))) {
+            for (;;) {
                 if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
                     multiply_pending(other);
+                else if (ready(&s.full[kSlot][part], (t >> 1) & 1) &&
+                         (part != 0 || !first || ready(&s.query, segment & 1)))
+                    break;
                 else if (__any_sync(kFull, clock64() - since > kWaitCycles))
                     return false;
             }
