@@ -57,6 +57,7 @@ __device__ __forceinline__ int length_of(const PagedBatch &b, int r)
 constexpr int kDealThreads = 512;
 constexpr int kDealWarps = kDealThreads / 32;
 constexpr int kDealWords = 4 * kDealWarps + 4;
+static_assert(kDealWarps <= 32, "a lane has a warp's sums");
 
 // kStartCost: start_cost() below.  kTrees: the arguments may hold trees of drafted tokens.
 template <int kKeys, int kStartCost, bool kTrees>
@@ -171,16 +172,12 @@ struct KeyTiles {
                 sums[kDealWarps + warp] = units_upto;
             }
             __syncthreads();
-            all = units_all = 0;
-#pragma unroll
-            for (int w = 0; w < kDealWarps; ++w) {
-                if (w < warp) {
-                    upto += sums[w];
-                    units_upto += sums[kDealWarps + w];
-                }
-                all += sums[w];
-                units_all += sums[kDealWarps + w];
-            }
+            const int tiles = lane < kDealWarps ? sums[lane] : 0;
+            const int with_tiles = lane < kDealWarps ? sums[kDealWarps + lane] : 0;
+            all = __reduce_add_sync(kFull, tiles);
+            units_all = __reduce_add_sync(kFull, with_tiles);
+            upto += __reduce_add_sync(kFull, lane < warp ? tiles : 0);
+            units_upto += __reduce_add_sync(kFull, lane < warp ? with_tiles : 0);
             half ^= 1;
         };
         int total = 0, units = 0;
