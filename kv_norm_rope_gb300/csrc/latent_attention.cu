@@ -16,16 +16,36 @@
 //    measurement an instruction with 64 x 64 results takes 32 cycles, one with 128 x 64 takes
 //    48 (6 KB of operands at 128 bytes a cycle): 1024 and 768 cycles a tile, and 512 more of
 //    shared memory's time to write the rows.
-//  * Warps 8..23 load: a warp has 4 keys of each tile, one row a load instruction, in
-//    registers while the tile before is computed; a row becomes bf16 on its way to shared memory.
-//    One tile of bytes is in flight a SM.
 //  * Warps 0..7 do the softmax: a warp has 16 rows and half of the keys; what a row needs
 //    (its reference, sum, range, tree bits) is in the registers of 8 threads.
+//  * The warps from 8 on bring the rows: 16 that convert FP8 rows, 8 that copy bf16 rows.
+//  * The last four: one issues the products, one notes what the run leaves for the join
+//    (run_join.cuh), one copies queries, one finds where FP8 rows are.
 //  * The softmax needs no maximum per tile.  Each row has a reference m, the largest score of
 //    the first tile it saw; p = 2^(x - m) is taken against that, and only when some x exceeds m
 //    by more than kSlack is m moved and everything rescaled (fp32 and bf16 have the same
 //    range, so a p of 2^kSlack loses nothing).  Sums stay per thread, in fp32, until the segment ends.
-//  * Warp 24 issues the products, warp 25 notes what the run leaves for the join (run_join.cuh).
+//
+// What it takes (with the results joined), and what bounds it:
+//  * 128 requests of 1024 to 8192 FP8 keys, 128 heads: 251 us, 577 TFLOP/s; 32 requests of up to 4096,
+//    16 drafted tokens of 64 heads: 302 us.  About 3900 cycles a tile.  Counters give the data pipe of
+//    shared memory 91% busy (42% the products' operands, 49% loads and stores) and 60% of all issue
+//    slots: each row tile converts its keys for itself.
+//  * 6 requests of up to 4096 bf16 keys in a window, 61 drafted tokens of 128 heads: 616 us, 529 TFLOP/s;
+//    one of 262147 keys, 128 heads: 108.6 us.  About 3100 cycles a tile: a tile's copy, product, softmax
+//    and product follow one another, with two tiles to fill the gaps.
+//  * 48 requests of up to 4096 FP8 keys, 64 heads: 37.4 us in a graph, two requests of 130 keys: 12.5 us.
+//    A run's first product comes after 9000 to 14000 cycles (the deal, the lengths, tables, rows and
+//    queries, one load behind the other), a whole row tile's results take 7500, a part's 4200.
+//
+// Slower, each beside the best of its time (us, the first case unless another is named):
+//  * 8 converting warps of 8 keys, all rows in registers: 311 to 252; 16 warps so: 259;
+//  * two teams of converting warps, each with every second tile: 308 to 264;
+//  * pairs of CTAs that convert half a tile each for both: 386 by remote stores, 296 by bulk copies, to 264;
+//  * the FP8 tile in two halves like the bf16 one: 286 to 257;
+//  * the next kernel let in from the start: 39.8 to 38.2 for the 48 requests;
+//  * rows put in L2 by the copy unit; the two products in a fixed order.
+// Without the look at the codes for NaN it was 247 to 260, and without any conversion 232.
 //
 // A key whose row is not finite may be masked for some rows of the tile, and 0 times an
 // infinity is NaN in the second product.  So such a row enters the operands as zeros and the key
@@ -229,6 +249,7 @@ __device__ __forceinline__ void computed(uint4 &v)
 // into each lane's own bytes), those of the fourth and the rope dims in registers: what is on its way
 // to registers takes lines of the L1 that shared memory leaves, about 28 KB, and a load that
 // finds none waits.  Where the rows are, one warp finds for all, and puts them on their way to L2.
+// Rows on 16-byte boundaries have a kernel of their own: chosen at each load it took 264 us, not 256.
 
 constexpr int kWarpKeys = 4, kRingRows = 3;
 
@@ -487,12 +508,15 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
 
 // ---- bf16 rows into operands: warps 8..15, a warp 8 keys of each tile
 //
-// Copied as they are, asynchronously, half a row an instruction.  (By the copy unit, in boxes of up to 64
-// rows, a tile took no less: its copies wait for the products' use of shared memory as these
-// do.  Gathering single rows it took 3400 cycles a tile.)  A tile that is not seen whole by all rows
-// of the unit, or lacks keys, is looked through for rows that are not finite; in a tile that every
-// row sees whole, such a row makes scores that are not finite in every row of S, and the softmax
-// makes NaN of those.
+// Copied as they are, asynchronously, half a row an instruction.  The halves of the dims are filled and
+// freed apart, so that the first product begins on one while the other is on its way, and the copies
+// arrive at the tile's barrier by themselves (together 653 us to 626 for wide trees).  By the copy unit, in
+// boxes of up to 64 rows, a tile took no less: its copies wait for the products' use of shared
+// memory as these do.  Gathering single rows it took 3400 cycles a tile.
+//
+// A tile that is not seen whole by all rows of the unit, or lacks keys, is looked through for rows
+// that are not finite; in a tile that every row sees whole, such a row makes scores that are not
+// finite in every row of S, and the softmax makes NaN of those.
 
 // the keys that all rows of the unit see, but those of tokens that see nothing
 __device__ __forceinline__ Tiles::Range whole_range(const AParams &p, const Cursor &c)
@@ -655,6 +679,9 @@ __device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst
                      o.probs + (kProbSlot * kProbBytes + 32 * k), inst, !first || k > 0, o.elected);
 }
 
+// What other threads wrote of P and of bf16 rows is ordered before the products here, by one fence after
+// the barrier; a writer's own, before it, waits for the writer's loads as well.
+//
 // Tile t's first product runs as soon as its rows are there, the second one of tile t - 1 as soon as
 // its P is there, whichever is first, and the second if both are.  (In a fixed order each waited for the other's operands.)
 template <bool kFp8>
@@ -899,7 +926,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
                 v[j + 2] = __fmaf_rn(v[j + 2], scale, -ref1);
                 v[j + 3] = __fmaf_rn(v[j + 3], scale, -ref1);
             }
-if constexpr (!kFp8) {
+            if constexpr (!kFp8) {
                 // an infinite score is one of a row that is not finite, or of a sum outside fp32
                 float least = v[0];
 #pragma unroll

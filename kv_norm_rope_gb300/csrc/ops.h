@@ -99,7 +99,9 @@ struct Fp4EvictArgs {
 };
 
 // Keys in a tile of the attention over the FP8 and bf16 caches, and the positions that
-// beginning a row tile takes on its line.
+// beginning a row tile takes on its line: with 0, 2, 3, 4, 6 and 8 of them 48 requests of up to 4096
+// FP8 keys took 47, 41, 41, 40, 41 and 42 us, 128 of up to 8192 275, 265, 264, 264, 267 and 269, and 32 with
+// 16 drafted tokens 352, 311, 304, 308, 314 and 317.
 constexpr int kLatentTileKeys = 64;
 constexpr int kLatentStartCost = 4;
 
