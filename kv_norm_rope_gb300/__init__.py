@@ -571,12 +571,14 @@ def _check_rows(name: str, t, kind: str, batch: int) -> tuple:
     contiguous and may be further apart than they are long."""
     if t.dtype not in _kinds()[kind]:
         raise TypeError(f"{name}: expected {kind} data, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != batch:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != batch:
         raise ValueError(f"{name}: expected one row for each of {batch} requests, got "
-                         f"{tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or batch > 1 and t.stride(0) < t.shape[1]:
+                         f"{tuple(shape)}")
+    (stride, inner), width = t.stride(), shape[1]
+    if width > 1 and inner != 1 or batch > 1 and stride < width:
         raise ValueError(f"{name}: its rows must be contiguous and apart")
-    return (t.stride(0) if batch > 1 else t.shape[1]), t.shape[1]
+    return (stride if batch > 1 else width), width
 
 
 _CACHE_BYTES = {STORE_BF16: bf16_cache_bytes, STORE_FP4: fp4_cache_bytes, STORE_INDEXER: indexer_cache_bytes}
@@ -587,9 +589,10 @@ def _cache_bytes(store_mode, num_blocks, block_size):
 
 
 def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens, store_mode=STORE_FP4):
-    if q.dim() != 4 or q.shape[3] != 512:
-        raise ValueError(f"q: expected [batch, q_len, heads, 512], got {tuple(q.shape)}")
-    B, Q, H, _ = q.shape
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != 512:
+        raise ValueError(f"q: expected [batch, q_len, heads, 512], got {tuple(shape)}")
+    B, Q, H, _ = shape
     _check("q", q, "bf16")
     _check("kv_cache", kv_cache, "bytes", min_bytes=_cache_bytes(store_mode, num_blocks, block_size))
     _check("seq_lens", seq_lens, "i32", B)
