@@ -4,6 +4,8 @@
     python bench.py [--gpus N] [--steps K] [--warmup W] [--workload stress]
     python bench.py --impl reference ...      # the CPU oracle on a bounded sample
     python bench.py --op fp4 --case attention_long   # a case of the 4-bit cache
+    python bench.py --op drafts --case tree_verify   # of attention over the FP8 and bf16 caches, drafted
+                                                     # trees, rotary tables and rows
 
 A step is one pass of the whole fused step (one launch) over one batch: by default
 the "stress" workload, 131072 tokens x 128 q heads (q is 17.2 GB of bf16), FP8 cache
@@ -1123,14 +1125,18 @@ def run_ours(args):
     return 0
 
 
-def run_fp4(args):
-    """One case of perf/operators.py through the package's entry points: the median over
+CASE_FILES = {"fp4": "operators", "drafts": "more_operators"}  # of perf/
+
+
+def run_case(args):
+    """One case of a file of perf/ through the package's entry points: the median over
     K passes of the time between events around a pass, each after a write larger than L2
     (which also lets the host run ahead of the device)."""
+    import importlib
+
     import torch
 
-    from perf import operators
-
+    operators = importlib.import_module("perf." + CASE_FILES[args.op])
     cases = {c["name"]: c for c in operators.listed()}
     if args.case not in cases:
         raise SystemExit("--case must be one of " + ", ".join(cases))
@@ -1157,7 +1163,7 @@ def run_fp4(args):
         "metric": "us a pass, cold L2", "value": us, "unit": "us", "higher_is_better": False,
         "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "data": "synthetic",
         "gbs": work["bytes"] / us / 1e3, "tflops": work["flops"] / us / 1e6,
-        "config": {"op": "fp4", "case": case, "l2": f"{FP4_FLUSH_BYTES >> 20} MB written before each pass"},
+        "config": {"op": args.op, "case": case, "l2": f"{FP4_FLUSH_BYTES >> 20} MB written before each pass"},
         "clocks": clocks}), flush=True)
     return 0
 
@@ -1171,14 +1177,15 @@ def main(argv=None):
     ap.add_argument("--workload", choices=sorted(configs.WORKLOADS), default="stress")
     ap.add_argument("--variant", choices=sorted(VARIANTS), default="auto",
                     help="launch variant of the fused op (default: the library's choice)")
-    ap.add_argument("--op", choices=OPS + ("fp4",), default="fused",
+    ap.add_argument("--op", choices=OPS + tuple(CASE_FILES), default="fused",
                     help="fused (default); prenorm: KV arrives normalised; kv_only: no q; "
                          "gather: read the FP8 cache back out; mxfp8: residual add + Gemma "
                          "RMSNorm + MXFP8 of [T, 7168] activation rows; indexer: indexer-K "
                          "quant-insert of [T, 128] rows; indexer_gather: read them back out; "
-                         "fp4: a case of the 4-bit cache (--case)")
+                         "fp4: a case of the 4-bit cache (--case); drafts: one of attention over the FP8 "
+                         "and bf16 caches, drafted trees, rotary tables and rows (--case)")
     ap.add_argument("--case", default="attention_decode",
-                    help="case of --op fp4, by its name in perf/operators.py")
+                    help="case of --op fp4 or drafts, by its name in perf/operators.py or perf/more_operators.py")
     ap.add_argument("--hidden", type=int, default=MXFP8_HIDDEN,
                     help="row width of --op mxfp8 (a multiple of 128 up to 16384)")
     ap.add_argument("--tokens", type=int, default=0,
@@ -1193,10 +1200,10 @@ def main(argv=None):
     args = ap.parse_args(argv)
     if args.warmup < 3:
         ap.error("--warmup must be at least 3")
-    if args.op == "fp4":
+    if args.op in CASE_FILES:
         if args.impl == "reference" or args.gpus != 1 or dist_env()[1] != 1:
-            ap.error("--op fp4 runs this library on one GPU")
-        return run_fp4(args)
+            ap.error(f"--op {args.op} runs this library on one GPU")
+        return run_case(args)
     if args.impl == "reference":
         return run_reference(args)
     return run_ours(args)

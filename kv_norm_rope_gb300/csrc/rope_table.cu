@@ -10,10 +10,10 @@
 // 2^-40), and cos a and sin a are pairs of floats.  What is rounded before the last addition is
 // below 2^-5 of the result's largest, so entries are within 0.6 steps of 1.
 //
-// Bound by its stores (8 bytes a pair): 1048576 rows of 64 columns take 46 us (87% of a copy's rate),
-// 52 with positions given in any order, where the points' loads meet in banks.  CTAs an SM, each
-// with its part of the rows: 2 took 45 and 72 us, 3 45.5 and 58, 8 51 and 64; without the next row's
-// position on its way meanwhile 4 took 61 for given ones.
+// Bound by its stores (8 bytes a pair): 1048576 rows of 64 columns take 40.8 us (98% of a copy's rate),
+// 52 with positions given in any order.  With one copy of the points instead of eight their loads met in
+// banks (46 us).  CTAs an SM, each with its part of the rows: 2 take 40 and 72 us, 3 41 and 58, 6 40 and
+// 49 but more where the table is small (100000 rows: 6.6 by 4, 7.1 by 6).
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -48,9 +48,10 @@ static_assert(sizeof(TableParams) <= 4000, "kernel parameters");
 template <int kPairs>
 __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ TableParams p)
 {
-    __shared__ float4 points[kPoints];
-    if (threadIdx.x < kPoints)
-        points[threadIdx.x] = p.points[threadIdx.x];
+    // eight copies, each in its own banks: no two lanes that load at once meet in one
+    __shared__ float4 points[kPoints * 8];
+    for (int i = threadIdx.x; i < kPoints * 8; i += kTableThreads)
+        points[i] = p.points[i >> 3];
     __syncthreads();
     wait_for_kernel_before();
     const uint32_t groups = uint32_t(p.pairs) / kPairs, rows = kTableThreads / groups;
@@ -67,8 +68,10 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
     const auto position = [&](int64_t row) {
         if (p.positions == nullptr)
             return p.first + row;
-        return row < p.count ? ldg_i64_in(p.positions + row, Span{p.positions, uint64_t(p.count) * 8u}, p.err)
-                             : int64_t(0);
+        if (row >= p.count)
+            return int64_t(0);
+        const uint2 v = ldg8_now_in(p.positions + row, Span{p.positions, uint64_t(p.count) * 8u}, p.err);
+        return int64_t(uint64_t(v.y) << 32 | v.x);
     };
     int64_t next = position(int64_t(blockIdx.x) * rows + local);
     for (int64_t row = int64_t(blockIdx.x) * rows + local; row < p.count; row += step) {
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
             const float b = float(rest) * (6.283185307179586f * 0x1p-39f), b2 = b * b;
             const float sin_b = __fmaf_rn(b * b2, __fmaf_rn(b2, 1.0f / 120.0f, -1.0f / 6.0f), b);
             const float cos_b1 = b2 * __fmaf_rn(b2, 1.0f / 24.0f, -0.5f);
-            const float4 a = points[point & (kPoints - 1)];
+            const float4 a = points[(point & (kPoints - 1)) * 8 + (threadIdx.x & 7)];
             c[k] = a.x + __fmaf_rn(-a.z, sin_b, __fmaf_rn(a.x, cos_b1, a.y));
             s[k] = a.z + __fmaf_rn(a.x, sin_b, __fmaf_rn(a.z, cos_b1, a.w));
         }
