@@ -510,10 +510,9 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
 //
 // Copied as they are, asynchronously, half a row an instruction.  The halves of the dims are filled and
 // freed apart, so that the first product begins on one while the other is on its way, and the copies
-// arrive at the tile's barrier by themselves (together 653 us to 626 for wide trees; in quarters it
-// took 735).  By the copy unit, in
-// boxes of up to 64 rows, a tile took no less: its copies wait for the products' use of shared
-// memory as these do.  Gathering single rows it took 3400 cycles a tile.
+// arrive at the tile's barrier by themselves (together 653 us to 626 for wide trees; in quarters
+// it took 735).  By the copy unit, in boxes of up to 64 rows, a tile took no less: its copies wait for the
+// products' use of shared memory as these do.  Gathering single rows it took 3400 cycles a tile.
 //
 // A tile that is not seen whole by all rows of the unit, or lacks keys, is looked through for rows
 // that are not finite; in a tile that every row sees whole, such a row makes scores that are not
