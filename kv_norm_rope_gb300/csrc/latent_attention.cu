@@ -44,6 +44,8 @@
 //  * pairs of CTAs that convert half a tile each for both: 386 by remote stores, 296 by bulk copies, to 264;
 //  * the FP8 tile in two halves like the bf16 one: 286 to 257;
 //  * the next kernel let in from the start: 39.8 to 38.2 for the 48 requests;
+//  * three bf16 tiles of 48 keys in flight: 665 to 616 for the trees (what lands waits for the products'
+//    operands, and 48 keys a product take 28 cycles to 32 of 64);
 //  * rows put in L2 by the copy unit; the two products in a fixed order.
 // Without the look at the codes for NaN it was 247 to 260, and without any conversion 232.
 //
