@@ -40,7 +40,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_VALUE, ERR_CUDA = range(6)
 DEVERR_SLOT_RANGE, DEVERR_POS_RANGE, DEVERR_TIMEOUT, DEVERR_BOUNDS = 1, 2, 4, 8
 STORE_FP8, STORE_BF16, STORE_FP4, STORE_INDEXER = range(4)
 VARIANT_AUTO, VARIANT_SMALL, VARIANT_STREAM, VARIANT_HALF = 0, 1, 2, 4
-FP8_SLOT_BYTES, BF16_SLOT_BYTES, FP4_SLOT_BYTES = 584, 1024, 368
+FP8_SLOT_BYTES, BF16_SLOT_BYTES, FP4_SLOT_BYTES, INDEXER_SLOT_BYTES = 584, 1024, 368, 132
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = range(4)  # scalings of the frequencies
 ROPE_PAIRS, ROPE_HALF = range(2)                         # layouts of the rotated dims
 
@@ -581,20 +581,13 @@ def _check_rows(name: str, t, kind: str, batch: int) -> tuple:
     return (stride if batch > 1 else width), width
 
 
-_CACHE_BYTES = {STORE_BF16: bf16_cache_bytes, STORE_FP4: fp4_cache_bytes, STORE_INDEXER: indexer_cache_bytes}
-
-
-def _cache_bytes(store_mode, num_blocks, block_size):
-    return _CACHE_BYTES.get(store_mode, fp8_cache_bytes)(num_blocks, block_size)
-
-
-def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens, store_mode=STORE_FP4):
+def _check_attention(q, kv_cache, num_blocks, block_size, block_table, seq_lens):
     shape = q.shape
     if len(shape) != 4 or shape[3] != 512:
         raise ValueError(f"q: expected [batch, q_len, heads, 512], got {tuple(shape)}")
     B, Q, H, _ = shape
     _check("q", q, "bf16")
-    _check("kv_cache", kv_cache, "bytes", min_bytes=_cache_bytes(store_mode, num_blocks, block_size))
+    _check("kv_cache", kv_cache, "bytes", min_bytes=fp4_cache_bytes(num_blocks, block_size))
     _check("seq_lens", seq_lens, "i32", B)
     return B, Q, H, _check_rows("block_table", block_table, "i32", B)
 
@@ -723,18 +716,55 @@ def latent_attention_workspace_bytes() -> int:
     return _latent_workspace_bytes
 
 
-def _launch(what: str, device, stream, call) -> None:
-    """call(stream handle) on ``device``, which need not be torch's current one."""
+def _placed(name: str, t, where: int) -> None:
+    """Refuse a tensor that is not on the device with the index ``where`` (-1: the host)."""
+    if t.get_device() != where:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        raise ValueError(f"{name}: on {t.device}, other tensor arguments on "
+                         f"{'the host' if where < 0 else f'cuda:{where}'}")
+
+
+def _address(name: str, t, kind: str, numel: int | None, where: int) -> int | None:
+    """The address of an argument: a tensor's, once it has passed _check and lies where the others do
+    (the host is refused at the launch), or the address or None that it is."""
+    if t is None or isinstance(t, int):
+        return t
+    allowed = (_kinds_table or _kinds())[kind]
+    if allowed is not None and t.dtype not in allowed or not t.is_contiguous() or \
+            numel is not None and t.numel() != numel:
+        _check(name, t, kind, numel)
+    if t.get_device() != where:
+        _placed(name, t, where)
+    return t.data_ptr()
+
+
+_SLOT_BYTES = {STORE_FP8: FP8_SLOT_BYTES, STORE_BF16: BF16_SLOT_BYTES, STORE_FP4: FP4_SLOT_BYTES,
+               STORE_INDEXER: INDEXER_SLOT_BYTES}
+
+
+def _cache_address(t, store_mode: int, num_blocks: int, block_size: int, where: int) -> int | None:
+    if t is not None and not isinstance(t, int) and num_blocks > 0 and block_size > 0:
+        need = num_blocks * block_size * _SLOT_BYTES.get(store_mode, 0)
+        if t.numel() * t.element_size() < need:
+            _check("kv_cache", t, "bytes", min_bytes=need)
+    return _address("kv_cache", t, "bytes", None, where)
+
+
+def _launch(what: str, where: int, stream, entry, *args) -> None:
+    """entry(*args, stream handle) on the device with this index, which need not be torch's current one."""
     import torch
-    if not isinstance(stream, int) and stream is not None and stream.device != device:
-        raise ValueError(f"stream: on {stream.device}, the tensors on {device}")
+    if where < 0:
+        raise ValueError(f"{what}: tensor arguments must be CUDA tensors (there is no CPU path)")
+    if stream is not None and not isinstance(stream, int) and stream.device.index != where:
+        raise ValueError(f"stream: on {stream.device}, the tensors on cuda:{where}")
     current = torch.cuda.current_device()
-    if device.index == current:
+    if where == current:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) if stream is None else None
-        st = call(raw(current) if raw is not None else _stream_handle(stream))
+        st = entry(*args, raw(current) if raw is not None else _stream_handle(stream))
     else:
-        with torch.cuda.device(device):
-            st = call(_stream_handle(stream))
+        with torch.cuda.device(where):
+            st = entry(*args, _stream_handle(stream))
     if st != OK:
         raise Dsv4Error(st, what)
 
@@ -752,25 +782,32 @@ def latent_attention(store_mode: int, q, kv_cache, num_blocks: int, block_size: 
     token that is padding.  workspace: uint8 of latent_attention_workspace_bytes(), or the address
     of that many; None takes one from torch's allocator for the call, on ``stream``, which is
     then torch's current one, or a torch stream."""
-    B, Q, H, (stride, width) = _check_attention(q, kv_cache, num_blocks, block_size, block_table,
-                                                seq_lens, store_mode)
-    _check("out", out, "bf16", q.numel())
-    _check("lse", lse, "f32", B * Q * H)
-    _check("sinks", sinks, "f32", H)
-    _check("tree", tree, "i64", B * Q)
-    _check("device_error", device_error, "i32")
-    workspace_bytes = latent_attention_workspace_bytes()
+    shape, where = q.shape, q.get_device()
+    if len(shape) != 4 or shape[3] != 512:
+        raise ValueError(f"q: expected [batch, q_len, heads, 512], got {tuple(shape)}")
+    B, Q, H, _ = shape
+    rows = B * Q * H
+    q_at = _address("q", q, "bf16", None, where)
+    cache_at = _cache_address(kv_cache, store_mode, num_blocks, block_size, where)
+    lens_at = _address("seq_lens", seq_lens, "i32", B, where)
+    stride, width = _check_rows("block_table", block_table, "i32", B)
+    out_at = _address("out", out, "bf16", rows * 512, where)
+    lse_at = _address("lse", lse, "f32", rows, where)
+    sinks_at = _address("sinks", sinks, "f32", H, where)
+    tree_at = _address("tree", tree, "i64", B * Q, where)
+    error_at = _address("device_error", device_error, "i32", None, where)
+    workspace_bytes = _latent_workspace_bytes or latent_attention_workspace_bytes()
     if workspace is None:
         workspace = _workspace(workspace_bytes, q.device, stream)
-    elif not isinstance(workspace, int):
-        _check("workspace", workspace, "bytes")
-        workspace_bytes = workspace.numel() * workspace.element_size()
-    _on_cuda(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse,
-             sinks=sinks, tree=tree, workspace=workspace, device_error=device_error)
-    _launch("dsv4_latent_attention", q.device, stream, lambda handle: lib().dsv4_latent_attention(
-        store_mode, q.data_ptr(), _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride,
-        width, _ptr(seq_lens), B, Q, H, scale, _int32(window), _ptr(tree), _ptr(sinks), _ptr(out),
-        _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(device_error), handle))
+        workspace_at = workspace.data_ptr()
+    else:
+        if not isinstance(workspace, int):
+            workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace_at = _address("workspace", workspace, "bytes", None, where)
+    _placed("block_table", block_table, where)
+    _launch("dsv4_latent_attention", where, stream, lib().dsv4_latent_attention, store_mode, q_at, cache_at,
+            num_blocks, block_size, block_table.data_ptr(), stride, width, lens_at, B, Q, H, scale, _int32(window),
+            tree_at, sinks_at, out_at, lse_at, workspace_at, workspace_bytes, error_at)
 
 
 def tree_keep(store_mode: int, kv_cache, num_blocks: int, block_size: int, block_table, seq_lens, path,
@@ -782,19 +819,17 @@ def tree_keep(store_mode: int, kv_cache, num_blocks: int, block_size: int, block
     if path.dim() != 2:
         raise ValueError(f"path: expected [batch, q_len], got {tuple(path.shape)}")
     B, Q = path.shape
-    _check("kv_cache", kv_cache, "bytes", min_bytes=_cache_bytes(store_mode, num_blocks, block_size))
-    _check("seq_lens", seq_lens, "i32", B)
+    where = path.get_device()
+    cache_at = _cache_address(kv_cache, store_mode, num_blocks, block_size, where)
+    lens_at = _address("seq_lens", seq_lens, "i32", B, where)
     stride, width = _check_rows("block_table", block_table, "i32", B)
-    _check("path", path, "i32")
-    _check("path_lens", path_lens, "i32", B)
-    _check("new_seq_lens", new_seq_lens, "i32", B)
-    _check("device_error", device_error, "i32")
-    _on_cuda(kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, path=path, path_lens=path_lens,
-             new_seq_lens=new_seq_lens, device_error=device_error)
-    _launch("dsv4_tree_keep", path.device, stream, lambda handle: lib().dsv4_tree_keep(
-        store_mode, _ptr(kv_cache), num_blocks, block_size, block_table.data_ptr(), stride, width,
-        _ptr(seq_lens), B, Q, path.data_ptr(), _ptr(path_lens), _ptr(new_seq_lens), _ptr(device_error),
-        handle))
+    path_at = _address("path", path, "i32", None, where)
+    path_lens_at = _address("path_lens", path_lens, "i32", B, where)
+    new_at = _address("new_seq_lens", new_seq_lens, "i32", B, where)
+    error_at = _address("device_error", device_error, "i32", None, where)
+    _placed("block_table", block_table, where)
+    _launch("dsv4_tree_keep", where, stream, lib().dsv4_tree_keep, store_mode, cache_at, num_blocks, block_size,
+            block_table.data_ptr(), stride, width, lens_at, B, Q, path_at, path_lens_at, new_at, error_at)
 
 
 # ---- rotary positions
@@ -821,20 +856,30 @@ def rope_table(frequencies, out, positions=None, first: int = 0, magnitude: floa
     pairs = len(frequencies)
     if out.dim() != 2 or out.shape[1] != 2 * pairs:
         raise ValueError(f"out: expected [n, {2 * pairs}], got {tuple(out.shape)}")
-    _check("out", out, "f32")
-    _check("positions", positions, "i64", out.shape[0])
-    _check("device_error", device_error, "i32")
-    _on_cuda(out=out, positions=positions, device_error=device_error)
+    where = out.get_device()
+    out_at = _address("out", out, "f32", None, where)
+    positions_at = _address("positions", positions, "i64", out.shape[0], where)
+    error_at = _address("device_error", device_error, "i32", None, where)
     angles = (ctypes.c_double * pairs)(*frequencies)
-    _launch("dsv4_rope_table", out.device, stream, lambda handle: lib().dsv4_rope_table(
-        angles, 2 * pairs, magnitude, _ptr(positions), first, out.shape[0], out.data_ptr(),
-        _ptr(device_error), handle))
+    _launch("dsv4_rope_table", where, stream, lib().dsv4_rope_table, angles, 2 * pairs, magnitude, positions_at,
+            first, out.shape[0], out_at, error_at)
 
 
 def _row_strides(name: str, t):
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    strides = t.stride()
+    if strides[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: its innermost stride must be 1")
-    return (t.stride(0), t.stride(1)) if t.dim() == 3 else (t.stride(0), t.shape[1])
+    return strides[:2] if len(strides) == 3 else (strides[0], t.shape[1])
+
+
+_row_types = None
+
+
+def _find_row_types():
+    global _row_types
+    import torch
+    _row_types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    return _row_types
 
 
 def rope_rows(x, positions, cos_sin_cache, out=None, offset: int | None = None, inverse: bool = False,
@@ -844,28 +889,27 @@ def rope_rows(x, positions, cos_sin_cache, out=None, offset: int | None = None, 
     itself), d being the width of cos_sin_cache (fp32 [max_position, d]) and offset D - d (the
     trailing dims) unless given.  inverse: turned back, which is also the gradient's way.  layout:
     ROPE_PAIRS (neighbouring dims) or ROPE_HALF (i and i + d / 2)."""
-    import torch
-    types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    types = _row_types or _find_row_types()
     if out is None:
         out = x
     if x.dtype not in types:
         raise TypeError(f"x: expected bf16, fp16 or fp32 data, got {x.dtype}")
     if out.dtype != x.dtype:
         raise TypeError(f"out: expected {x.dtype} data, got {out.dtype}")
-    if x.dim() not in (2, 3) or out.shape != x.shape:
-        raise ValueError(f"x, out: expected [tokens, heads, width] of one shape, got {tuple(x.shape)} and "
+    shape, where = x.shape, x.get_device()
+    if len(shape) not in (2, 3) or out.shape != shape:
+        raise ValueError(f"x, out: expected [tokens, heads, width] of one shape, got {tuple(shape)} and "
                          f"{tuple(out.shape)}")
     if cos_sin_cache.dim() != 2:
         raise ValueError("cos_sin_cache: expected [max_position, d]")
     max_position, dim = cos_sin_cache.shape
-    T, H, D = x.shape[0], (x.shape[1] if x.dim() == 3 else 1), x.shape[-1]
-    _check("positions", positions, "i64", T)
-    _check("cos_sin_cache", cos_sin_cache, "f32")
-    _check("device_error", device_error, "i32")
-    _on_cuda(x=x, positions=positions, cos_sin_cache=cos_sin_cache, out=out, device_error=device_error)
+    T, H, D = shape[0], (shape[1] if len(shape) == 3 else 1), shape[-1]
+    positions_at = _address("positions", positions, "i64", T, where)
+    table_at = _address("cos_sin_cache", cos_sin_cache, "f32", None, where)
+    error_at = _address("device_error", device_error, "i32", None, where)
+    _placed("out", out, where)
     offset = D - dim if offset is None else offset
     x_strides, out_strides = _row_strides("x", x), _row_strides("out", out)
-    _launch("dsv4_rope_rows", x.device, stream, lambda handle: lib().dsv4_rope_rows(
-        types[x.dtype], x.data_ptr(), *x_strides, out.data_ptr(), *out_strides, T, H, D, _int32(offset), dim,
-        layout, 1 if inverse else 0, _ptr(positions), _ptr(cos_sin_cache), max_position, _ptr(device_error),
-        handle))
+    _launch("dsv4_rope_rows", where, stream, lib().dsv4_rope_rows, types[x.dtype], x.data_ptr(), *x_strides,
+            out.data_ptr(), *out_strides, T, H, D, _int32(offset), dim, layout, 1 if inverse else 0, positions_at,
+            table_at, max_position, error_at)
