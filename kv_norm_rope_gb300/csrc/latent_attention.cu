@@ -46,6 +46,8 @@
 //  * the next kernel let in from the start: 39.8 to 38.2 for the 48 requests;
 //  * three bf16 tiles of 48 keys in flight: 665 to 616 for the trees (what lands waits for the products'
 //    operands, and 48 keys a product take 28 cycles to 32 of 64);
+//  * half of the queries in tensor memory, so that the first product reads a quarter less of shared memory:
+//    269 to 252, and 613 to 614 for the trees;
 //  * rows put in L2 by the copy unit; the two products in a fixed order.
 // Without the look at the codes for NaN it was 247 to 260, and without any conversion 232.
 //
