@@ -160,3 +160,107 @@ def test_example_runs():
     from examples import tree_decode
     lens, x = tree_decode.main(steps=12, batch=3, heads=16, seed=0)
     assert all(n >= 12 for n in lens) and bool(torch.isfinite(x).all())
+
+
+def test_arguments_on_the_host_are_refused():
+    """Before anything is launched, and naming the one that is not on the device."""
+    q = torch.zeros(2, 1, 3, 512, dtype=torch.bfloat16, device=DEV)
+    cache = torch.zeros(k.fp8_cache_bytes(4, 16), dtype=torch.uint8, device=DEV)
+    table, lens = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+
+    def attend(**kw):
+        a = dict(q=q, cache=cache, table=table, lens=lens, out=torch.empty_like(q)) | kw
+        k.latent_attention(k.STORE_FP8, a["q"], a["cache"], 4, 16, a["table"], a["lens"], 1.0, a["out"],
+                           lse=kw.get("lse"), tree=kw.get("tree"))
+
+    attend()
+    for name, t in dict(cache=cache, table=table, lens=lens, out=q, lse=torch.zeros(2, 1, 3),
+                        tree=torch.ones(2, 1, dtype=torch.int64)).items():
+        with pytest.raises(ValueError, match=dict(cache="kv_cache", table="block_table", lens="seq_lens").get(name, name)):
+            attend(**{name: t.cpu()})
+    with pytest.raises(ValueError, match="host"):
+        attend(q=q.cpu())
+    path = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    for at in range(3):
+        moved = [t.cpu() if i == at else t for i, t in enumerate((table, lens, path))]
+        with pytest.raises(ValueError, match="CUDA|host"):
+            k.tree_keep(k.STORE_FP8, cache, 4, 16, moved[0], moved[1], moved[2], lens, lens)
+    x, positions = torch.zeros(3, 2, 8, device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV)
+    cos_sin = torch.zeros(4, 8, device=DEV)
+    for call in (lambda: k.rope_rows(x, positions.cpu(), cos_sin), lambda: k.rope_rows(x, positions, cos_sin.cpu()),
+                 lambda: k.rope_rows(x, positions, cos_sin, out=x.cpu()), lambda: k.rope_rows(x.cpu(), positions, cos_sin),
+                 lambda: k.rope_table((1.0, 0.5), torch.zeros(3, 4, device=DEV), positions=positions.cpu())):
+        with pytest.raises(ValueError, match="CUDA|host"):
+            call()
+    torch.cuda.synchronize()
+
+
+def test_host_threads_on_streams_of_their_own():
+    """Four threads that each run all of it, from the same inputs, against a serial run."""
+    import threading
+
+    servers = [Server("fp8" if i % 2 else "bf16", [70 + i, 9], 6, 5, seed=20 + i) for i in range(4)]
+    words = words_tensor([random_tree(s.rng, 6) for s in servers for _ in range(2)]).view(4, 2, 6)
+    queries = [s.randn(2, 6, 5, 512).bfloat16() for s in servers]
+    rows = [s.randn(12, 512).bfloat16() for s in servers]
+    images = [s.drafting.clone() for s in servers]
+
+    def run(i):
+        s = servers[i]
+        cache = images[i].clone()
+        at = [(b, s.lens[b] + j) for b in range(2) for j in range(6)]
+        positions = [s.lens[b] + j for b in range(2) for j in range(6)]
+        q = queries[i].clone()
+        s.insert(cache, q.view(12, 5, 512), rows[i], at, positions)
+        lens = dev([n + 6 for n in s.lens], np.int32)
+        out = s.attend(cache, q, lens, words[i])
+        k.rope_rows(out.view(12, 5, 512), dev(positions, np.int64), s.cos_sin, inverse=True)
+        path, path_lens = dev(np.array([[1, 3, 5, -1, -1, -1]] * 2), np.int32), dev([3, 2], np.int32)
+        k.tree_keep(STORES[s.store], cache, s.nb, BLOCK, s.table, lens, path, path_lens, lens)
+        return out, cache, lens
+
+    serial = [run(i) for i in range(4)]
+    torch.cuda.synchronize()
+    found = [[] for _ in range(4)]
+
+    def worker(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                found[i].append(run(i))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(4):
+        assert len(found[i]) == 5
+        for got in found[i]:
+            for one, other in zip(got, serial[i]):
+                assert torch.equal(one.view(torch.uint8), other.view(torch.uint8)), i
+
+
+@pytest.mark.parametrize("store", STORES)
+@pytest.mark.parametrize("lens", [[333, 390], [333, 700]])
+def test_a_chunk_of_a_prompt(store, lens):
+    """Hundreds of new tokens of a request at once, as a prompt's chunk, in a window too.  (Rows past the
+    400 positions of the table are not inserted: the tokens that see their slots get NaN.)"""
+    s = Server(store, lens, 1, 1, seed=31)
+    assert int(s.err.item()) == (k.DEVERR_POS_RANGE if max(lens) > POSITIONS else 0)
+    Q, H = 150, 5
+    lens = dev(s.lens, np.int32)
+    q = s.randn(2, Q, H, 512).bfloat16()
+    image, q64 = s.drafting.cpu().numpy(), q.double().cpu().numpy()
+    for window in (0, 90):
+        out = torch.empty_like(q)
+        k.latent_attention(STORES[store], q, s.drafting, s.nb, BLOCK, s.table, lens, SCALE, out, window=window)
+        out = out.double().cpu().numpy()
+        for b, n in enumerate(s.lens):
+            rows, ok = latent.rows_of(image, store, BLOCK, s.table_np[b], n, s.nb)
+            want, _, size, reach = latent.attention(q64[b], rows, ok, n, SCALE, window)
+            ds = SCALE * reach * 2.0 ** -15 + 2.0 ** -18
+            near = np.abs(out[b] - want) <= np.abs(want) * 2.0 ** -8 + size * (2.0 ** -8 + 2 * ds[..., None])
+            assert np.all(near | (np.isnan(want) & np.isnan(out[b])))
+            assert np.array_equal(np.isnan(want), np.isnan(out[b])) and (n > POSITIONS or not np.isnan(want).any())
