@@ -31,8 +31,8 @@
 //    16 drafted tokens of 64 heads: 302 us.  About 3900 cycles a tile.  Counters give the data pipe of
 //    shared memory 91% busy (42% the products' operands, 49% loads and stores) and 60% of all issue
 //    slots: each row tile converts its keys for itself.
-//  * 6 requests of up to 4096 bf16 keys in a window, 61 drafted tokens of 128 heads: 616 us, 529 TFLOP/s;
-//    one of 262147 keys, 128 heads: 108.6 us.  About 3100 cycles a tile: a tile's copy, product, softmax
+//  * 6 requests of up to 4096 bf16 keys in a window, 61 drafted tokens of 128 heads: 602 us, 541 TFLOP/s;
+//    one of 262147 keys, 128 heads: 106 us.  About 3000 cycles a tile: a tile's copy, product, softmax
 //    and product follow one another, with two tiles to fill the gaps.
 //  * 48 requests of up to 4096 FP8 keys, 64 heads: 37.4 us in a graph, two requests of 130 keys: 12.5 us.
 //    A run's first product comes after 9000 to 14000 cycles (the deal, the lengths, tables, rows and
@@ -725,13 +725,12 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
     const auto step = [&](auto slot) {
         constexpr int kSlot = decltype(slot)::value;
         constexpr std::integral_constant<int, 1 - kSlot> other;
-        const auto rows_ready = [&](int part) {
+        const auto rows_ready = [&] {
             const long long since = clock64();
             for (;;) {
                 if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
                     multiply_pending(other);
-                else if (ready(&s.full[kSlot][part], (t >> 1) & 1) &&
-                         (part != 0 || !first || ready(&s.query, segment & 1)))
+                else if (ready(&s.full[kSlot][0], (t >> 1) & 1) && (!first || ready(&s.query, segment & 1)))
                     break;
                 else if (__any_sync(kFull, clock64() - since > kWaitCycles))
                     return false;
@@ -741,12 +740,16 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
                 fence_proxy_async_smem();
             return true;
         };
-        if (!rows_ready(0))
+        if (!rows_ready())
             return false;
         multiply_scores<kSlot, 0, kParts>(o);
         if constexpr (kParts == 2) {
-            if (!rows_ready(1))
+            // (The pending product waits as well: with its code here once more wide trees took 613 us to 601, a long
+            // request 108 to 105.8.)
+            if (!warp_wait(&s.full[kSlot][1], (t >> 1) & 1))
                 return false;
+            tmem_fence_after();
+            fence_proxy_async_smem();
             multiply_scores<kSlot, 1, kParts>(o);
         }
         mma_commit(&s.scores[kSlot], o.elected);
