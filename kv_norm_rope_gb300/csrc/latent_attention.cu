@@ -687,7 +687,8 @@ __device__ __forceinline__ void multiply_values(const Operands &o, uint32_t inst
 // the barrier; a writer's own, before it, waits for the writer's loads as well.
 //
 // Tile t's first product runs as soon as its rows are there, the second one of tile t - 1 as soon as
-// its P is there, whichever is first, and the second if both are.  (In a fixed order each waited for the other's operands.)
+// its P is there, whichever is first, and the second if both are.  (In a fixed order each waited for the
+// other's operands.)  Each stands in the code once a slot: the warp fetches most of it anew for each tile.
 template <bool kFp8>
 __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor c)
 {
@@ -725,41 +726,42 @@ __device__ void multiply_role(const AParams &p, Shared &s, uint32_t smem, Cursor
     const auto step = [&](auto slot) {
         constexpr int kSlot = decltype(slot)::value;
         constexpr std::integral_constant<int, 1 - kSlot> other;
-        const auto rows_ready = [&] {
-            const long long since = clock64();
-            for (;;) {
-                if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
-                    multiply_pending(other);
-                else if (ready(&s.full[kSlot][0], (t >> 1) & 1) && (!first || ready(&s.query, segment & 1)))
+        bool last = false, issued = false;
+        long long since = clock64();
+        for (;;) {
+            if (pending && ready(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1)) {
+                multiply_pending(other);
+                if (issued)
                     break;
-                else if (__any_sync(kFull, clock64() - since > kWaitCycles))
+                since = clock64();
+            } else if (!issued && ready(&s.full[kSlot][0], (t >> 1) & 1) && (!first || ready(&s.query, segment & 1))) {
+                tmem_fence_after();
+                if constexpr (!kFp8)
+                    fence_proxy_async_smem();
+                multiply_scores<kSlot, 0, kParts>(o);
+                if constexpr (kParts == 2) {
+                    // (the pending product waits as well: with its code here too 613 us to 601 for wide trees)
+                    if (!warp_wait(&s.full[kSlot][1], (t >> 1) & 1))
+                        return false;
+                    tmem_fence_after();
+                    fence_proxy_async_smem();
+                    multiply_scores<kSlot, 1, kParts>(o);
+                }
+                mma_commit(&s.scores[kSlot], o.elected);
+                last = c.ends_segment();
+                if (last)
+                    mma_commit(&s.query_free, o.elected);
+                if (!pending)
+                    break;
+                issued = true;
+                // asleep until then beside the converting warps (298 us to 290 for drafted trees), polling beside
+                // copying ones (107.8 to 106.3 for a long request)
+                if (kFp8 && !warp_wait(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
                     return false;
+                since = clock64();
+            } else if (__any_sync(kFull, clock64() - since > kWaitCycles)) {
+                return false;
             }
-            tmem_fence_after();
-            if constexpr (!kFp8)
-                fence_proxy_async_smem();
-            return true;
-        };
-        if (!rows_ready())
-            return false;
-        multiply_scores<kSlot, 0, kParts>(o);
-        if constexpr (kParts == 2) {
-            // (The pending product waits as well: with its code here once more wide trees took 613 us to 601, a long
-            // request 108 to 105.8.)
-            if (!warp_wait(&s.full[kSlot][1], (t >> 1) & 1))
-                return false;
-            tmem_fence_after();
-            fence_proxy_async_smem();
-            multiply_scores<kSlot, 1, kParts>(o);
-        }
-        mma_commit(&s.scores[kSlot], o.elected);
-        const bool last = c.ends_segment();
-        if (last)
-            mma_commit(&s.query_free, o.elected);
-        if (pending) {
-            if (!warp_wait(&s.probs[1 - kSlot], ((t - 1) >> 1) & 1))
-                return false;
-            multiply_pending(other);
         }
         inst = instruction_of(128, uint32_t((c.row1 - c.row0 + 15) & ~15), true, false);
         begins = first;
