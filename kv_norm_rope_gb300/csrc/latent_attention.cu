@@ -28,10 +28,10 @@
 //
 // What it takes (with the results joined), and what bounds it:
 //  * 128 requests of 1024 to 8192 FP8 keys, 128 heads: 251 us, 577 TFLOP/s; 32 requests of up to 4096,
-//    16 drafted tokens of 64 heads: 302 us.  About 3900 cycles a tile.  Counters give the data pipe of
+//    16 drafted tokens of 64 heads: 290 us.  About 3900 cycles a tile.  Counters give the data pipe of
 //    shared memory 91% busy (42% the products' operands, 49% loads and stores) and 60% of all issue
 //    slots: each row tile converts its keys for itself.
-//  * 6 requests of up to 4096 bf16 keys in a window, 61 drafted tokens of 128 heads: 602 us, 541 TFLOP/s;
+//  * 6 requests of up to 4096 bf16 keys in a window, 61 drafted tokens of 128 heads: 594 us, 549 TFLOP/s;
 //    one of 262147 keys, 128 heads: 106 us.  About 3000 cycles a tile: a tile's copy, product, softmax
 //    and product follow one another, with two tiles to fill the gaps.
 //  * 48 requests of up to 4096 FP8 keys, 64 heads: 37.4 us in a graph, two requests of 130 keys: 12.5 us.
