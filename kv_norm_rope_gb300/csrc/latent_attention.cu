@@ -140,7 +140,9 @@ struct Shared {
     int scratch[kDealWords];
     float m[kRows];
     alignas(16) float factor[kRows];
-    float half_rows[2][kRows];  // maxima or sums over the keys of either half
+    // maxima and sums over the keys of either half: apart, for in a segment of one tile no barrier
+    // stands between the last look at the maxima and the sums
+    float half_max[2][kRows], half_sum[2][kRows];
     alignas(4) uint8_t state[2][kTileKeys];
     Cursor place[kSoftmaxWarps];
 };
@@ -985,13 +987,13 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
                 top1 = fmaxf(top1, __shfl_xor_sync(kFull, top1, d));
             }
             if ((lane & 3) == 0) {
-                s.half_rows[half][r] = top0;
-                s.half_rows[half][r + 8] = top1;
+                s.half_max[half][r] = top0;
+                s.half_max[half][r + 8] = top1;
             }
             named_barrier(1, 256);
             // (fmaxf takes the number of a NaN and a number)
-            const float new0 = fmaxf(m0, fmaxf(s.half_rows[0][r], s.half_rows[1][r]));
-            const float new1 = fmaxf(m1, fmaxf(s.half_rows[0][r + 8], s.half_rows[1][r + 8]));
+            const float new0 = fmaxf(m0, fmaxf(s.half_max[0][r], s.half_max[1][r]));
+            const float new1 = fmaxf(m1, fmaxf(s.half_max[0][r + 8], s.half_max[1][r + 8]));
             const float factor0 = exp2_approx(m0 - new0), factor1 = exp2_approx(m1 - new1);
             m0 = new0;
             m1 = new1;
@@ -1051,8 +1053,8 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
                 sum1 += __shfl_xor_sync(kFull, sum1, d);
             }
             if ((lane & 3) == 0) {
-                s.half_rows[half][r] = sum0;
-                s.half_rows[half][r + 8] = sum1;
+                s.half_sum[half][r] = sum0;
+                s.half_sum[half][r + 8] = sum1;
                 if (half == 0) {
                     s.m[r] = m0;
                     s.m[r + 8] = m1;
@@ -1073,7 +1075,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
             const Span ps = partial_span(w);
             if (threadIdx.x < kRows) {
                 const int i = threadIdx.x;
-                const float total = s.half_rows[0][i] + s.half_rows[1][i];
+                const float total = s.half_sum[0][i] + s.half_sum[1][i];
                 if (whole_range) {
                     float lse = 0.0f;
                     s.factor[i] = 1.0f;
@@ -1117,7 +1119,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
                 }
             }
             tmem_fence_before();
-            named_barrier(1, 256);  // m, factor and the halves' rows are free for the next segment
+            named_barrier(1, 256);  // m, factor and the halves' sums are free for the next segment
         }
         first = last;
         __syncwarp();
