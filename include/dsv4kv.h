@@ -602,7 +602,8 @@ int dsv4_tree_keep(int store_mode, void *kv_cache, int64_t num_blocks, int32_t b
  *   DSV4_ROPE_YARN    f_i (1 - r_i) + f_i / factor r_i, r_i rising from 0 to 1 between the pair that
  *                     makes turns_fast turns over original_positions and the one that makes
  *                     turns_slow (Peng et al., "YaRN", 2023; the ramp goes by the pair's index, its
- *                     ends rounded outwards).
+ *                     ends rounded outwards, and begins at pair 0 and ends at rope_dim - 1 at most:
+ *                     past the last pair where that makes more than turns_slow turns).
  * rope_dim even, 2 to 256; theta in (1, 10^12]; factor in [1, 10^6] (not looked at for PLAIN); the last
  * three for YARN only: positive, turns_fast > turns_slow.
  */

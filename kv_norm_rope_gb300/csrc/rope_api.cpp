@@ -81,7 +81,9 @@ int dsv4_rope_frequencies(int scaling, int32_t rope_dim, double theta, double fa
             return pairs * std::log(original_positions / (6.283185307179586476925 * turns)) / std::log(theta);
         };
         low = std::max(0.0, std::floor(pair_of(turns_fast)));
-        high = std::min(double(pairs - 1), std::ceil(pair_of(turns_slow)));
+        // (it may lie past the last pair: ended there, the ramp of 65536 positions and theta 10^4 would
+        // leave pair 31 of 32 with 0.30 of its frequency)
+        high = std::min(double(rope_dim - 1), std::ceil(pair_of(turns_slow)));
         high = std::max(high, low + 0.001);
     }
     for (int i = 0; i < pairs; ++i) {
