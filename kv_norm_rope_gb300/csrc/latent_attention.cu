@@ -441,11 +441,12 @@ __device__ __forceinline__ void convert_role(const AParams &p, Shared &s, KindSh
     int slot = 0, round = 0;  // of the tile's place
     for (int t = 0; alive && t < count; ++t) {
         // Converted before the wait for its place: that way only the stores stand between the product
-        // that frees it and the one that reads it.
+        // that frees it and the one that reads it.  (Lanes without codes take the last block's exponent:
+        // byte 7 of a scale row is padding and may hold anything.)
         uint32_t e[kWarpKeys];
 #pragma unroll
         for (int i = 0; i < kWarpKeys; ++i)
-            e[i] = reinterpret_cast<const uint8_t *>(&ks.exponents[slot][key0 + i])[lane < 28 ? lane >> 2 : 7];
+            e[i] = reinterpret_cast<const uint8_t *>(&ks.exponents[slot][key0 + i])[lane < 28 ? lane >> 2 : 6];
         const bool there = ks.row[slot][key0 + (lane & (kWarpKeys - 1))] != nullptr;
         copies_wait();
         uint4 first[kWarpKeys], second[kWarpKeys];
