@@ -619,7 +619,8 @@ int dsv4_rope_frequencies(int scaling, int32_t rope_dim, double theta, double fa
  * position below 2^32, values to 0.6 fp32 steps at the row's magnitude.
  *
  *  frequencies   (host) double [rope_dim / 2], in [0, 65536); read before the call returns.
- *  magnitude     0 or 2^-16 to 2^16 in absolute value (a stretched context's scale of q and k).
+ *  magnitude     0 or 2^-16 to 2^16 in absolute value (a stretched context's scale of q and k; what
+ *                was turned by such a table is turned back by one of 1 / magnitude, see dsv4_rope_rows).
  *  positions     (device, nullable) int64 [num_positions], 8-byte aligned.  One outside [0, 2^32)
  *                sets DSV4_DEVERR_POS_RANGE and its row is not written.
  *  first         >= 0, first + num_positions <= 2^32 (not looked at with positions).
@@ -633,9 +634,12 @@ int dsv4_rope_table(const double *frequencies, int32_t rope_dim, double magnitud
 /*
  * Rotation of rows: the pairs of dims [offset, offset + rope_dim) of every head of token t are turned by
  * the angles of row positions[t] of the table: (a, b) -> (a cos - b sin, b cos + a sin), or back,
- * (a cos + b sin, b cos - a sin), with inverse 1, which is also the gradient: that of x is the
- * inverse of the gradient of out.  An attention's output is turned back by its token's position: its
- * trailing dims are sums of rows that were turned by theirs.
+ * (a cos + b sin, b cos - a sin), with inverse 1.  With one table, of any magnitude, that is the
+ * transpose, and so the gradient: that of x is the gradient of out with inverse 1.  It undoes the
+ * rotation where the table's magnitude is 1; a rotation by a table of magnitude m (its cos and sin are m
+ * times those of the angles) is undone with one of magnitude 1 / m, while its own would give m^2 x.  An
+ * attention's output is turned back by its token's position: its trailing dims are sums of rows that
+ * were turned by theirs, and m times as large where the rows' table had a magnitude m.
  *
  *  type       DSV4_TYPE_BF16, DSV4_TYPE_FP16 or DSV4_TYPE_FP32, of x and out; the arithmetic is
  *             fp32, rounded once.

@@ -887,8 +887,10 @@ def rope_rows(x, positions, cos_sin_cache, out=None, offset: int | None = None, 
     """dsv4_rope_rows: dims [offset, offset + d) of x ([T, H, D] or [T, D]; bf16, fp16 or fp32; the
     outer dims may be strided) turned by the angles of each token's position into out (None: x
     itself), d being the width of cos_sin_cache (fp32 [max_position, d]) and offset D - d (the
-    trailing dims) unless given.  inverse: turned back, which is also the gradient's way.  layout:
-    ROPE_PAIRS (neighbouring dims) or ROPE_HALF (i and i + d / 2)."""
+    trailing dims) unless given.  inverse: the transpose, which is the gradient's way and, with a
+    table of magnitude 1, turns back; what a table of magnitude m turned (rows, and an attention's output
+    over such rows) is turned back with one of magnitude 1 / m.  layout: ROPE_PAIRS (neighbouring
+    dims) or ROPE_HALF (i and i + d / 2)."""
     types = _row_types or _find_row_types()
     if out is None:
         out = x

@@ -1,6 +1,6 @@
 // Rotation of rows by a table of cosines and sines: (a, b) -> (a cos - b sin, b cos + a sin) for
-// the pairs of a row's rotated dims, or with -sin, which is the inverse and the gradient; in fp32
-// with one rounding to the row's type.  In place only the rotated dims are touched; out of place
+// the pairs of a row's rotated dims, or with -sin, which is the gradient and, by a table of magnitude 1,
+// the inverse; in fp32 with one rounding to the row's type.  In place only the rotated dims are touched; out of place
 // the others are copied.
 //
 // Bound by memory.  A thread has one column (a vector of 16 bytes; two of them in the half
