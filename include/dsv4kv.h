@@ -546,8 +546,8 @@ int dsv4_fp4_evict(uint8_t *kv_cache, int64_t num_blocks, int32_t block_size,
  *               that may run at the same time need two.
  *
  * Scores and sums are fp32; the probabilities are rounded to bf16 for the product with the
- * rows.  A score outside fp32's range makes its row NaN, but one below it over the FP8 cache may take
- * no part instead.  FP8 rows are taken as they are stored while their values are from 2^-78 to
+ * rows.  A score that, times log2 e, lies outside fp32's range makes its row NaN, but one below it over
+ * the FP8 cache may take no part instead.  FP8 rows are taken as they are stored while their values are from 2^-78 to
  * 2^63 in magnitude, or 0; a smaller one may be taken as any other that small, 0 among them.  A
  * row that holds a value that is not finite (or, in the FP8 cache, a block with an exponent byte
  * above 182) gives NaN (all dims and lse) to the tokens that see it and nothing to the others.  A

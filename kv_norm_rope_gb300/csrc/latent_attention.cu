@@ -931,24 +931,25 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
         const auto load_scores = [&](float ref0, float ref1) {
             tmem_load16_rows16(tmem + kScoresAt + (t & 1) * kTileKeys + key0, v);
             tmem_wait_load();
+            if constexpr (!kFp8) {
+                // an infinite score is one of a row that is not finite, or outside fp32 (looked for here: a
+                // score's distance from the reference may be infinite where both are finite)
+                float least = v[0];
+#pragma unroll
+                for (int j = 1; j < 16; ++j)
+                    least = fminf(least, v[j]);
+                if (least * scale == -INFINITY) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = v[j] * scale == -INFINITY ? __int_as_float(0x7FFFFFFF) : v[j];
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
                 v[j] = __fmaf_rn(v[j], scale, -ref0);
                 v[j + 1] = __fmaf_rn(v[j + 1], scale, -ref0);
                 v[j + 2] = __fmaf_rn(v[j + 2], scale, -ref1);
                 v[j + 3] = __fmaf_rn(v[j + 3], scale, -ref1);
-            }
-            if constexpr (!kFp8) {
-                // an infinite score is one of a row that is not finite, or of a sum outside fp32
-                float least = v[0];
-#pragma unroll
-                for (int j = 1; j < 16; ++j)
-                    least = fminf(least, v[j]);
-                if (least == -INFINITY) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[j] = v[j] == -INFINITY ? __int_as_float(0x7FFFFFFF) : v[j];
-                }
             }
             if (__any_sync(kFull, (missing | marked) != 0u) || !whole) {
 #pragma unroll

@@ -4,7 +4,7 @@ do to the tokens that see it.  Bounds as in test_latent_gpu.
 import numpy as np
 import pytest
 
-from tests.test_latent_gpu import Batch, random_tree, torch
+from tests.test_latent_gpu import STORES, Batch, bf16, bf16_bytes, random_tree, torch
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +25,27 @@ def test_fp8_padding_byte_means_nothing(block, narrow, tree):
     s.refresh()
     out, lse = s.attention()
     assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("store", STORES)
+@pytest.mark.parametrize("order", ["low first", "high first", "mixed"])
+@pytest.mark.parametrize("n", [50, 300, 5000])
+def test_finite_scores_further_apart_than_fp32_reaches(store, order, n):
+    """Scores of 2^127 and -2^127 (1.44 times that in powers of two): the low ones have a probability of 0."""
+    s = Batch(store, [n], 2, 5, 16, seed=41)
+    high = {"low first": np.arange(n) >= n // 2, "high first": np.arange(n) < n // 2,
+            "mixed": np.arange(n) % 3 == 0}[order]
+    high[-1] = False  # (the token before the last sees as many)
+    for i in range(n):
+        s.row(0, i)[0][-128:-126] = bf16_bytes([1.0 if high[i] else -1.0])
+    s.refresh()
+    q = np.zeros_like(s.q64)
+    q[..., 448] = 2.0 ** 127
+    s.q, s.q64 = bf16(q)
+    s.scale = 1.0
+    out, lse = s.attention()
+    rows = s.rows[0][high]
+    want, size = rows.mean(0), np.abs(rows).mean(0)
+    # every p that is not 0 is 1: half a step of the output, and the roundings of fp32 sums
+    assert np.all(np.abs(out[0].double().cpu().numpy() - want) <= np.abs(want) * 2.0 ** -8 + size * 2.0 ** -8)
+    assert np.allclose(lse[0].double().cpu().numpy(), s.q64[0, 0, 0, 448], rtol=2.0 ** -20, atol=0)
