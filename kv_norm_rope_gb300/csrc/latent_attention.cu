@@ -90,6 +90,7 @@ constexpr uint32_t kQueryBytes = kChunks * kRows * 128;
 constexpr uint32_t kProbBytes = kRows * 128;  // 64 rows of 64 keys
 constexpr int kSoftmaxWarps = 8, kRowWarp = kSoftmaxWarps;  // warps from kRowWarp on see to the rows
 constexpr float kSlack = 16.0f;
+constexpr float kLargeScore = 16777216.0f;  // half a step there is 1
 static_assert(kRows == 64 && kTileKeys == 64, "the lanes are dealt for these");
 
 // What differs with the store.
@@ -904,6 +905,10 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
     RowView lo{0, 0, 0u}, hi{0, 0, 0u};
     int whole_to = 0, whole_from = 0;  // keys that all of the warp's rows see
     float m0 = 0.0f, m1 = 0.0f, sum0 = 0.0f, sum1 = 0.0f;
+    // A reference is a rounded product.  Its error is a factor that all keys of the row have in common, but
+    // one outside any range for scores this large: there the scores are rounded alike.  (Looked up where
+    // references move: FP8 as before, wide trees 598.5 to 601 us.  Looked up at each tile 292 to 294 and 604.)
+    bool large = false;
     bool first = true, valid_lo = true, valid_hi = true;  // of rows r and r + 8: of the unit
     int segment = 0, from_tile = 0;
     for (uint32_t t = 0; c.left > 0; ++t) {
@@ -916,6 +921,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
             whole_to = __reduce_min_sync(kFull, min(lo.to, hi.to));
             whole_from = __reduce_max_sync(kFull, max(lo.from, hi.from));
             m0 = m1 = kUnset;
+            large = false;
             sum0 = sum1 = 0.0f;
         }
         const bool last = c.ends_segment();
@@ -928,9 +934,16 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
         const uint32_t marked = __ballot_sync(kFull, state == kNotFinite) >> pair;
         float v[16];
         // v = the scores less a reference, -infinity where unseen
-        const auto load_scores = [&](float ref0, float ref1) {
+        const auto load_scores = [&](float ref0, float ref1, bool alike) {
             tmem_load16_rows16(tmem + kScoresAt + (t & 1) * kTileKeys + key0, v);
             tmem_wait_load();
+            float by = scale;
+            if (alike) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] *= scale;
+                by = 1.0f;
+            }
             if constexpr (!kFp8) {
                 // an infinite score is one of a row that is not finite, or outside fp32 (looked for here: a
                 // score's distance from the reference may be infinite where both are finite)
@@ -938,18 +951,18 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
 #pragma unroll
                 for (int j = 1; j < 16; ++j)
                     least = fminf(least, v[j]);
-                if (least * scale == -INFINITY) {
+                if (least * by == -INFINITY) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        v[j] = v[j] * scale == -INFINITY ? __int_as_float(0x7FFFFFFF) : v[j];
+                        v[j] = v[j] * by == -INFINITY ? __int_as_float(0x7FFFFFFF) : v[j];
                 }
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
-                v[j] = __fmaf_rn(v[j], scale, -ref0);
-                v[j + 1] = __fmaf_rn(v[j + 1], scale, -ref0);
-                v[j + 2] = __fmaf_rn(v[j + 2], scale, -ref1);
-                v[j + 3] = __fmaf_rn(v[j + 3], scale, -ref1);
+                v[j] = __fmaf_rn(v[j], by, -ref0);
+                v[j + 1] = __fmaf_rn(v[j + 1], by, -ref0);
+                v[j + 2] = __fmaf_rn(v[j + 2], by, -ref1);
+                v[j + 3] = __fmaf_rn(v[j + 3], by, -ref1);
             }
             if (__any_sync(kFull, (missing | marked) != 0u) || !whole) {
 #pragma unroll
@@ -964,7 +977,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
             }
         };
         __syncwarp();
-        load_scores(m0, m1);
+        load_scores(m0, m1, large);
         // (rows past the unit's last move nothing)
         float over = -INFINITY;
 #pragma unroll
@@ -980,7 +993,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
             }
             tmem_fence_after();
             // move the references up to this tile's scores and rescale what was taken before
-            load_scores(0.0f, 0.0f);
+            load_scores(0.0f, 0.0f, false);
             float top0 = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[4], v[5])), fmaxf(fmaxf(v[8], v[9]), fmaxf(v[12], v[13])));
             float top1 = fmaxf(fmaxf(fmaxf(v[2], v[3]), fmaxf(v[6], v[7])), fmaxf(fmaxf(v[10], v[11]), fmaxf(v[14], v[15])));
 #pragma unroll
@@ -999,6 +1012,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
             const float factor0 = exp2_approx(m0 - new0), factor1 = exp2_approx(m1 - new1);
             m0 = new0;
             m1 = new1;
+            large = fmaxf(fabsf(m0), fabsf(m1)) > kLargeScore;
             sum0 *= factor0;
             sum1 *= factor1;
             if (!first) {
@@ -1020,7 +1034,7 @@ __device__ void softmax_role(const WParams &w, Shared &s, uint32_t smem, const C
                 }
                 tmem_wait_store();
             }
-            load_scores(m0, m1);
+            load_scores(m0, m1, large);
         }
         uint32_t packed[8];
 #pragma unroll

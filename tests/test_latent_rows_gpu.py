@@ -30,8 +30,9 @@ def test_fp8_padding_byte_means_nothing(block, narrow, tree):
 @pytest.mark.parametrize("store", STORES)
 @pytest.mark.parametrize("order", ["low first", "high first", "mixed"])
 @pytest.mark.parametrize("n", [50, 300, 5000])
-def test_finite_scores_further_apart_than_fp32_reaches(store, order, n):
-    """Scores of 2^127 and -2^127 (1.44 times that in powers of two): the low ones have a probability of 0."""
+@pytest.mark.parametrize("score", [2.0 ** 127, 2e38, 3e30, 1.7e12, 1.1e9, 5e8, 3e7, 7e6])
+def test_large_scores_of_either_sign(store, order, n, score):
+    """Finite scores, the largest further apart than fp32 reaches: the low ones have a probability of 0."""
     s = Batch(store, [n], 2, 5, 16, seed=41)
     high = {"low first": np.arange(n) >= n // 2, "high first": np.arange(n) < n // 2,
             "mixed": np.arange(n) % 3 == 0}[order]
@@ -40,7 +41,7 @@ def test_finite_scores_further_apart_than_fp32_reaches(store, order, n):
         s.row(0, i)[0][-128:-126] = bf16_bytes([1.0 if high[i] else -1.0])
     s.refresh()
     q = np.zeros_like(s.q64)
-    q[..., 448] = 2.0 ** 127
+    q[..., 448] = score
     s.q, s.q64 = bf16(q)
     s.scale = 1.0
     out, lse = s.attention()
@@ -48,4 +49,4 @@ def test_finite_scores_further_apart_than_fp32_reaches(store, order, n):
     want, size = rows.mean(0), np.abs(rows).mean(0)
     # every p that is not 0 is 1: half a step of the output, and the roundings of fp32 sums
     assert np.all(np.abs(out[0].double().cpu().numpy() - want) <= np.abs(want) * 2.0 ** -8 + size * 2.0 ** -8)
-    assert np.allclose(lse[0].double().cpu().numpy(), s.q64[0, 0, 0, 448], rtol=2.0 ** -20, atol=0)
+    assert np.allclose(lse[0].double().cpu().numpy(), s.q64[0, 0, 0, 448] + np.log(high.sum()), rtol=2.0 ** -20, atol=0)
