@@ -4,7 +4,7 @@ do to the tokens that see it.  Bounds as in test_latent_gpu.
 import numpy as np
 import pytest
 
-from tests.test_latent_gpu import STORES, Batch, bf16, bf16_bytes, random_tree, torch
+from tests.test_latent_gpu import BAD, STORES, Batch, bf16, bf16_bytes, dev, random_tree, spoil, torch
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,39 @@ def test_large_scores_of_either_sign(store, order, n, score):
     # every p that is not 0 is 1: half a step of the output, and the roundings of fp32 sums
     assert np.all(np.abs(out[0].double().cpu().numpy() - want) <= np.abs(want) * 2.0 ** -8 + size * 2.0 ** -8)
     assert np.allclose(lse[0].double().cpu().numpy(), s.q64[0, 0, 0, 448] + np.log(high.sum()), rtol=2.0 ** -20, atol=0)
+
+
+WHOLE = [("fp8", kind) for kind in BAD["fp8"]] + [("bf16", kind) for kind in BAD["bf16"]]
+
+
+@pytest.mark.parametrize("store,kind", WHOLE)
+@pytest.mark.parametrize("n,Q,H,window", [(300, 1, 4, 0), (300, 3, 40, 0), (3000, 2, 24, 0), (500, 3, 64, 400)])
+def test_rows_not_finite_that_every_token_sees(store, kind, n, Q, H, window):
+    """A row that is not finite in a tile that all tokens see whole: NaN for all of them (all dims and
+    lse), whatever its scores' signs, and nothing for the other requests."""
+    s = Batch(store, [n, 77, n], Q, H, 16, seed=42)
+    spoil(s, 0, n - 200 if window else 10, kind)
+    s.cache = dev(s.cache_np)
+    for sinks in (None, torch.linspace(-3, 3, H, device=s.q.device)):
+        out, lse = s.attention(window=window, sinks=sinks)
+        assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+        s.check(out, lse, window, sinks, skip={(0, j) for j in range(Q)})
+
+
+@pytest.mark.parametrize("store,kind", WHOLE)
+@pytest.mark.parametrize("n", [200, 4000])
+def test_padding_beside_context_rows_not_finite(store, kind, n):
+    """In a tree, tokens that are padding give zeros although their row tile holds products of 0 and
+    rows that are not finite; the others give NaN."""
+    Q, H = 8, 9
+    tree = [1, 0b11, 0, 0b1011, 0, 0, 0, 0]
+    s = Batch(store, [n, n], Q, H, 16, seed=43, trees=[tree, [0] * Q])
+    for b in (0, 1):
+        spoil(s, b, 70, kind)
+    s.cache = dev(s.cache_np)
+    seeing, padding = [0, 1, 3], [2, 4, 5, 6, 7]
+    for sinks in (None, torch.linspace(-3, 3, H, device=s.q.device)):
+        out, lse = s.attention(sinks=sinks)
+        assert torch.isnan(out[0, seeing]).all() and torch.isnan(lse[0, seeing]).all()
+        assert bool((out[0, padding] == 0).all()) and bool((out[1] == 0).all())
+        s.check(out, lse, 0, sinks, skip={(0, j) for j in seeing})
