@@ -652,7 +652,8 @@ int dsv4_rope_table(const double *frequencies, int32_t rope_dim, double magnitud
  *  positions  (device) int64 [num_tokens], 8-byte aligned.  One outside [0, max_position) sets
  *             DSV4_DEVERR_POS_RANGE and its token's rows are not written.
  *  cos_sin    (device) fp32 [max_position, rope_dim]: columns 0.. cos, rope_dim / 2.. sin.  16-byte aligned.
- * rope_dim even, 2 to 256; width <= 65536; num_tokens * num_heads < 2^31; num_tokens >= 0 (0: no launch).
+ * rope_dim even, 2 to 256; width <= 65536; num_tokens * num_heads < 2^31, and the bytes from the first
+ * to behind the last row of x or out below 2^63; num_tokens >= 0 (0: no launch).
  */
 enum { DSV4_TYPE_BF16 = 0, DSV4_TYPE_FP16 = 1, DSV4_TYPE_FP32 = 2 };
 enum { DSV4_ROPE_PAIRS = 0, DSV4_ROPE_HALF = 1 };

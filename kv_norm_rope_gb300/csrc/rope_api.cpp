@@ -41,6 +41,13 @@ bool bad_rope_dim(int32_t rope_dim)
     return rope_dim < 2 || rope_dim > dsv4::kMaxRopeDim || rope_dim % 2 != 0;
 }
 
+// elements from the first of the rows to behind the last; strides to 2^31, tokens and heads below 2^31:
+// at most 2^63
+uint64_t extent(int64_t tokens, int64_t heads, int64_t width, int64_t token_stride, int64_t head_stride)
+{
+    return uint64_t(tokens - 1) * uint64_t(token_stride) + uint64_t(heads - 1) * uint64_t(head_stride) + width;
+}
+
 // strides that keep the rows of an output apart, whichever of tokens and heads lies inside
 bool rows_apart(int64_t tokens, int64_t heads, int64_t width, int64_t token_stride, int64_t head_stride)
 {
@@ -147,20 +154,24 @@ int dsv4_rope_rows(int type, const void *x, int64_t x_token_stride, int64_t x_he
     if (num_tokens > INT32_MAX / num_heads)  // rows are counted in 32 bits
         return DSV4_ERR_SHAPE;
     for (const int64_t s : {x_token_stride, x_head_stride, out_token_stride, out_head_stride})
-        if (s < 0 || s > (int64_t(1) << 31))  // times rows and a size: below 2^63
+        if (s < 0 || s > (int64_t(1) << 31))
             return DSV4_ERR_SHAPE;
     if (type < DSV4_TYPE_BF16 || type > DSV4_TYPE_FP32 || (layout != DSV4_ROPE_PAIRS && layout != DSV4_ROPE_HALF) ||
         (inverse != 0 && inverse != 1))
         return DSV4_ERR_VALUE;
     if (num_tokens == 0)
         return DSV4_OK;
+    // bytes are counted in 64 bits
+    const int64_t size = type == DSV4_TYPE_FP32 ? 4 : 2;
+    if (extent(num_tokens, num_heads, width, x_token_stride, x_head_stride) > INT64_MAX / size ||
+        extent(num_tokens, num_heads, width, out_token_stride, out_head_stride) > INT64_MAX / size)
+        return DSV4_ERR_SHAPE;
     if (!rows_apart(num_tokens, num_heads, width, out_token_stride, out_head_stride))
         return DSV4_ERR_SHAPE;
     if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
         return DSV4_ERR_SHAPE;
     if (!x || !out || !positions || !cos_sin)
         return DSV4_ERR_NULL;
-    const uintptr_t size = type == DSV4_TYPE_FP32 ? 4 : 2;
     if (!aligned(x, size) || !aligned(out, size) || !aligned(positions, 8) || !aligned(cos_sin, 16) ||
         !aligned(device_error, 4))
         return DSV4_ERR_ALIGN;
