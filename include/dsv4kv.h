@@ -646,7 +646,9 @@ int dsv4_rope_table(const double *frequencies, int32_t rope_dim, double magnitud
  *  x, out     (device) [num_tokens, num_heads, width] with strides in elements (0 to 2^31), the
  *             innermost 1; aligned to their element.  out is x itself, with the same strides: only
  *             the rotated dims are read and written; or apart from it: the other dims are copied.  The
- *             rows of out do not overlap; those of x may (stride 0).
+ *             rows of out do not overlap; those of x may (stride 0).  DSV4_ERR_SHAPE where rows of out
+ *             overlap, or with the strides of x overlap those of x at another place; that rows of other
+ *             strides do not, the caller sees to.
  *  layout     DSV4_ROPE_PAIRS: pair i is dims (offset + 2i, offset + 2i + 1);
  *             DSV4_ROPE_HALF: dims (offset + i, offset + rope_dim / 2 + i).
  *  positions  (device) int64 [num_tokens], 8-byte aligned.  One outside [0, max_position) sets

@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "dsv4kv.h"
 #include "hostcheck.h"
@@ -56,6 +57,31 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t width, int64_t token_stri
     const bool tokens_inside = (tokens == 1 || token_stride >= width) &&
                                (heads == 1 || head_stride >= (tokens - 1) * token_stride + width);
     return heads_inside || tokens_inside;
+}
+
+// For rows that lie apart: whether some of them, moved by `by` > 0 bytes, meet others or themselves.
+// Strides and width in bytes.
+bool moved_rows_meet(uint64_t by, int64_t tokens, int64_t heads, int64_t width, int64_t token_stride,
+                     int64_t head_stride)
+{
+    int64_t outer = tokens, inner = heads, outer_stride = token_stride, inner_stride = head_stride;
+    const bool heads_inside = (heads == 1 || head_stride >= width) &&
+                              (tokens == 1 || token_stride >= (heads - 1) * head_stride + width);
+    if (!heads_inside) {
+        std::swap(outer, inner);
+        std::swap(outer_stride, inner_stride);
+    }
+    // a multiple of each stride, less by `by`, that is below the width
+    const auto meets = [&](int64_t rest) {  // of the inner stride
+        rest = rest < 0 ? -rest : rest;
+        const int64_t j = inner == 1 ? 0 : std::min(rest / inner_stride, inner - 1);
+        return rest - j * inner_stride < width || (j + 1 < inner && (j + 1) * inner_stride - rest < width);
+    };
+    if (by > uint64_t(INT64_MAX))
+        return false;
+    const int64_t i = outer == 1 ? 0 : std::min(int64_t(by) / outer_stride, outer - 1);
+    return meets(int64_t(by) - i * outer_stride) ||
+           (i + 1 < outer && meets(int64_t(by) - (i + 1) * outer_stride));
 }
 
 }  // namespace
@@ -175,6 +201,12 @@ int dsv4_rope_rows(int type, const void *x, int64_t x_token_stride, int64_t x_he
     if (!aligned(x, size) || !aligned(out, size) || !aligned(positions, 8) || !aligned(cos_sin, 16) ||
         !aligned(device_error, 4))
         return DSV4_ERR_ALIGN;
+    const uint64_t x_at = reinterpret_cast<uintptr_t>(x), out_at = reinterpret_cast<uintptr_t>(out);
+    if (x != out && (num_tokens == 1 || x_token_stride == out_token_stride) &&
+        (num_heads == 1 || x_head_stride == out_head_stride) &&
+        moved_rows_meet(x_at < out_at ? out_at - x_at : x_at - out_at, num_tokens, num_heads, width * size,
+                        out_token_stride * size, out_head_stride * size))
+        return DSV4_ERR_SHAPE;
     dsv4::RopeRowsArgs a = {};
     a.x = static_cast<const uint8_t *>(x);
     a.out = static_cast<uint8_t *>(out);
