@@ -805,6 +805,8 @@ def latent_attention(store_mode: int, q, kv_cache, num_blocks: int, block_size: 
             workspace_bytes = workspace.numel() * workspace.element_size()
         workspace_at = _address("workspace", workspace, "bytes", None, where)
     _placed("block_table", block_table, where)
+    if out_at is not None and abs(q_at - out_at) < 1024 * rows:
+        raise ValueError("out overlaps q")
     _launch("dsv4_latent_attention", where, stream, lib().dsv4_latent_attention, store_mode, q_at, cache_at,
             num_blocks, block_size, block_table.data_ptr(), stride, width, lens_at, B, Q, H, scale, _int32(window),
             tree_at, sinks_at, out_at, lse_at, workspace_at, workspace_bytes, error_at)
