@@ -807,9 +807,10 @@ def latent_attention(store_mode: int, q, kv_cache, num_blocks: int, block_size: 
     _placed("block_table", block_table, where)
     if out_at is not None and abs(q_at - out_at) < 1024 * rows:
         raise ValueError("out overlaps q")
-    _launch("dsv4_latent_attention", where, stream, lib().dsv4_latent_attention, store_mode, q_at, cache_at,
-            num_blocks, block_size, block_table.data_ptr(), stride, width, lens_at, B, Q, H, scale, _int32(window),
-            tree_at, sinks_at, out_at, lse_at, workspace_at, workspace_bytes, error_at)
+    _launch("dsv4_latent_attention", where, stream, lib().dsv4_latent_attention,
+            store_mode if store_mode in _SLOT_BYTES else -1, q_at, cache_at, num_blocks,
+            block_size if 0 < block_size < 2 ** 31 else -1, block_table.data_ptr(), stride, width, lens_at, B, Q, H,
+            scale, _int32(window), tree_at, sinks_at, out_at, lse_at, workspace_at, workspace_bytes, error_at)
 
 
 def tree_keep(store_mode: int, kv_cache, num_blocks: int, block_size: int, block_table, seq_lens, path,
@@ -830,8 +831,9 @@ def tree_keep(store_mode: int, kv_cache, num_blocks: int, block_size: int, block
     new_at = _address("new_seq_lens", new_seq_lens, "i32", B, where)
     error_at = _address("device_error", device_error, "i32", None, where)
     _placed("block_table", block_table, where)
-    _launch("dsv4_tree_keep", where, stream, lib().dsv4_tree_keep, store_mode, cache_at, num_blocks, block_size,
-            block_table.data_ptr(), stride, width, lens_at, B, Q, path_at, path_lens_at, new_at, error_at)
+    _launch("dsv4_tree_keep", where, stream, lib().dsv4_tree_keep, store_mode if store_mode in _SLOT_BYTES else -1,
+            cache_at, num_blocks, block_size if 0 < block_size < 2 ** 31 else -1, block_table.data_ptr(), stride, width,
+            lens_at, B, Q, path_at, path_lens_at, new_at, error_at)
 
 
 # ---- rotary positions
@@ -843,7 +845,7 @@ def rope_frequencies(rope_dim: int, theta: float = 10000.0, scaling: int = ROPE_
     """dsv4_rope_frequencies: the rope_dim / 2 angles per position (floats, on the host), plain or
     stretched for long contexts (ROPE_LINEAR, ROPE_NTK, ROPE_YARN)."""
     out = (ctypes.c_double * (max(2, min(rope_dim, 256)) // 2))()
-    st = lib().dsv4_rope_frequencies(scaling, _int32(rope_dim), theta, factor, original_positions, turns_fast,
+    st = lib().dsv4_rope_frequencies(_int32(scaling), _int32(rope_dim), theta, factor, original_positions, turns_fast,
                                      turns_slow, out)
     if st != OK:
         raise Dsv4Error(st, "dsv4_rope_frequencies")
@@ -864,7 +866,7 @@ def rope_table(frequencies, out, positions=None, first: int = 0, magnitude: floa
     error_at = _address("device_error", device_error, "i32", None, where)
     angles = (ctypes.c_double * pairs)(*frequencies)
     _launch("dsv4_rope_table", where, stream, lib().dsv4_rope_table, angles, 2 * pairs, magnitude, positions_at,
-            first, out.shape[0], out_at, error_at)
+            first if 0 <= first < 2 ** 62 else -1, out.shape[0], out_at, error_at)
 
 
 def _row_strides(name: str, t):
@@ -915,5 +917,5 @@ def rope_rows(x, positions, cos_sin_cache, out=None, offset: int | None = None, 
     offset = D - dim if offset is None else offset
     x_strides, out_strides = _row_strides("x", x), _row_strides("out", out)
     _launch("dsv4_rope_rows", where, stream, lib().dsv4_rope_rows, types[x.dtype], x.data_ptr(), *x_strides,
-            out.data_ptr(), *out_strides, T, H, D, _int32(offset), dim, layout, 1 if inverse else 0, positions_at,
+            out.data_ptr(), *out_strides, T, H, D, _int32(offset), dim, layout if layout in (ROPE_PAIRS, ROPE_HALF) else -1, 1 if inverse else 0, positions_at,
             table_at, max_position, error_at)
