@@ -321,7 +321,7 @@ __device__ __forceinline__ void copy_fp8_16(const AParams &p, uint32_t to, const
 
 // A lane has keys `lane` and `lane + 32` of a tile: their addresses and exponents, kPlaceSlots tiles
 // ahead of the converting warps at most, found two tiles and loaded one tile ahead of that.
-__device__ __forceinline__ void place_role(const AParams &p, Shared &s, KindShared<true> &ks, Cursor c)
+__device__ __forceinline__ void place_role(const AParams &p, KindShared<true> &ks, Cursor c)
 {
     const int lane = threadIdx.x & 31, count = c.left;
     struct Two {
@@ -1197,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) latent_attention_kernel(con
         else if (warp == kMultiplyWarp<kFp8> + 2)
             query_role(l, s, smem, c);
         else if constexpr (kFp8)
-            place_role(p, s, ks, c);
+            place_role(p, ks, c);
     } else if (c.left == 0) {
         // more CTAs than tiles
     } else if (warp < kSoftmaxWarps) {
