@@ -441,7 +441,8 @@ int dsv4_fp4_dequant_gather(const uint8_t *kv_cache, int64_t num_blocks, int32_t
  *               that may run at the same time need two.
  *
  * Scores and sums are fp32; the probabilities are rounded to bf16 for the product with
- * the rows.  A score below fp32's range is -infinity: its key takes no part.  Rows are taken
+ * the rows.  A score below fp32's range is -infinity: its key takes no part.  A token with a score of
+ * 2^30 or more in magnitude may give zeros or NaN instead of its softmax.  Rows are taken
  * as they are stored while their values are from 2^-46 to 2^83 in magnitude, or 0; a
  * smaller one may be taken as any other that small, 0 among them.  A row that holds a value
  * that is not finite, or a group with e_g > 208, gives NaN (all dims and lse) to the tokens

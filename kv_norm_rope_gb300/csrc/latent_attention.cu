@@ -27,16 +27,18 @@
 //    range, so a p of 2^kSlack loses nothing).  Sums stay per thread, in fp32, until the segment ends.
 //
 // What it takes (with the results joined), and what bounds it:
-//  * 128 requests of 1024 to 8192 FP8 keys, 128 heads: 251 us, 577 TFLOP/s; 32 requests of up to 4096,
-//    16 drafted tokens of 64 heads: 290 us.  About 3900 cycles a tile.  Counters give the data pipe of
+//  * 128 requests of 1024 to 8192 FP8 keys, 128 heads: 253 us, 573 TFLOP/s; 32 requests of up to 4096,
+//    16 drafted tokens of 64 heads: 291 us.  About 3900 cycles a tile.  Counters give the data pipe of
 //    shared memory 91% busy (42% the products' operands, 49% loads and stores) and 60% of all issue
 //    slots: each row tile converts its keys for itself.
-//  * 6 requests of up to 4096 bf16 keys in a window, 61 drafted tokens of 128 heads: 594 us, 549 TFLOP/s;
-//    one of 262147 keys, 128 heads: 106 us.  About 3000 cycles a tile: a tile's copy, product, softmax
+//  * 6 requests of up to 4096 bf16 keys in a window, 61 drafted tokens of 128 heads: 598 us, 545 TFLOP/s;
+//    one of 262147 keys, 128 heads: 107 us.  About 3000 cycles a tile: a tile's copy, product, softmax
 //    and product follow one another, with two tiles to fill the gaps.
-//  * 48 requests of up to 4096 FP8 keys, 64 heads: 37.4 us in a graph, two requests of 130 keys: 12.5 us.
+//  * 48 requests of up to 4096 FP8 keys, 64 heads: 37.9 us in a graph, two requests of 130 keys: 12.3 us.
 //    A run's first product comes after 9000 to 14000 cycles (the deal, the lengths, tables, rows and
 //    queries, one load behind the other), a whole row tile's results take 7500, a part's 4200.
+//
+// (Not built: products that two SMs issue together, cta_group::2, with a row tile each.)
 //
 // Slower, each beside the best of its time (us, the first case unless another is named):
 //  * 8 converting warps of 8 keys, all rows in registers: 311 to 252; 16 warps so: 259;

@@ -100,8 +100,9 @@ struct Fp4EvictArgs {
 
 // Keys in a tile of the attention over the FP8 and bf16 caches, and the positions that
 // beginning a row tile takes on its line: with 0, 2, 3, 4, 6 and 8 of them 48 requests of up to 4096
-// FP8 keys took 47, 41, 41, 40, 41 and 42 us, 128 of up to 8192 275, 265, 264, 264, 267 and 269, and 32 with
-// 16 drafted tokens 352, 311, 304, 308, 314 and 317.
+// FP8 keys take (in a graph) 45.8, 38.4, 38.7, 37.9, 38.9 and 39.4 us, 128 of up to 8192 266, 253, 251, 253,
+// 255 and 256, 32 with 16 drafted tokens 339, 293, 289, 290, 297 and 302, and wide trees over bf16 rows
+// 590, 596, 597, 598, 600 and 603.
 constexpr int kLatentTileKeys = 64;
 constexpr int kLatentStartCost = 4;
 
